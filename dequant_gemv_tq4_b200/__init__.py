@@ -10,12 +10,14 @@ Two layers:
   * ``tq_*`` functions with the C names and raw integer pointers (what the
     ABI tests call);
   * tensor helpers (``quantize``, ``dequantize``, ``prerotate``, ``gemm``,
-    ``gemv``, ``gemm_xrot``) that allocate outputs with torch and pass
-    ``data_ptr()`` and the current CUDA stream.
+    ``gemv``, ``gemm_xrot``; ``rope``, ``kv_append``, ``kv_read``,
+    ``kv_attention``, ``kv_commit`` for the key/value cache) that allocate
+    outputs with torch and pass ``data_ptr()`` and the current CUDA stream.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -58,6 +60,20 @@ _lock = threading.Lock()
 _lib = None
 
 
+class KvCache(ctypes.Structure):
+    """Mirror of ``tq_kv_cache`` in include/tq.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("batch", ctypes.c_int64), ("pages_per_seq", ctypes.c_int64),
+                ("page_table_ld", ctypes.c_int64), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
+
+
+class RopeDesc(ctypes.Structure):
+    """Mirror of ``tq_rope_desc`` in include/tq.h."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class TQError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -98,6 +114,16 @@ def load_library() -> ctypes.CDLL:
             "tq_prefill_xrot_bytes": ([I64, I64], SZ),
             "tq_prerotate_plain": ([P, I, I64, I64, I64, P, P], I),
             "tq_gemm_prefill_xrot": ([P, P, I64, I64, P, I64, P, I, I64, P, SZ, P], I),
+            "tq_rope": ([P, P, I, I64, I64, I64, I64, I64, I64, I64, P, ctypes.POINTER(RopeDesc), P], I),
+            "tq_kv_codes_bytes": ([I64, I64, I64, I64], SZ),
+            "tq_kv_scales_bytes": ([I64, I64, I64, I64], SZ),
+            "tq_kv_append": ([ctypes.POINTER(KvCache), P, P, I64, P, I64, I64, P, I64, I64, I, P,
+                              ctypes.POINTER(RopeDesc), P], I),
+            "tq_kv_read": ([ctypes.POINTER(KvCache), P, P, I64, P, I64, I64, P, I64, I64, I, P], I),
+            "tq_kv_attention_workspace_bytes": ([I64, I64, I64, I64, I64], SZ),
+            "tq_kv_attention": ([ctypes.POINTER(KvCache), P, P, I64, P, I, I64, I64, I64, P, I, I64, I64, I64, I64,
+                                 I64, ctypes.c_float, P, SZ, P], I),
+            "tq_kv_commit": ([ctypes.POINTER(KvCache), I64, I64, I64, P, P, I64, I64, P], I),
             "tq_nvfp4_scales_bytes": ([I64, I64], SZ),
             "tq_nvfp4_quantize": ([P, I, I64, I64, I64, P, P, P, P], I),
             "tq_nvfp4_dequantize": ([P, P, P, I64, I64, P, I, I64, P], I),
@@ -241,6 +267,49 @@ def tq_nvfp4_gemm_batch_workspace_bytes(descs, count, m) -> int:
 
 def tq_nvfp4_gemm_batch(descs, count, m, xt, yt, workspace, ws_bytes, stream) -> int:
     return load_library().tq_nvfp4_gemm_batch(descs, count, m, xt, yt, workspace, ws_bytes, stream)
+
+
+def tq_rope(x, out, t, tokens, heads, dim, x_token_stride, x_head_stride, out_token_stride, out_head_stride,
+            positions, rope, stream) -> int:
+    return load_library().tq_rope(x, out, t, tokens, heads, dim, x_token_stride, x_head_stride, out_token_stride,
+                                  out_head_stride, positions, rope, stream)
+
+
+def tq_kv_codes_bytes(pages: int, kv_heads: int, head_dim: int, page_size: int) -> int:
+    return int(load_library().tq_kv_codes_bytes(pages, kv_heads, head_dim, page_size))
+
+
+def tq_kv_scales_bytes(pages: int, kv_heads: int, head_dim: int, page_size: int) -> int:
+    return int(load_library().tq_kv_scales_bytes(pages, kv_heads, head_dim, page_size))
+
+
+def tq_kv_append(cache, seqs, places, tokens, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, t,
+                 positions, rope, stream) -> int:
+    return load_library().tq_kv_append(cache, seqs, places, tokens, k, k_token_stride, k_head_stride, v,
+                                       v_token_stride, v_head_stride, t, positions, rope, stream)
+
+
+def tq_kv_read(cache, seqs, places, tokens, k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, t,
+               stream) -> int:
+    return load_library().tq_kv_read(cache, seqs, places, tokens, k, k_token_stride, k_head_stride, v,
+                                     v_token_stride, v_head_stride, t, stream)
+
+
+def tq_kv_attention_workspace_bytes(batch: int, tree: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(load_library().tq_kv_attention_workspace_bytes(batch, tree, heads, kv_heads, head_dim))
+
+
+def tq_kv_attention(cache, lens, parents, parents_ld, q, qt, q_batch_stride, q_token_stride, q_head_stride, out, ot,
+                    out_batch_stride, out_token_stride, out_head_stride, tree, heads, scale, workspace, ws_bytes,
+                    stream) -> int:
+    return load_library().tq_kv_attention(cache, lens, parents, parents_ld, q, qt, q_batch_stride, q_token_stride,
+                                          q_head_stride, out, ot, out_batch_stride, out_token_stride,
+                                          out_head_stride, tree, heads, scale, workspace, ws_bytes, stream)
+
+
+def tq_kv_commit(cache, layers, code_layer_stride, scale_layer_stride, lens, path, path_ld, steps, stream) -> int:
+    return load_library().tq_kv_commit(cache, layers, code_layer_stride, scale_layer_stride, lens, path, path_ld,
+                                       steps, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -523,3 +592,239 @@ def nvfp4_gemm_batch(items, m: int = 1, ws=None, stream=None, descs=None):
     _check(tq_nvfp4_gemm_batch(descs, len(items), m, _dt(X0.dtype), _dt(Y0.dtype), ws.data_ptr(), ws.numel(),
                                _stream(stream)), "tq_nvfp4_gemm_batch")
     return [it[6] for it in items]
+
+
+# ---------------------------------------------------------------------------
+# key/value cache (tensor helpers)
+# ---------------------------------------------------------------------------
+class _on:
+    """Makes a tensor's device the current one for a call, where it is not already."""
+
+    def __init__(self, t: torch.Tensor):
+        if not t.is_cuda:
+            raise ValueError("expected CUDA tensors")
+        i = t.device.index
+        self.guard = None if i == torch.cuda.current_device() else torch.cuda.device(i)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _ints(t: torch.Tensor, name: str, device, *shape) -> int:
+    """Address of a contiguous int32 tensor of this shape (None: any extent)."""
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 tensor on {device}")
+    if t.dim() != len(shape) or any(want is not None and want != got for want, got in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _heads(t: torch.Tensor, name: str, device, *shape):
+    """(address, strides of all but the last dimension) of a head operand."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: expected unit stride in the last dimension")
+    return (t.data_ptr(), *t.stride()[:-1])
+
+
+def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, layers: int | None = None, device=None):
+    """A zero-filled pool of pages: (codes uint8 [pages, 2, kv_heads, page_size,
+    head_dim / 2], scales int16 [pages, 2, kv_heads, page_size, head_dim / 16]),
+    both with a leading dimension ``layers`` if that is given."""
+    nbytes = tq_kv_codes_bytes(pages, kv_heads, head_dim, page_size)
+    if nbytes == 0 and pages != 0:
+        raise ValueError("kv_cache: head_dim is a multiple of 32 up to 256, page_size a power of two from 16 to 1024")
+    lead = () if layers is None else (layers,)
+    device = device or torch.cuda.current_device()
+    codes = torch.zeros((*lead, pages, 2, kv_heads, page_size, head_dim // 2), dtype=torch.uint8, device=device)
+    scales = torch.zeros((*lead, pages, 2, kv_heads, page_size, head_dim // 16), dtype=torch.int16, device=device)
+    return codes, scales
+
+
+def _cache(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, layers: bool = False) -> KvCache:
+    """The C description of one layer's cache (of layer 0, with ``layers``)."""
+    shape = tuple(codes.shape[1:] if layers else codes.shape)
+    if codes.dtype != torch.uint8 or len(shape) != 5 or shape[1] != 2:
+        raise ValueError("codes: expected uint8 [pages, 2, kv_heads, page_size, head_dim / 2]")
+    pages, _, kv_heads, page_size, half = shape
+    if scales.dtype != torch.int16 or tuple(scales.shape) != (*codes.shape[:-1], half // 8):
+        raise ValueError("scales: expected int16 [pages, 2, kv_heads, page_size, head_dim / 16]")
+    inner = codes[0] if layers and codes.shape[0] else codes
+    inner_s = scales[0] if layers and scales.shape[0] else scales
+    if not inner.is_contiguous() or not inner_s.is_contiguous() or scales.device != codes.device:
+        raise ValueError("codes and scales: expected contiguous tensors on one device")
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != codes.device or (
+            page_table.stride(1) != 1 and page_table.shape[1] > 1):
+        raise ValueError("page_table: expected int32 [batch, pages of a sequence] on the cache's device")
+    batch, per_seq = page_table.shape
+    return KvCache(codes.data_ptr(), scales.data_ptr(), pages, page_table.data_ptr(), batch, per_seq,
+                   max(page_table.stride(0), per_seq) if batch < 2 else page_table.stride(0), kv_heads, 2 * half,
+                   page_size)
+
+
+def _rope_desc(inv_freq: torch.Tensor, device, interleaved=False, scale=1.0, inverse=False) -> RopeDesc:
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or \
+            inv_freq.device != device:
+        raise ValueError(f"inv_freq: expected a contiguous float32 vector on {device}")
+    return RopeDesc(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), int(inverse), scale)
+
+
+def rope_frequencies(rot_dim: int, theta: float = 10000.0, factor: float = 1.0, scaling: str = "none",
+                     original_context: int = 8192, low: float = 1.0, high: float = 4.0,
+                     device=None) -> torch.Tensor:
+    """Angles per position of ``rope``, theta^(-2i/rot_dim) for i < rot_dim / 2,
+    computed in 64 bits, as a float32 vector on the GPU.  ``scaling`` lengthens
+    the context by ``factor``:
+      "linear"   every frequency divided by factor;
+      "ntk"      theta multiplied by factor^(rot_dim / (rot_dim - 2));
+      "by_parts" a frequency that turns more than ``high`` times over
+                 original_context stays, one that turns fewer than ``low``
+                 times is divided by factor, between them a linear blend."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim: a positive even number")
+    if theta <= 0 or factor <= 0:
+        raise ValueError("theta and factor: positive numbers")
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim of at least 4")
+        theta = theta * factor ** (rot_dim / (rot_dim - 2))
+    freq = theta ** (-2.0 * torch.arange(rot_dim // 2, dtype=torch.float64) / rot_dim)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "by_parts":
+        if not high > low:
+            raise ValueError("by_parts: high has to be above low")
+        turns = original_context * freq / (2.0 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0.0, 1.0)
+        freq = freq * (keep + (1.0 - keep) / factor)
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return freq.to(torch.float32).to(device or torch.cuda.current_device())
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = False,
+         scale: float = 1.0, inverse: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotary positions of x [tokens, heads, dim]: the first 2 * len(inv_freq)
+    elements of each head rotated by positions[token] * inv_freq, the rest
+    unchanged.  ``inverse`` rotates back (the gradient).  ``out`` may be x."""
+    if x.dim() != 3:
+        raise ValueError("x: expected [tokens, heads, dim]")
+    with _on(x):
+        if out is None:
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        if out.dtype != x.dtype:
+            raise ValueError("out: expected x's dtype")
+        n, heads, dim = x.shape
+        desc = _rope_desc(inv_freq, x.device, interleaved, scale, inverse)
+        xp, xt, xh = _heads(x, "x", x.device, n, heads, dim)
+        op, ot, oh = _heads(out, "out", x.device, n, heads, dim)
+        _check(tq_rope(xp, op, _dt(x.dtype), n, heads, dim, xt, xh, ot, oh,
+                       _ints(positions, "positions", x.device, n), desc, _stream(stream)), "tq_rope")
+    return out
+
+
+def kv_append(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, seqs: torch.Tensor,
+              places: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope=None, interleaved: bool = False,
+              rope_scale: float = 1.0, stream=None) -> None:
+    """Writes the records of keys k and values v [n, kv_heads, head_dim]: token i
+    goes to place places[i] of sequence seqs[i].  ``rope`` = (positions,
+    inv_freq) rotates the keys on their way in."""
+    cache = _cache(codes, scales, page_table)
+    dev = codes.device
+    with _on(codes):
+        n = seqs.numel()
+        if k.dtype != v.dtype:
+            raise ValueError("k and v: expected one dtype")
+        kp, kt, kh = _heads(k, "k", dev, n, cache.kv_heads, cache.head_dim)
+        vp, vt, vh = _heads(v, "v", dev, n, cache.kv_heads, cache.head_dim)
+        desc, pos = None, None
+        if rope is not None:
+            pos = _ints(rope[0], "positions", dev, n)
+            desc = _rope_desc(rope[1], dev, interleaved, rope_scale)
+        _check(tq_kv_append(cache, _ints(seqs, "seqs", dev, n), _ints(places, "places", dev, n), n, kp, kt, kh, vp,
+                            vt, vh, _dt(k.dtype), pos, desc, _stream(stream)), "tq_kv_append")
+
+
+def kv_read(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, seqs: torch.Tensor,
+            places: torch.Tensor, dtype=torch.bfloat16, k: torch.Tensor | None = None,
+            v: torch.Tensor | None = None, stream=None):
+    """(keys, values) [n, kv_heads, head_dim] of the tokens at places[i] of seqs[i]."""
+    cache = _cache(codes, scales, page_table)
+    dev = codes.device
+    with _on(codes):
+        n = seqs.numel()
+        shape = (n, cache.kv_heads, cache.head_dim)
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=dev)
+        if v is None:
+            v = torch.empty(shape, dtype=k.dtype, device=dev)
+        if k.dtype != v.dtype:
+            raise ValueError("k and v: expected one dtype")
+        kp, kt, kh = _heads(k, "k", dev, *shape)
+        vp, vt, vh = _heads(v, "v", dev, *shape)
+        _check(tq_kv_read(cache, _ints(seqs, "seqs", dev, n), _ints(places, "places", dev, n), n, kp, kt, kh, vp, vt,
+                          vh, _dt(k.dtype), _stream(stream)), "tq_kv_read")
+    return k, v
+
+
+def kv_attention_workspace(batch: int, tree: int, heads: int, kv_heads: int, head_dim: int,
+                           device=None) -> torch.Tensor:
+    """A workspace tensor for ``kv_attention`` of these sizes."""
+    nbytes = tq_kv_attention_workspace_bytes(batch, tree, heads, kv_heads, head_dim)
+    if nbytes == 0:
+        raise ValueError("invalid sizes for workspace query")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or torch.cuda.current_device())
+
+
+def kv_attention(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                 q: torch.Tensor, parents: torch.Tensor | None = None, scale: float | None = None, dtype=None,
+                 out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of q [batch, tree, heads, head_dim] over the cache: every row
+    sees the lens[b] tokens of its sequence, its own drafted token (record at
+    place lens[b] + i) and that token's ancestors by ``parents`` [batch, tree]
+    (None: a chain).  ``scale`` defaults to head_dim^-0.5, ``dtype`` to q's."""
+    cache = _cache(codes, scales, page_table)
+    dev = codes.device
+    if q.dim() != 4:
+        raise ValueError("q: expected [batch, tree, heads, head_dim]")
+    batch, tree, heads, dim = q.shape
+    with _on(codes):
+        if out is None:
+            out = torch.empty(q.shape, dtype=dtype or q.dtype, device=dev)
+        shape = (cache.batch, tree, heads, cache.head_dim)
+        qp, qb, qt, qh = _heads(q, "q", dev, *shape)
+        op, ob, ot, oh = _heads(out, "out", dev, *shape)
+        par = None if parents is None else _ints(parents, "parents", dev, batch, tree)
+        if ws is None:
+            ws = kv_attention_workspace(batch, tree, heads, cache.kv_heads, dim, dev)
+        elif ws.device != dev:
+            raise ValueError(f"ws: expected a tensor on {dev}")
+        _check(tq_kv_attention(cache, _ints(lens, "lens", dev, batch), par, tree, qp, _dt(q.dtype), qb, qt, qh, op,
+                               _dt(out.dtype), ob, ot, oh, tree, heads, dim ** -0.5 if scale is None else scale,
+                               ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)), "tq_kv_attention")
+    return out
+
+
+def kv_commit(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+              path: torch.Tensor, stream=None) -> None:
+    """Moves the records of accepted drafted tokens together: record
+    lens[b] + path[b, i] to place lens[b] + i, for increasing path[b] up to its
+    first entry that does not increase (-1).  codes and scales of one layer, or
+    with a leading dimension of layers that share the page table."""
+    layered = codes.dim() == 6
+    cache = _cache(codes, scales, page_table, layered)
+    dev = codes.device
+    layers = codes.shape[0] if layered else 1
+    with _on(codes):
+        batch, steps = cache.batch, path.shape[-1]
+        _check(tq_kv_commit(cache, layers, codes.stride(0) if layered else 0, scales.stride(0) if layered else 0,
+                            _ints(lens, "lens", dev, batch), _ints(path, "path", dev, batch, steps), steps, steps,
+                            _stream(stream)), "tq_kv_commit")

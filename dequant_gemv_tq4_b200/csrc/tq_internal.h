@@ -194,4 +194,83 @@ cudaError_t launch_nvfp4_quantize(const void *w, int dtype, int64_t n, int64_t k
 cudaError_t launch_nvfp4_dequantize(const uint8_t *codes, const uint8_t *scales, const float *tensor_scale,
                                     int64_t n, int64_t k, void *w_out, int dtype, int64_t ldo, cudaStream_t stream);
 
+// ---- key/value cache -----------------------------------------------------------
+// Largest scale of a cache record: 2.7326 * 23968 is the largest fp16 product
+// of a centroid and a scale that stays finite.
+constexpr float kKvScaleMax = 23968.0f;
+
+struct KvCache {  // device-side description (tq_kv_cache with a checked layout)
+    uint8_t *codes;
+    uint16_t *scales;
+    const int32_t *page_table;
+    int64_t pages, table_ld;
+    int batch, pages_per_seq, kv_heads, head_dim, page_shift;
+};
+
+struct RopeJob {
+    const void *x;
+    void *out;
+    const int32_t *positions;
+    const float *inv_freq;
+    int64_t tokens, x_token, x_head, o_token, o_head;
+    int heads, dim, rot, interleaved, inverse, dtype;
+    float scale;
+};
+cudaError_t launch_rope(const RopeJob &job, cudaStream_t stream);
+
+struct KvAppendJob {
+    KvCache c;
+    const void *x[2];  // keys, values
+    int64_t token_stride[2], head_stride[2];
+    const int32_t *seqs, *places;
+    const int32_t *positions;  // null: keys enter as they are
+    const float *inv_freq;
+    int64_t tokens;
+    int rot, interleaved, dtype;
+    float scale;
+};
+cudaError_t launch_kv_append(const KvAppendJob &job, cudaStream_t stream);
+
+struct KvReadJob {
+    KvCache c;
+    void *out[2];
+    int64_t token_stride[2], head_stride[2];
+    const int32_t *seqs, *places;
+    int64_t tokens;
+    int dtype;
+};
+cudaError_t launch_kv_read(const KvReadJob &job, cudaStream_t stream);
+
+struct KvCommitJob {
+    KvCache c;
+    int64_t layers, code_layer, scale_layer;
+    const int32_t *lens, *path;
+    int64_t path_ld;
+    int steps;
+};
+cudaError_t launch_kv_commit(const KvCommitJob &job, cudaStream_t stream);
+
+// Attention over the cache (tq_attention.cu).  A unit is (sequence, key/value
+// head, tile of kRows rows); a row is one query head of one drafted token, a
+// tile's rows share the head's keys and values.  Units are cut into groups of
+// 16 tokens, and the groups of all units into equal ranges, one per CTA; the
+// part of a unit that one CTA takes leaves a partial result in slot
+// (unit + CTA) of the workspace, and a second launch joins each unit's parts.
+struct AttentionJob {
+    KvCache c;
+    const int32_t *lens, *parents;
+    int64_t parents_ld;
+    const void *q;
+    int64_t q_batch, q_token, q_head;
+    void *out;
+    int64_t o_batch, o_token, o_head;
+    int tree, heads, qdtype, odtype;
+    float scale;
+    char *workspace;
+};
+constexpr int kAttnMaxTree = 64;
+constexpr int64_t kAttnMaxBatch = 4096;
+size_t attention_workspace_bytes(int64_t batch, int tree, int heads, int kv_heads, int head_dim, int sm_count);
+cudaError_t launch_attention(const AttentionJob &job, int sm_count, cudaStream_t stream);
+
 }  // namespace tq

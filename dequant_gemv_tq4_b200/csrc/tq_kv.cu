@@ -1,0 +1,554 @@
+// tq_kv.cu -- the TQ4_1S key/value cache: rotary positions, quantising keys
+// and values into the paged cache, reading them back, and moving an accepted
+// branch's records together.
+//
+// A cache record is one token's head vector in the codec of the weights: per
+// 32-element block the sign flip, the 32-point Walsh-Hadamard transform, two
+// fp16 half-block scales and sixteen nibble codes per half (include/tq.h).
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+namespace {
+
+__constant__ uint32_t c_kv_thr_bits[7] = TQ_THR_F32_INIT;
+__constant__ uint32_t c_kv_mag_bits[8] = TQ_MAG_F32_INIT;
+
+constexpr int kKvThreads = 256;
+
+// One element as fp32, at any alignment of its own type.
+template <int DT>
+__device__ __forceinline__ float load1(const char *p) {
+    if (DT == kF32) return *reinterpret_cast<const float *>(p);
+    if (DT == kBF16) return __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p));
+    return __half2float(*reinterpret_cast<const __half *>(p));
+}
+
+// cos and sin of position * frequency, times `scale`.  The product of a 31-bit
+// position and a 24-bit frequency is held in fp64 and reduced there to a
+// fraction of a turn: in fp32 the angle of position 10^6 would be off by up
+// to 0.03 rad.  What is left lies in [-1/2, 1/2] turns, where rounding it to
+// fp32 costs at most 2^-25 turns.
+__device__ __forceinline__ float2 rope_cos_sin(int position, float inv_freq, float scale, bool inverse) {
+    constexpr double kPerTurn = 0.15915494309189533577;
+    const double turns = (double)position * (double)inv_freq * kPerTurn;
+    float s, c;
+    sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+    if (inverse) s = -s;
+    return make_float2(c * scale, s * scale);
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions.  A work item is V neighbouring pairs (or V elements past
+// the rotated part) of one token for `hchunk` heads: the angles, which all
+// heads share, are computed once per item.  Bound by HBM for long inputs
+// (each element is read and written once), by the launch for one step.
+// ---------------------------------------------------------------------------
+struct RopeParams {
+    const char *x;
+    char *out;
+    const int32_t *positions;
+    const float *inv_freq;
+    int64_t x_token, x_head, o_token, o_head;  // strides in elements
+    int64_t items;
+    int heads, dim, rot, hchunk, chunks, slots, rot_slots;
+    float scale;
+    int interleaved, inverse, copy_tail;
+};
+
+// V elements at p: one 16-byte access or a scalar one.
+template <int DT, int V>
+__device__ __forceinline__ void load_v(const char *p, float (&v)[V]) {
+    if constexpr (V == 1) {
+        v[0] = load1<DT>(p);
+    } else if constexpr (DT == kF32) {
+        const float4 q = *reinterpret_cast<const float4 *>(p);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (DT == kBF16) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void store_v(char *p, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        store1<DT>(p, v[0]);
+    } else if constexpr (DT == kF32) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (DT == kBF16) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <int DT, int V>
+__global__ void __launch_bounds__(kKvThreads) rope_kernel(const RopeParams P) {
+    constexpr int E = ElemSize<DT>::value;
+    const int64_t item = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
+    if (item >= P.items) return;
+    const int slot = (int)(item % P.slots);
+    const int64_t rest = item / P.slots;
+    const int chunk = (int)(rest % P.chunks);
+    const int64_t token = rest / P.chunks;
+    const int h0 = chunk * P.hchunk, h1 = min(P.heads, h0 + P.hchunk);
+    const char *x = P.x + token * P.x_token * E;
+    char *o = P.out + token * P.o_token * E;
+
+    if (slot >= P.rot_slots) {  // past the rotated part: copied
+        if (!P.copy_tail) return;
+        const int e = P.rot + (slot - P.rot_slots) * V;
+        for (int h = h0; h < h1; ++h) {
+            float v[V];
+            load_v<DT, V>(x + (h * P.x_head + e) * E, v);
+            store_v<DT, V>(o + (h * P.o_head + e) * E, v);
+        }
+        return;
+    }
+    const int position = P.positions[token];
+    float2 cs[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) cs[i] = rope_cos_sin(position, P.inv_freq[slot * V + i], P.scale, P.inverse);
+    // pair i of the item: (a0 + i, a1 + i), or elements 2i, 2i+1 of 2V neighbours
+    const int a0 = P.interleaved ? 2 * slot * V : slot * V;
+    const int a1 = P.interleaved ? a0 + V : a0 + P.rot / 2;
+    for (int h = h0; h < h1; ++h) {
+        float u[V], w[V];
+        load_v<DT, V>(x + (h * P.x_head + a0) * E, u);
+        load_v<DT, V>(x + (h * P.x_head + a1) * E, w);
+        float ru[V], rw[V];
+        if (P.interleaved && V > 1) {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float2 c0 = cs[i / 2], c1 = cs[(V + i) / 2];
+                ru[i] = u[i] * c0.x - u[i + 1] * c0.y;
+                ru[i + 1] = u[i] * c0.y + u[i + 1] * c0.x;
+                rw[i] = w[i] * c1.x - w[i + 1] * c1.y;
+                rw[i + 1] = w[i] * c1.y + w[i + 1] * c1.x;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                ru[i] = u[i] * cs[i].x - w[i] * cs[i].y;
+                rw[i] = u[i] * cs[i].y + w[i] * cs[i].x;
+            }
+        }
+        store_v<DT, V>(o + (h * P.o_head + a0) * E, ru);
+        store_v<DT, V>(o + (h * P.o_head + a1) * E, rw);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Cache addressing.
+// ---------------------------------------------------------------------------
+// Record of (page, plane, head, row), or -1 where the token has no place: a
+// negative sequence or position, one past the table, or a page id outside the pool.
+__device__ __forceinline__ int64_t record_page(const KvCache &C, int seq, int place) {
+    if (seq < 0 || seq >= C.batch || place < 0) return -1;
+    const int col = place >> C.page_shift;
+    if (col >= C.pages_per_seq) return -1;
+    const int64_t page = C.page_table[seq * C.table_ld + col];
+    return page >= 0 && page < C.pages ? page : -1;
+}
+
+__device__ __forceinline__ int64_t record_index(const KvCache &C, int64_t page, int plane, int head, int place) {
+    return (((page * 2 + plane) * C.kv_heads + head) << C.page_shift) + (place & ((1 << C.page_shift) - 1));
+}
+
+// ---------------------------------------------------------------------------
+// Append: eight lanes own one 32-element block of one token (lane p elements
+// 4p..4p+3) and walk `hchunk` heads of the key plane or of the value plane, so
+// that a token's rotary angles are computed once for all of them.
+// The arithmetic is tq_quantize's, operation for operation (butterfly stages
+// 1, 2 in registers, 4, 8, 16 across lanes; adjacent-pair tree of squares).
+// ---------------------------------------------------------------------------
+struct AppendParams {
+    KvCache c;
+    const char *x[2];
+    int64_t token_stride[2], head_stride[2];  // elements
+    const int32_t *seqs, *places;
+    const int32_t *positions;  // null: no rotation
+    const float *inv_freq;
+    int64_t items;  // tokens * planes * chunks * blocks
+    int rot, interleaved, blocks, hchunk, chunks;
+    float scale;
+};
+
+// A half-block's code of y against its seven scaled thresholds.
+__device__ __forceinline__ uint32_t cache_code(float y, const float (&t)[7]) {
+    const float a = fabsf(y);
+    const bool b2 = a > t[3];
+    const bool b1 = a > (b2 ? t[5] : t[1]);
+    const bool b0 = a > (b1 ? (b2 ? t[6] : t[2]) : (b2 ? t[4] : t[0]));
+    return (b2 ? 4u : 0u) + (b1 ? 2u : 0u) + (b0 ? 1u : 0u) + (y < 0.0f ? 8u : 0u);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendParams P) {
+    constexpr int E = ElemSize<DT>::value;
+    const int64_t item = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) >> 3;
+    const int p = threadIdx.x & 7;
+    // lanes past the last item follow along without storing (the shuffles need whole warps)
+    const int64_t it = item < P.items ? item : P.items - 1;
+    const int block = (int)(it % P.blocks);
+    int64_t rest = it / P.blocks;
+    const int chunk = (int)(rest % P.chunks);
+    rest /= P.chunks;
+    const int plane = (int)(rest & 1);
+    const int64_t token = rest >> 1;
+    const int place = P.places[token];
+    const int64_t page = record_page(P.c, P.seqs[token], place);
+    const bool store = item < P.items && page >= 0;
+
+    const int e0 = 32 * block + 4 * p;  // this lane's elements of the head
+    uint32_t flips[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) flips[i] = sign_mask(e0 + i);
+    float thr[7];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) thr[i] = __uint_as_float(c_kv_thr_bits[i]);
+
+    // rotary partners: element e0 + i pairs with partner[i], its rotated value
+    // is x cos + partner * (signed sin)
+    const bool rotate = plane == 0 && P.positions != nullptr && e0 < P.rot;
+    const int half = P.rot / 2;
+    float2 cs[4];
+    int first = 0;
+    if (rotate) {
+        const int position = P.positions[token];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = e0 + i;
+            const bool lower = P.interleaved ? (e & 1) == 0 : e < half;
+            const int pair = P.interleaved ? e >> 1 : (e < half ? e : e - half);
+            cs[i] = e < P.rot ? rope_cos_sin(position, P.inv_freq[pair], P.scale, false) : make_float2(1.f, 0.f);
+            if (lower) cs[i].y = -cs[i].y;
+        }
+        first = e0 < half ? e0 + half : e0 - half;
+    }
+    // the partners are four neighbours when the halves are split between lanes
+    const bool whole = !P.interleaved && (half & 3) == 0 && (P.rot & 3) == 0;
+
+    const char *base = P.x[plane] + token * P.token_stride[plane] * E;
+    const int h0 = chunk * P.hchunk, h1 = min(P.c.kv_heads, h0 + P.hchunk);
+    for (int h = h0; h < h1; ++h) {
+        const char *x = base + (int64_t)h * P.head_stride[plane] * E;
+        float v[4];
+        load4<DT>(x + e0 * E, v);
+        if (rotate) {
+            float o[4];
+            if (P.interleaved) {
+                o[0] = v[1]; o[1] = v[0]; o[2] = v[3]; o[3] = v[2];
+            } else if (whole) {
+                load4<DT>(x + first * E, o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = e0 + i;
+                    o[i] = e < P.rot ? load1<DT>(x + (e < half ? e + half : e - half) * E) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = v[i] * cs[i].x + o[i] * cs[i].y;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = flip(v[i], flips[i]);
+        fwht32_warp(v, p);
+
+        float q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = __fmul_rn(v[i], v[i]);
+        float sum = __fadd_rn(__fadd_rn(q[0], q[1]), __fadd_rn(q[2], q[3]));
+        sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, 1));
+        sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, 2));
+        // the scale saturates (and a NaN becomes the limit), so that every
+        // record decodes to finite fp16 products c * d
+        const __half hd = __float2half_rn(fminf(__fsqrt_rn(__fmul_rn(sum, 0.0625f)), kKvScaleMax));
+        const float d = __half2float(hd);
+        float t[7];
+#pragma unroll
+        for (int i = 0; i < 7; ++i) t[i] = __fmul_rn(thr[i], d);
+        uint32_t code = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code |= cache_code(v[i], t) << (4 * i);
+        code |= __shfl_down_sync(kFull, code, 1) << 16;  // even lanes: eight codes
+        const uint32_t dw = __half_as_ushort(hd);
+        const uint32_t d2 = dw | (__shfl_down_sync(kFull, dw, 4) << 16);
+        if (store) {
+            const int64_t r = record_index(P.c, page, plane, h, place);
+            if ((p & 1) == 0)
+                *reinterpret_cast<uint32_t *>(P.c.codes + r * (P.c.head_dim / 2) + 16 * block + 2 * p) = code;
+            if (p == 0) *reinterpret_cast<uint32_t *>(P.c.scales + r * (P.c.head_dim / 16) + 2 * block) = d2;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Read: the same lane layout in reverse.  x~ = s . (H (c d)) / 32 in fp32
+// (tq_dequantize's order), rounded once to the output type.
+// ---------------------------------------------------------------------------
+struct ReadParams {
+    KvCache c;
+    char *out[2];
+    int64_t token_stride[2], head_stride[2];
+    const int32_t *seqs, *places;
+    int64_t items;
+    int blocks, hchunk, chunks;
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const ReadParams P) {
+    constexpr int E = ElemSize<DT>::value;
+    // sixteen signed centroids, one bank each: any mix of codes in a warp is
+    // one conflict-free access
+    __shared__ float table[16];
+    if (threadIdx.x < 16)
+        table[threadIdx.x] = __uint_as_float(c_kv_mag_bits[threadIdx.x & 7] ^ ((threadIdx.x & 8u) << 28));
+    __syncthreads();
+    const int64_t item = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) >> 3;
+    const int p = threadIdx.x & 7;
+    const int64_t it = item < P.items ? item : P.items - 1;
+    const int block = (int)(it % P.blocks);
+    int64_t rest = it / P.blocks;
+    const int chunk = (int)(rest % P.chunks);
+    rest /= P.chunks;
+    const int plane = (int)(rest & 1);
+    const int64_t token = rest >> 1;
+    const int place = P.places[token];
+    const int64_t page = record_page(P.c, P.seqs[token], place);
+    const int e0 = 32 * block + 4 * p;
+    uint32_t flips[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) flips[i] = sign_mask(e0 + i);
+    char *base = P.out[plane] + token * P.token_stride[plane] * E;
+    const int h0 = chunk * P.hchunk, h1 = min(P.c.kv_heads, h0 + P.hchunk);
+    for (int h = h0; h < h1; ++h) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (page >= 0) {
+            const int64_t r = record_index(P.c, page, plane, h, place);
+            const uint32_t w =
+                *reinterpret_cast<const uint16_t *>(P.c.codes + r * (P.c.head_dim / 2) + 16 * block + 2 * p);
+            const float d = __fmul_rn(
+                __half2float(__ushort_as_half(P.c.scales[r * (P.c.head_dim / 16) + 2 * block + (p >> 2)])), 0.03125f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(table[(w >> (4 * i)) & 15u], d);
+        }
+        fwht32_warp(v, p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = flip(v[i], flips[i]);
+        if (item < P.items) store4<DT>(base + ((int64_t)h * P.head_stride[plane] + e0) * E, v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Commit: the records of an accepted branch move down to where the sequence
+// continues.  One thread owns one 16-byte piece of the codes (or one 4-byte
+// piece of the scales) of a (layer, sequence, plane, head) and moves it for
+// the whole branch, eight records at a time: all eight loads before the
+// stores.  The branch increases, so a record's target never lies behind a
+// source that is still to be read.
+// ---------------------------------------------------------------------------
+struct CommitParams {
+    KvCache c;  // of layer 0
+    int64_t code_layer, scale_layer;  // strides of a layer, elements
+    const int32_t *lens, *path;
+    int64_t path_ld;
+    int64_t items;  // layers * batch * 2 * heads * pieces
+    int steps, pieces, code_pieces;
+};
+
+template <typename T>
+__device__ __forceinline__ void move_branch(const CommitParams &P, char *plane0, int64_t record_bytes, int seq,
+                                            int plane, int head, int offset) {
+    const int len = max(P.lens[seq], 0);
+    const int32_t *path = P.path + seq * P.path_ld;
+    int last = -1;
+    for (int i0 = 0; i0 < P.steps; i0 += 8) {
+        T v[8];
+        int64_t to[8];
+        bool end = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            to[i] = -1;
+            const int src = !end && i0 + i < P.steps ? path[i0 + i] : -1;
+            if (src <= last || src > INT32_MAX - len) {  // the branch ends here
+                end = true;
+                continue;
+            }
+            last = src;
+            if (src == i0 + i) continue;  // in place already
+            const int64_t from_page = record_page(P.c, seq, len + src);
+            const int64_t to_page = record_page(P.c, seq, len + i0 + i);
+            if (from_page < 0 || to_page < 0) continue;
+            v[i] = *reinterpret_cast<const T *>(
+                plane0 + record_index(P.c, from_page, plane, head, len + src) * record_bytes + offset);
+            to[i] = record_index(P.c, to_page, plane, head, len + i0 + i) * record_bytes + offset;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (to[i] >= 0) *reinterpret_cast<T *>(plane0 + to[i]) = v[i];
+        if (end) return;
+    }
+}
+
+__global__ void __launch_bounds__(kKvThreads) kv_commit_kernel(const CommitParams P) {
+    const int64_t item = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
+    if (item >= P.items) return;
+    const int piece = (int)(item % P.pieces);
+    int64_t rest = item / P.pieces;
+    const int head = (int)(rest % P.c.kv_heads);
+    rest /= P.c.kv_heads;
+    const int plane = (int)(rest & 1);
+    rest >>= 1;
+    const int seq = (int)(rest % P.c.batch);
+    const int64_t layer = rest / P.c.batch;
+    if (piece < P.code_pieces)
+        move_branch<uint4>(P, reinterpret_cast<char *>(P.c.codes + layer * P.code_layer), P.c.head_dim / 2, seq, plane,
+                           head, 16 * piece);
+    else
+        move_branch<uint32_t>(P, reinterpret_cast<char *>(P.c.scales + layer * P.scale_layer), P.c.head_dim / 8, seq,
+                              plane, head, 4 * (piece - P.code_pieces));
+}
+
+// Heads per work item: as many as share work (angles, indices) while the
+// launch still has `enough` threads to fill the GPU's 148 SMs; short inputs
+// take one head per item.
+int heads_per_item(int64_t threads_per_head, int heads, int64_t enough) {
+    int h = heads;
+    while (h > 1 && threads_per_head * ((heads + h - 1) / h) < enough) h = (h + 1) / 2;
+    return h;
+}
+
+unsigned blocks_of(int64_t threads) { return (unsigned)((threads + kKvThreads - 1) / kKvThreads); }
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeJob &j, cudaStream_t stream) {
+    const int esize = j.dtype == kF32 ? 4 : 2, vec = 16 / esize;
+    // whole 16-byte accesses where every part and stride allows them; else
+    // element by element
+    const bool wide = j.rot % (2 * vec) == 0 && j.dim % vec == 0 && j.x_token % vec == 0 && j.x_head % vec == 0 &&
+                      j.o_token % vec == 0 && j.o_head % vec == 0 && reinterpret_cast<uintptr_t>(j.x) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(j.out) % 16 == 0;
+    const int V = wide ? vec : 1;
+    RopeParams P;
+    P.x = static_cast<const char *>(j.x);
+    P.out = static_cast<char *>(j.out);
+    P.positions = j.positions;
+    P.inv_freq = j.inv_freq;
+    P.x_token = j.x_token;
+    P.x_head = j.x_head;
+    P.o_token = j.o_token;
+    P.o_head = j.o_head;
+    P.heads = j.heads;
+    P.dim = j.dim;
+    P.rot = j.rot;
+    P.scale = j.scale;
+    P.interleaved = j.interleaved;
+    P.inverse = j.inverse;
+    P.copy_tail = j.out != j.x || j.x_token != j.o_token || j.x_head != j.o_head;
+    P.rot_slots = j.rot / 2 / V;
+    P.slots = P.rot_slots + (P.copy_tail ? (j.dim - j.rot) / V : 0);
+    if (P.slots == 0) return cudaSuccess;
+    P.hchunk = heads_per_item(j.tokens * P.slots, j.heads, (int64_t)1 << 18);
+    P.chunks = (j.heads + P.hchunk - 1) / P.hchunk;
+    P.items = j.tokens * P.chunks * P.slots;
+    const unsigned grid = blocks_of(P.items);
+    auto run = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        constexpr int W = 16 / ElemSize<DT>::value;
+        if (wide) rope_kernel<DT, W><<<grid, kKvThreads, 0, stream>>>(P);
+        else rope_kernel<DT, 1><<<grid, kKvThreads, 0, stream>>>(P);
+    };
+    if (j.dtype == kF32) run(std::integral_constant<int, kF32>());
+    else if (j.dtype == kBF16) run(std::integral_constant<int, kBF16>());
+    else run(std::integral_constant<int, kF16>());
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append(const KvAppendJob &j, cudaStream_t stream) {
+    AppendParams P;
+    P.c = j.c;
+    for (int i = 0; i < 2; ++i) {
+        P.x[i] = static_cast<const char *>(j.x[i]);
+        P.token_stride[i] = j.token_stride[i];
+        P.head_stride[i] = j.head_stride[i];
+    }
+    P.seqs = j.seqs;
+    P.places = j.places;
+    P.positions = j.positions;
+    P.inv_freq = j.inv_freq;
+    P.rot = j.rot;
+    P.interleaved = j.interleaved;
+    P.scale = j.scale;
+    P.blocks = j.c.head_dim / 32;
+    P.hchunk = heads_per_item(j.tokens * 2 * P.blocks * 8, j.c.kv_heads, (int64_t)1 << 18);
+    P.chunks = (j.c.kv_heads + P.hchunk - 1) / P.hchunk;
+    P.items = j.tokens * 2 * P.chunks * P.blocks;
+    const unsigned grid = blocks_of(P.items * 8);
+    if (j.dtype == kF32) kv_append_kernel<kF32><<<grid, kKvThreads, 0, stream>>>(P);
+    else if (j.dtype == kBF16) kv_append_kernel<kBF16><<<grid, kKvThreads, 0, stream>>>(P);
+    else kv_append_kernel<kF16><<<grid, kKvThreads, 0, stream>>>(P);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_read(const KvReadJob &j, cudaStream_t stream) {
+    ReadParams P;
+    P.c = j.c;
+    for (int i = 0; i < 2; ++i) {
+        P.out[i] = static_cast<char *>(j.out[i]);
+        P.token_stride[i] = j.token_stride[i];
+        P.head_stride[i] = j.head_stride[i];
+    }
+    P.seqs = j.seqs;
+    P.places = j.places;
+    P.blocks = j.c.head_dim / 32;
+    P.hchunk = heads_per_item(j.tokens * 2 * P.blocks * 8, j.c.kv_heads, (int64_t)1 << 18);
+    P.chunks = (j.c.kv_heads + P.hchunk - 1) / P.hchunk;
+    P.items = j.tokens * 2 * P.chunks * P.blocks;
+    const unsigned grid = blocks_of(P.items * 8);
+    if (j.dtype == kF32) kv_read_kernel<kF32><<<grid, kKvThreads, 0, stream>>>(P);
+    else if (j.dtype == kBF16) kv_read_kernel<kBF16><<<grid, kKvThreads, 0, stream>>>(P);
+    else kv_read_kernel<kF16><<<grid, kKvThreads, 0, stream>>>(P);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_commit(const KvCommitJob &j, cudaStream_t stream) {
+    CommitParams P;
+    P.c = j.c;
+    P.code_layer = j.code_layer;
+    P.scale_layer = j.scale_layer;
+    P.lens = j.lens;
+    P.path = j.path;
+    P.path_ld = j.path_ld;
+    P.steps = j.steps;
+    P.code_pieces = j.c.head_dim / 32;
+    P.pieces = P.code_pieces + j.c.head_dim / 32;
+    P.items = j.layers * j.c.batch * 2 * j.c.kv_heads * P.pieces;
+    kv_commit_kernel<<<blocks_of(P.items), kKvThreads, 0, stream>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace tq

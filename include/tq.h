@@ -440,6 +440,166 @@ TQ_API size_t tq_nvfp4_gemm_batch_workspace_bytes(const tq_nvfp4_gemm_desc *desc
 TQ_API tq_status tq_nvfp4_gemm_batch(const tq_nvfp4_gemm_desc *descs, int count, int64_t m, tq_dtype xt, tq_dtype yt,
                                      void *workspace, size_t ws_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Key/value cache in TQ4_1S, and what works on it
+ * ---------------------------------------------------------------------------
+ * The attention half of a decoding step next to the products above: rotary
+ * positions, writing keys and values into a paged cache in the codec of the
+ * weights (TQ page, 格式原理), reading them back, attention over the packed
+ * records, and moving an accepted branch of drafted tokens together.
+ *
+ * The cache is a pool of pages that the caller allocates:
+ *  - codes   uint8  [pages][2][kv_heads][page_size][head_dim / 2]
+ *  - scales  uint16 [pages][2][kv_heads][page_size][head_dim / 16]
+ *    plane 0 the keys, plane 1 the values; 5.0 bits per element.
+ *  - A record is one token's head vector: per 32-element block of the head
+ *    (element index = column index of the sign hash) the codes and scales of
+ *    tq_quantize, bit for bit, except that a scale saturates at 23968 (so that
+ *    every centroid times its scale is finite in fp16; a block that holds a
+ *    NaN gets that scale and code 0).  Byte i of a record's codes holds
+ *    elements 2i (low nibble) and 2i + 1; its scales are d0, d1 of each block.
+ *  - page_table[b][i] is the page of tokens i * page_size .. of sequence b.  A
+ *    token whose column is past pages_per_seq, or whose page id is outside
+ *    [0, pages), has no place: writes of it are dropped, reads give zeros, and
+ *    attention leaves it out.
+ *  - Sizes: head_dim a multiple of 32 up to TQ_KV_MAX_HEAD_DIM; page_size a
+ *    power of two from 16 to TQ_KV_MAX_PAGE; a sequence's table spans at most
+ *    2^30 tokens.  Offsets into the pool are 64-bit.
+ *
+ * Head operands (x, k, v, q, out) are [tokens][heads][dim] with unit element
+ * stride and the strides given, in elements.
+ */
+#define TQ_KV_MAX_HEAD_DIM 256
+#define TQ_KV_MAX_PAGE 1024
+#define TQ_KV_MAX_HEADS 1024
+#define TQ_KV_MAX_BATCH 4096
+#define TQ_KV_MAX_TREE 64
+#define TQ_KV_MAX_LAYERS 4096
+#define TQ_KV_MAX_TOKENS ((int64_t)1 << 24)
+#define TQ_ROPE_MAX_DIM 1024
+
+typedef struct {
+    uint8_t *codes;            /* device, 16-byte aligned */
+    uint16_t *scales;          /* device, 16-byte aligned */
+    int64_t pages;             /* pages of the pool */
+    const int32_t *page_table; /* device, [batch][page_table_ld] */
+    int64_t batch;             /* sequences, <= TQ_KV_MAX_BATCH */
+    int64_t pages_per_seq;     /* columns of the table in use */
+    int64_t page_table_ld;     /* >= pages_per_seq */
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+} tq_kv_cache;
+
+/* Bytes of a pool's codes (2 * pages * kv_heads * page_size * head_dim / 2)
+ * and scales (a quarter of that); 0 for invalid sizes. */
+TQ_API size_t tq_kv_codes_bytes(int64_t pages, int64_t kv_heads, int64_t head_dim, int64_t page_size);
+TQ_API size_t tq_kv_scales_bytes(int64_t pages, int64_t kv_heads, int64_t head_dim, int64_t page_size);
+
+/* A rotation by positions: the first rot_dim elements of a head in pairs
+ * (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved; the rest pass
+ * unchanged. */
+typedef struct {
+    const float *inv_freq; /* device, rot_dim / 2 angles per position, in radians */
+    int32_t rot_dim;       /* even, 2 .. dim */
+    int32_t interleaved;
+    int32_t inverse;       /* rotate back (by minus the angle): the transpose, i.e. the gradient */
+    float scale;           /* multiplies cos and sin (1 unless a long-context scaling asks for more) */
+} tq_rope_desc;
+
+/*
+ * tq_rope -- for pair (x, y) of frequency f at position p, with a = p f:
+ *   out = scale * (x cos a - y sin a, x sin a + y cos a)
+ * The angle is formed and reduced in 64 bits, so positions of any size keep
+ * their accuracy; the rotation is fp32, rounded once to t.
+ *   x, out     device, tokens x heads x dim of dtype t, aligned to t (16-byte
+ *              alignment and strides that are multiples of 16 bytes run
+ *              fastest); out may be x itself (same strides), and must not
+ *              overlap it otherwise
+ *   positions  device, one per token (any value, also negative)
+ */
+TQ_API tq_status tq_rope(const void *x, void *out, tq_dtype t, int64_t tokens, int64_t heads, int64_t dim,
+                         int64_t x_token_stride, int64_t x_head_stride, int64_t out_token_stride,
+                         int64_t out_head_stride, const int32_t *positions, const tq_rope_desc *rope, void *stream);
+
+/*
+ * tq_kv_append -- writes the records of `tokens` tokens: token i goes to place
+ * places[i] (0-based) of sequence seqs[i].  Tokens without a place (a negative
+ * sequence or place among them) are dropped.  Two tokens with the same place
+ * in one call leave that record undefined.
+ *   k, v       device, tokens x kv_heads x head_dim of dtype t, 16-byte
+ *              aligned, strides multiples of 8 elements
+ *   rope       host, or NULL: rotates the keys on their way in (fp32, not
+ *              rounded before the codec); inverse must be 0
+ *   positions  device, the tokens' rotary positions (a drafted token's is its
+ *              depth in the tree, not its place); ignored without rope
+ */
+TQ_API tq_status tq_kv_append(const tq_kv_cache *cache, const int32_t *seqs, const int32_t *places, int64_t tokens,
+                              const void *k, int64_t k_token_stride, int64_t k_head_stride, const void *v,
+                              int64_t v_token_stride, int64_t v_head_stride, tq_dtype t, const int32_t *positions,
+                              const tq_rope_desc *rope, void *stream);
+
+/*
+ * tq_kv_read -- the inverse: keys and values of the given tokens,
+ * x~ = s .* (H c) / 32 in fp32, rounded once to t; zeros for a token without a
+ * place.  k and v as in tq_kv_append (written; they must not overlap).
+ */
+TQ_API tq_status tq_kv_read(const tq_kv_cache *cache, const int32_t *seqs, const int32_t *places, int64_t tokens,
+                            void *k, int64_t k_token_stride, int64_t k_head_stride, void *v, int64_t v_token_stride,
+                            int64_t v_head_stride, tq_dtype t, void *stream);
+
+/*
+ * tq_kv_attention -- attention of `tree` drafted tokens per sequence (1 for
+ * plain decoding) over the cache.  Sequence b holds lens[b] tokens, and its
+ * drafted tokens' records stand behind them, token i at place lens[b] + i
+ * (tq_kv_append them first).  Query head h reads key/value head
+ * h / (heads / kv_heads).  Row (b, i, h) attends to all lens[b] tokens, to
+ * drafted token i and to its ancestors:
+ *   out = sum_j softmax_j(scale * q . k~_j) v~_j
+ *   lens     device, [batch] (negative counts as 0)
+ *   parents  device, [batch][parents_ld], parents[b][i] the drafted token that
+ *            i continues (an earlier one), or -1 where it continues the
+ *            sequence; any other value says that token i is not there: it and
+ *            its descendants are not attended to and their output is zero.
+ *            NULL: a chain, token i continues i - 1
+ *   q        device, batch x tree x heads x head_dim of dtype qt, 16-byte
+ *            aligned, strides multiples of 8 elements; |q| below 65504
+ *   out      device, same shape, dtype ot, the same rules (written; must not
+ *            overlap q or the cache)
+ *   heads    query heads, a multiple of kv_heads
+ *   workspace  device, >= tq_kv_attention_workspace_bytes(...) bytes, 256-byte
+ *            aligned, exclusively owned by this call until it completes on
+ *            `stream`; need not be cleared, keeps nothing between calls
+ * The rotated query, centroid times scale and the softmax weights enter the
+ * tensor cores as fp16; sums, the running maximum and the softmax's sum are
+ * fp32.  A record that no row attends to may hold anything.
+ * tree <= TQ_KV_MAX_TREE.
+ */
+TQ_API size_t tq_kv_attention_workspace_bytes(int64_t batch, int64_t tree, int64_t heads, int64_t kv_heads,
+                                              int64_t head_dim);
+TQ_API tq_status tq_kv_attention(const tq_kv_cache *cache, const int32_t *lens, const int32_t *parents,
+                                 int64_t parents_ld, const void *q, tq_dtype qt, int64_t q_batch_stride,
+                                 int64_t q_token_stride, int64_t q_head_stride, void *out, tq_dtype ot,
+                                 int64_t out_batch_stride, int64_t out_token_stride, int64_t out_head_stride,
+                                 int64_t tree, int64_t heads, float scale, void *workspace, size_t ws_bytes,
+                                 void *stream);
+
+/*
+ * tq_kv_commit -- after drafted tokens were accepted: their records move down
+ * to where the sequence continues.  path[b][0..] are the accepted tokens of
+ * sequence b in order, indices among its drafted tokens, increasing; the
+ * branch ends at `steps` or at the first entry that is not above the one
+ * before it (-1 by custom).  Record lens[b] + path[b][i] moves to place
+ * lens[b] + i, for keys and values of all heads and of `layers` layers whose
+ * pools lie code_layer_stride / scale_layer_stride elements apart (multiples
+ * of 16 bytes) and share the page table.  lens itself is the caller's to
+ * advance.  Records behind the branch keep what they hold.
+ */
+TQ_API tq_status tq_kv_commit(const tq_kv_cache *cache, int64_t layers, int64_t code_layer_stride,
+                              int64_t scale_layer_stride, const int32_t *lens, const int32_t *path, int64_t path_ld,
+                              int64_t steps, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
