@@ -9,8 +9,10 @@
 // token costs a table lookup and a scale per element.  The softmax runs in
 // one pass over the tokens with a running maximum and sum (both fp32).
 //
-// attend_kernel (mma.sync, tiles of 8 or 16 rows).  One CTA per SM; every
-// warp takes groups of 16 tokens on its own:
+// attend_kernel (mma.sync, tiles of 8 or 16 rows).  The groups of 16 tokens of
+// all units are cut into equal ranges, one per warp, and a warp works alone: no
+// barrier, no exchange but shuffles, so that one warp's wait for a unit's first
+// loads is hidden by the others.  Per group:
 //   S^T [16 tokens x 8 rows] = K [16 x D] q^T      (tokens on the M side, so
 //   O^T [D x 8 rows] += V^T [D x 16] P^T            no row of the product is padding)
 // A byte of codes (two elements) is turned into a pair of fp16 centroids by one
@@ -22,9 +24,15 @@
 // words are merged before the lookup (two operations per 8 codes).
 // Roundings to fp16: centroid (2^-12 relative), centroid x scale, rotated
 // query (as in the products of this library), and the softmax weights, which
-// are scaled by 2^14 so that weights down to 2^-38 of the largest survive.
+// are scaled by 2^7.  The maximum they refer to is followed only when it grows
+// by more than 2^8 (rescaling the accumulators is the exception), so a weight
+// is at most 2^15, and weights down to 2^-31 of the largest survive.
 #include "tq_device.cuh"
 #include "tq_internal.h"
+
+#include <math.h>
+
+#include <type_traits>
 
 namespace tq {
 
@@ -33,8 +41,9 @@ namespace {
 constexpr int kGroup = 16;               // tokens of a group
 constexpr uint32_t kLutBase = 0x10000u;  // shared-memory address of the centroid table
 constexpr uint32_t kLutStep = 256;       // bytes between its rows (128 used)
-constexpr float kWeightExp = 14.0f;      // softmax weights are held times 2^14
-constexpr int kSmemLimit = 227 * 1024;
+constexpr float kWeightExp = 7.0f;       // softmax weights are held times 2^7
+constexpr float kLazy = 8.0f;            // log2 by which a maximum may grow before it is followed
+constexpr int kLeastGroups = 4;          // groups of a warp's range at least
 
 struct AttnParams {
     KvCache c;
@@ -47,11 +56,12 @@ struct AttnParams {
     int tree, heads, group_heads;  // query heads per key/value head
     int rows, row_tiles;           // rows of a (sequence, head), tiles of them
     int qdtype;
-    float scale_log2;
+    float scale_log2;  // |scale| log2(e): maxima are taken of the scores before it
+    int negative;      // the scale is negative: the queries' sign is turned
     int *prefix;     // [batch + 1] groups before each sequence
     float *part_ml;  // [slots][rows of a tile][2]: maximum, sum
     float *part_o;   // [slots][rows of a tile][head_dim]
-    int grid;
+    int workers;  // warps of the launch
 };
 
 // Tokens that sequence b attends over, drafted ones included, within its table.
@@ -61,11 +71,11 @@ __device__ __forceinline__ int seq_tokens(const AttnParams &P, int len) {
     return (int)(n < cap ? n : cap);
 }
 
-// The split of W groups over the CTAs: CTA i takes [i W / g, (i + 1) W / g)
-// with g CTAs at work, at least `least` groups each.
-__device__ __forceinline__ int cta_count(int64_t W, int grid, int least) {
-    const int64_t g = (W + least - 1) / least;
-    return (int)(g < grid ? (g < 1 ? 1 : g) : grid);
+// The split of W groups over warps: of n warps at work, warp i takes
+// [i W / n, (i + 1) W / n), kLeastGroups groups or more.
+__device__ __forceinline__ int worker_count(int64_t W, int most) {
+    const int64_t n = (W + kLeastGroups - 1) / kLeastGroups;
+    return (int)(n < most ? n : most);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -112,147 +122,214 @@ __device__ __forceinline__ void fill_lut(int tid, int threads) {
     }
 }
 
-// Which drafted tokens each drafted token sees: itself and its ancestors, a
-// 64-bit word per token, 0 for a token that is not there (a parent that is
-// neither -1 nor an earlier token, its own or an ancestor's).  One warp, six
-// rounds of pointer doubling; `ptr` is scratch for 64 ints.
-__device__ __forceinline__ void ancestor_words(const AttnParams &P, int b, uint64_t *word, int *ptr, int lane) {
-#pragma unroll
-    for (int i = lane; i < kAttnMaxTree; i += 32) {
-        int par = i - 1;
-        if (i >= P.tree) par = -2;
-        else if (P.parents) par = P.parents[b * P.parents_ld + i];
-        ptr[i] = par < -1 || par >= i ? -2 : par;
-        word[i] = 1ull << i;
-    }
-    __syncwarp();
-    for (int hop = 1; hop < kAttnMaxTree; hop <<= 1) {
-        uint64_t w[2];
-        int p[2];
+// Which drafted tokens each drafted token sees, held by a warp: lane l has the
+// words of tokens l and l + 32.  A word is the token itself and its ancestors,
+// or 0 for a token that is not there (a parent that is neither -1 nor an
+// earlier token, its own or an ancestor's).  Six rounds of pointer doubling.
+struct TreeWords {
+    uint64_t w[2];
+    __device__ __forceinline__ TreeWords(const AttnParams &P, int b, int lane) {
+        int ptr[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int i = lane + 32 * k;
-            w[k] = word[i];
-            p[k] = ptr[i];
-            if (p[k] >= 0) {
-                w[k] |= word[p[k]];
-                p[k] = ptr[p[k]];
+            w[k] = i < P.tree ? (2ull << i) - 1 : 0;  // a chain
+            ptr[k] = -1;
+            if (P.parents && i < P.tree) {
+                const int par = P.parents[b * P.parents_ld + i];
+                ptr[k] = par < -1 || par >= i ? -2 : par;
+                w[k] = 1ull << i;
             }
         }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            word[lane + 32 * k] = w[k];
-            ptr[lane + 32 * k] = p[k];
+        if (!P.parents || P.tree == 1) {
+            if (ptr[0] == -2) w[0] = 0;
+            return;
         }
-        __syncwarp();
+        for (int hop = 1; hop < P.tree; hop <<= 1) {
+            uint64_t nw[2];
+            int np[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int from = ptr[k] & 31;
+                const uint64_t a0 = __shfl_sync(kFull, w[0], from), a1 = __shfl_sync(kFull, w[1], from);
+                const int p0 = __shfl_sync(kFull, ptr[0], from), p1 = __shfl_sync(kFull, ptr[1], from);
+                nw[k] = w[k];
+                np[k] = ptr[k];
+                if (ptr[k] >= 0) {
+                    nw[k] |= ptr[k] >= 32 ? a1 : a0;
+                    np[k] = ptr[k] >= 32 ? p1 : p0;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                w[k] = nw[k];
+                ptr[k] = np[k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (ptr[k] == -2) w[k] = 0;
     }
-#pragma unroll
-    for (int i = lane; i < kAttnMaxTree; i += 32)
-        if (ptr[i] == -2) word[i] = 0;
-    __syncwarp();
-}
-
-// One row's rotated query, fp16, into dst[0 .. DP): lane l holds elements
-// 4l .. 4l+3 of each 128; columns past the head dimension and rows past the
-// tile are zero.
-template <int DT, int DP>
-__device__ __forceinline__ void rotate_query(const AttnParams &P, const char *x, bool valid, uint32_t *dst, int lane) {
-#pragma unroll
-    for (int sb = 0; sb < (DP + 127) / 128; ++sb) {
-        const int e = sb * 128 + 4 * lane;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (valid && e < P.c.head_dim) load4<DT>(x + (int64_t)e * ElemSize<DT>::value, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = flip(v[i], sign_mask(e + i));
-        fwht32_warp(v, lane & 7);
-        __half2 a = __floats2half2_rn(v[0] * 0.03125f, v[1] * 0.03125f);
-        __half2 c = __floats2half2_rn(v[2] * 0.03125f, v[3] * 0.03125f);
-        if (e < DP)
-            *reinterpret_cast<uint2 *>(dst + e / 2) =
-                make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&c));
+    // word of token t (any per lane)
+    __device__ __forceinline__ uint64_t of(int t) const {
+        const uint64_t a0 = __shfl_sync(kFull, w[0], t & 31), a1 = __shfl_sync(kFull, w[1], t & 31);
+        return t >= 32 ? a1 : a0;
     }
-}
-
-// What a lane holds of one group of 16 tokens.
-template <int DP>
-struct GroupRegs {
-    static constexpr int KW = DP / 32;  // code words of a key row (DP / 4 elements)
-    static constexpr int KD = DP / 64;  // its half-block scales
-    static constexpr int VW = DP / 64;  // code words of a value row (DP / 8 elements)
-    static constexpr int VD = DP < 256 ? 1 : 2;
-    uint32_t k[2][KW];
-    uint32_t kd[2][(KD + 1) / 2];
-    uint32_t v[4][VW];
-    uint32_t vd[4];
+    // bit t: token t is there
+    __device__ __forceinline__ uint64_t present() const {
+        return (uint64_t)__ballot_sync(kFull, w[0] != 0) | ((uint64_t)__ballot_sync(kFull, w[1] != 0) << 32);
+    }
 };
 
-// Key rows of a lane (l = 4 g + c): tokens 4 (g / 2) + g % 2 and that + 2,
-// elements DP/4 * c ...; value rows: tokens 4 c .. 4 c + 3, elements DP/8 * g ...
-// This is the order in which S^T's accumulator, transposed by movmatrix, is
-// the weights operand of the second product.
+// The rotated query as operand fragments, straight from memory: lane
+// l = 4 g + c owns row g, elements DP/4 c .. of it, which for a head dimension
+// of 128 is one whole block (of 64: half of one, the other half at lane ^ 1),
+// so that the transform runs in registers.  `x` is the lane's row.
+template <int DT, int DP>
+__device__ __forceinline__ void rotate_query(const AttnParams &P, const char *x, bool valid, int c,
+                                             uint32_t (&qf)[DP / 16][2]) {
+    constexpr int N = DP / 4 < 32 ? 16 : 32;  // elements of a block that the lane holds
+    const float f = P.negative ? -0.03125f : 0.03125f;
+#pragma unroll
+    for (int blk = 0; blk < DP / 4 / N; ++blk) {
+        const int e0 = c * (DP / 4) + blk * N;
+        float v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.f;
+        if (valid && e0 < P.c.head_dim) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                float t[4];
+                load4<DT>(x + (int64_t)(e0 + i) * ElemSize<DT>::value, t);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[i + k] = flip(t[k], sign_mask(e0 + i + k));
+            }
+        }
+#pragma unroll
+        for (int h = 1; h < N; h <<= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if ((i & h) == 0) {
+                    const float a = v[i], b = v[i + h];
+                    v[i] = a + b;
+                    v[i + h] = a - b;
+                }
+        if (N == 16) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = butterfly_xlane(v[i], 1, c & 1);
+        }
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const __half2 h = __floats2half2_rn(v[i] * f, v[i + 1] * f);
+            qf[(blk * N + i) / 4][(i / 2) & 1] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+}
+
+// What a lane (l = 4 g + c) holds of a group of 16 tokens.  Key rows: tokens
+// 4 (g / 2) + g % 2 and that + 2, elements DP/4 * c ...; value rows: tokens
+// 4 c .. 4 c + 3, elements DP/8 * g ...  This is the order in which S^T's
+// accumulator, transposed by movmatrix, is the weights operand of the second
+// product.
 template <int DP>
-__device__ __forceinline__ void load_group(const AttnParams &P, int64_t page, int head, int row0, int lane,
-                                           GroupRegs<DP> &r) {
-    using R = GroupRegs<DP>;
-    const int g = lane >> 2, c = lane & 3, D = P.c.head_dim;
-    const int64_t krec = ((page * 2 * P.c.kv_heads + head) << P.c.page_shift) + row0;
-    const int64_t vrec = krec + ((int64_t)P.c.kv_heads << P.c.page_shift);
+struct KeyRegs {
+    static constexpr int W = DP / 32;  // code words of a row (DP / 4 elements)
+    static constexpr int D = DP / 64;  // its half-block scales
+    uint32_t w[2][W];
+    uint32_t d[2][(D + 1) / 2];
+};
+template <int DP>
+struct ValueRegs {
+    static constexpr int W = DP / 64;  // code words of a row (DP / 8 elements)
+    static constexpr int H = DP < 256 ? 1 : 2;
+    uint32_t w[4][W];
+    uint32_t d[4];  // one or two half-block scales
+};
+
+// Where this lane's rows begin within a group, in bytes of the codes and in
+// scales; with FULL the head dimension is DP itself and no piece is missing.
+template <int DP, bool FULL>
+struct LaneOffsets {
+    int dim, kc, ks, vc, vs;
+    __device__ __forceinline__ LaneOffsets(int head_dim, int lane) {
+        const int g = lane >> 2, c = lane & 3;
+        dim = FULL ? DP : head_dim;
+        const int row = 4 * (g >> 1) + (g & 1);
+        kc = row * (dim / 2) + c * (DP / 8);
+        ks = row * (dim / 16) + c * (DP / 64);
+        vc = 4 * c * (dim / 2) + g * (DP / 16);
+        vs = 4 * c * (dim / 16) + g * (DP / 8) / 16;
+    }
+};
+
+template <int DP, bool FULL>
+__device__ __forceinline__ void load_keys(const uint8_t *codes, const uint16_t *scales,
+                                          const LaneOffsets<DP, FULL> &o, int c, KeyRegs<DP> &r) {
+    const int dim = FULL ? DP : o.dim;
+    codes += o.kc;
+    scales += o.ks;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int64_t rec = krec + 4 * (g >> 1) + (g & 1) + 2 * i;
-        const uint8_t *codes = P.c.codes + rec * (D / 2) + c * (DP / 8);
-        const uint16_t *scales = P.c.scales + rec * (D / 16) + c * R::KD;
+        const uint8_t *cp = codes + i * dim;          // two rows on
+        const uint16_t *sp = scales + i * (dim / 8);
         if constexpr (DP == 64) {
             uint2 w = make_uint2(0u, 0u);
-            r.kd[i][0] = 0;
-            if (16 * c < D) {
-                w = __ldg(reinterpret_cast<const uint2 *>(codes));
-                r.kd[i][0] = __ldg(scales);
+            uint32_t d = 0;
+            if (FULL || 16 * c < dim) {
+                w = __ldg(reinterpret_cast<const uint2 *>(cp));
+                d = __ldg(sp);
             }
-            r.k[i][0] = w.x;
-            r.k[i][1] = w.y;
+            r.w[i][0] = w.x;
+            r.w[i][1] = w.y;
+            r.d[i][0] = d;
         } else {
 #pragma unroll
             for (int j = 0; j < DP / 128; ++j) {
                 uint4 w = make_uint4(0u, 0u, 0u, 0u);
                 uint32_t d = 0;
-                if (c * (DP / 4) + 32 * j < D) {
-                    w = __ldg(reinterpret_cast<const uint4 *>(codes) + j);
-                    d = __ldg(reinterpret_cast<const uint32_t *>(scales) + j);
+                if (FULL || c * (DP / 4) + 32 * j < dim) {
+                    w = __ldg(reinterpret_cast<const uint4 *>(cp) + j);
+                    d = __ldg(reinterpret_cast<const uint32_t *>(sp) + j);
                 }
-                r.k[i][4 * j] = w.x;
-                r.k[i][4 * j + 1] = w.y;
-                r.k[i][4 * j + 2] = w.z;
-                r.k[i][4 * j + 3] = w.w;
-                r.kd[i][j] = d;
+                r.w[i][4 * j] = w.x;
+                r.w[i][4 * j + 1] = w.y;
+                r.w[i][4 * j + 2] = w.z;
+                r.w[i][4 * j + 3] = w.w;
+                r.d[i][j] = d;
             }
         }
     }
+}
+
+template <int DP, bool FULL>
+__device__ __forceinline__ void load_values(const uint8_t *codes, const uint16_t *scales,
+                                            const LaneOffsets<DP, FULL> &o, int g, ValueRegs<DP> &r) {
+    const int dim = FULL ? DP : o.dim;
+    codes += o.vc;
+    scales += o.vs;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        const int64_t rec = vrec + 4 * c + t;
-        const uint8_t *codes = P.c.codes + rec * (D / 2) + g * (DP / 16);
-        const uint16_t *scales = P.c.scales + rec * (D / 16) + (g * (DP / 8)) / 16;
-        r.vd[t] = 0;
+        const uint8_t *cp = codes + t * (dim / 2);
+        const uint16_t *sp = scales + t * (dim / 16);
+        r.d[t] = 0;
 #pragma unroll
-        for (int j = 0; j < R::VW; ++j) r.v[t][j] = 0;
-        if (g * (DP / 8) < D) {
+        for (int j = 0; j < ValueRegs<DP>::W; ++j) r.w[t][j] = 0;
+        if (FULL || g * (DP / 8) < dim) {
             if constexpr (DP == 64) {
-                r.v[t][0] = __ldg(reinterpret_cast<const uint32_t *>(codes));
-                r.vd[t] = __ldg(scales);
+                r.w[t][0] = __ldg(reinterpret_cast<const uint32_t *>(cp));
+                r.d[t] = __ldg(sp);
             } else if constexpr (DP == 128) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(codes));
-                r.v[t][0] = w.x;
-                r.v[t][1] = w.y;
-                r.vd[t] = __ldg(scales);
+                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(cp));
+                r.w[t][0] = w.x;
+                r.w[t][1] = w.y;
+                r.d[t] = __ldg(sp);
             } else {
-                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(codes));
-                r.v[t][0] = w.x;
-                r.v[t][1] = w.y;
-                r.v[t][2] = w.z;
-                r.v[t][3] = w.w;
-                r.vd[t] = __ldg(reinterpret_cast<const uint32_t *>(scales));
+                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(cp));
+                r.w[t][0] = w.x;
+                r.w[t][1] = w.y;
+                r.w[t][2] = w.z;
+                r.w[t][3] = w.w;
+                r.d[t] = __ldg(reinterpret_cast<const uint32_t *>(sp));
             }
         }
     }
@@ -260,72 +337,122 @@ __device__ __forceinline__ void load_group(const AttnParams &P, int64_t page, in
 
 __device__ __forceinline__ uint32_t dup_half(uint32_t d, bool high) { return prmt(d, d, high ? 0x3232u : 0x1010u); }
 
+// Running state of a warp's rows: row 2c + k of each tile of 8.  A row without
+// a token so far has the finite maximum kNoMax and the sum 0.
+constexpr float kNoMax = -1e30f;
 template <int DP, int NT>
 struct AttnState {
     float o[NT][DP / 16][4];
     float m[NT][2], l[NT][2];
 };
 
-// One group: scores, mask, running softmax, weighted values.  `tail`: some of
-// its tokens are drafted, past the end, or without a page.
+constexpr int kStepGroups = 2;  // groups of a warp's step
+
+// Scores of a group against the rotated queries: s[n] = K q^T.
 template <int DP, int NT>
-__device__ __forceinline__ void attend_group(const AttnParams &P, const GroupRegs<DP> &r, const uint32_t (&qf)[NT][DP / 16][2],
-                                             AttnState<DP, NT> &st, uint32_t lane_base, int lane, bool tail,
-                                             bool has_page, int token0, int len, const uint64_t (&see)[NT][2],
-                                             const uint64_t *word) {
-    const int g = lane >> 2, c = lane & 3;
-    float s[NT][2][4];  // two accumulators, for shorter chains of products
+__device__ __forceinline__ void group_scores(const KeyRegs<DP> &r, const uint32_t (&qf)[NT][DP / 16][2],
+                                             float (&s)[NT][4], uint32_t lane_base) {
+    uint32_t kd[2] = {0u, 0u};
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[n][0][i] = s[n][1][i] = 0.f;
-    uint32_t kd[2] = {0u, 0u};
+        for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {  // 16 elements: bytes 2i and 2i + 1 of the lane's codes
         if (i % 4 == 0) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) kd[h] = dup_half(r.kd[h][i / 8], (i / 4) & 1);
+            for (int h = 0; h < 2; ++h) kd[h] = dup_half(r.d[h][i / 8], (i / 4) & 1);
         }
         uint32_t a[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t w = r.k[h][i / 2];
+            const uint32_t w = r.w[h][i / 2];
             a[h] = hmul2((i & 1) ? lut_pair<2>(w, lane_base) : lut_pair<0>(w, lane_base), kd[h]);
             a[2 + h] = hmul2((i & 1) ? lut_pair<3>(w, lane_base) : lut_pair<1>(w, lane_base), kd[h]);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816(s[n][i & 1], a[0], a[1], a[2], a[3], qf[n][i][0], qf[n][i][1]);
+        for (int n = 0; n < NT; ++n) mma16816(s[n], a[0], a[1], a[2], a[3], qf[n][i][0], qf[n][i][1]);
     }
+}
 
+// O^T += V^T P^T of a group.
+template <int DP, int NT>
+__device__ __forceinline__ void group_values(const ValueRegs<DP> &r, const uint32_t (&pb)[NT][2],
+                                             AttnState<DP, NT> &st, uint32_t lane_base) {
+#pragma unroll
+    for (int half = 0; half < ValueRegs<DP>::H; ++half) {
+        const uint32_t d01 = prmt(r.d[0], r.d[1], half ? 0x7632u : 0x5410u);
+        const uint32_t d23 = prmt(r.d[2], r.d[3], half ? 0x7632u : 0x5410u);
+        constexpr int kWords = ValueRegs<DP>::W / ValueRegs<DP>::H;
+#pragma unroll
+        for (int jj = 0; jj < kWords; ++jj) {
+            const int j = half * kWords + jj;
+            // byte b: element 2b (or 2b + 1) of two tokens
+            const uint32_t e01 = (r.w[0][j] & 0x0F0F0F0Fu) | ((r.w[1][j] << 4) & 0xF0F0F0F0u);
+            const uint32_t f01 = ((r.w[0][j] >> 4) & 0x0F0F0F0Fu) | (r.w[1][j] & 0xF0F0F0F0u);
+            const uint32_t e23 = (r.w[2][j] & 0x0F0F0F0Fu) | ((r.w[3][j] << 4) & 0xF0F0F0F0u);
+            const uint32_t f23 = ((r.w[2][j] >> 4) & 0x0F0F0F0Fu) | (r.w[3][j] & 0xF0F0F0F0u);
+            auto product = [&](auto byte) {
+                constexpr int B = decltype(byte)::value;
+                const uint32_t a0 = hmul2(lut_pair<B>(e01, lane_base), d01);
+                const uint32_t a1 = hmul2(lut_pair<B>(f01, lane_base), d01);
+                const uint32_t a2 = hmul2(lut_pair<B>(e23, lane_base), d23);
+                const uint32_t a3 = hmul2(lut_pair<B>(f23, lane_base), d23);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(st.o[n][4 * j + B], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            };
+            product(std::integral_constant<int, 0>());
+            product(std::integral_constant<int, 1>());
+            product(std::integral_constant<int, 2>());
+            product(std::integral_constant<int, 3>());
+        }
+    }
+}
+
+// Softmax weights of a step's groups under the running maximum, as operands of
+// the second product.  TAIL: some tokens are drafted, past the end or without
+// a page, and each score is checked; otherwise every token counts.
+template <int DP, int NT, bool TAIL>
+__device__ __forceinline__ void step_weights(const AttnParams &P, float (&s)[kStepGroups][NT][4],
+                                             AttnState<DP, NT> &st, uint32_t (&pb)[kStepGroups][NT][2], int lane,
+                                             int token0, int len, const int (&page)[kStepGroups],
+                                             const uint64_t (&see)[NT][2]) {
+    const int g = lane >> 2;
     const int tok = 4 * (g >> 1) + (g & 1);  // this lane's score rows: tok, tok + 2
-    uint32_t pb[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        float x[4];
+        uint32_t ok = ~0u;
+        if (TAIL) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (s[n][0][i] + s[n][1][i]) * P.scale_log2;
-        if (tail) {
+            for (int q = 0; q < kStepGroups; ++q)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = token0 + tok + 2 * (i >> 1) - len;
-                const bool ok = has_page && (j < 0 || (j < P.tree && ((see[n][i & 1] >> j) & 1ull)));
-                if (!ok) x[i] = -INFINITY;
-            }
+                for (int i = 0; i < 4; ++i) {
+                    const int j = token0 + q * kGroup + tok + 2 * (i >> 1) - len;
+                    const bool sees = page[q] >= 0 && (j < 0 || (j < P.tree && ((see[n][i & 1] >> j) & 1ull)));
+                    if (!sees) {
+                        ok &= ~(1u << (4 * q + i));
+                        s[q][n][i] = kNoMax;
+                    }
+                }
         }
-        float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+        float mx[2];
 #pragma unroll
-        for (int k = 4; k <= 16; k <<= 1) {
-            mx[0] = fmaxf(mx[0], __shfl_xor_sync(kFull, mx[0], k));
-            mx[1] = fmaxf(mx[1], __shfl_xor_sync(kFull, mx[1], k));
+        for (int k = 0; k < 2; ++k) {
+            mx[k] = st.m[n][k];
+#pragma unroll
+            for (int q = 0; q < kStepGroups; ++q) mx[k] = fmaxf(mx[k], fmaxf(s[q][n][k], s[q][n][k + 2]));
         }
-        const bool grows = mx[0] > st.m[n][0] || mx[1] > st.m[n][1];
-        if (__any_sync(kFull, grows)) {
+#pragma unroll
+        for (int x = 4; x <= 16; x <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(kFull, mx[0], x));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(kFull, mx[1], x));
+        }
+        if (__any_sync(kFull, (mx[0] - st.m[n][0]) * P.scale_log2 > kLazy ||
+                                  (mx[1] - st.m[n][1]) * P.scale_log2 > kLazy)) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float nm = fmaxf(st.m[n][k], mx[k]);
-                // rows without any token so far have nothing to rescale
-                const float f = st.m[n][k] == -INFINITY ? 0.f : ex2(st.m[n][k] - nm);
-                st.m[n][k] = nm;
+                const float f = ex2((st.m[n][k] - mx[k]) * P.scale_log2);
+                st.m[n][k] = mx[k];
                 st.l[n][k] *= f;
 #pragma unroll
                 for (int i = 0; i < DP / 16; ++i) {
@@ -334,92 +461,24 @@ __device__ __forceinline__ void attend_group(const AttnParams &P, const GroupReg
                 }
             }
         }
-        float p[4];
+        const float base[2] = {kWeightExp - st.m[n][0] * P.scale_log2, kWeightExp - st.m[n][1] * P.scale_log2};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float m = st.m[n][i & 1];
-            p[i] = m == -INFINITY ? 0.f : ex2(x[i] - (m - kWeightExp));
-        }
-        st.l[n][0] += p[0] + p[2];
-        st.l[n][1] += p[1] + p[3];
+        for (int q = 0; q < kStepGroups; ++q) {
+            float p[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const __half2 h = __floats2half2_rn(p[2 * k], p[2 * k + 1]);
-            pb[n][k] = movmatrix(*reinterpret_cast<const uint32_t *>(&h));
-        }
-    }
-
-    // scales of the lane's four value rows; a row that no query sees counts as
-    // zero whatever the memory holds
-    uint32_t vd[4];
+            for (int i = 0; i < 4; ++i) {
+                p[i] = ex2(fmaf(s[q][n][i], P.scale_log2, base[i & 1]));
+                if (TAIL && !((ok >> (4 * q + i)) & 1u)) p[i] = 0.f;
+            }
+            st.l[n][0] += p[0] + p[2];
+            st.l[n][1] += p[1] + p[3];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        vd[t] = r.vd[t];
-        if (tail) {
-            const int j = token0 + 4 * c + t - len;
-            const bool there = has_page && (j < 0 || (j < P.tree && word[j] != 0));
-            if (!there) vd[t] = 0;
-        }
-    }
-#pragma unroll
-    for (int half = 0; half < GroupRegs<DP>::VD; ++half) {
-        const uint32_t d01 = prmt(vd[0], vd[1], half ? 0x7632u : 0x5410u);
-        const uint32_t d23 = prmt(vd[2], vd[3], half ? 0x7632u : 0x5410u);
-        constexpr int kWords = GroupRegs<DP>::VW / GroupRegs<DP>::VD;
-#pragma unroll
-        for (int jj = 0; jj < kWords; ++jj) {
-            const int j = half * kWords + jj;
-            // byte b: element 2b (or 2b + 1) of two tokens
-            const uint32_t e01 = (r.v[0][j] & 0x0F0F0F0Fu) | ((r.v[1][j] << 4) & 0xF0F0F0F0u);
-            const uint32_t f01 = ((r.v[0][j] >> 4) & 0x0F0F0F0Fu) | (r.v[1][j] & 0xF0F0F0F0u);
-            const uint32_t e23 = (r.v[2][j] & 0x0F0F0F0Fu) | ((r.v[3][j] << 4) & 0xF0F0F0F0u);
-            const uint32_t f23 = ((r.v[2][j] >> 4) & 0x0F0F0F0Fu) | (r.v[3][j] & 0xF0F0F0F0u);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                uint32_t a[4];
-                if (b == 0) {
-                    a[0] = lut_pair<0>(e01, lane_base); a[1] = lut_pair<0>(f01, lane_base);
-                    a[2] = lut_pair<0>(e23, lane_base); a[3] = lut_pair<0>(f23, lane_base);
-                } else if (b == 1) {
-                    a[0] = lut_pair<1>(e01, lane_base); a[1] = lut_pair<1>(f01, lane_base);
-                    a[2] = lut_pair<1>(e23, lane_base); a[3] = lut_pair<1>(f23, lane_base);
-                } else if (b == 2) {
-                    a[0] = lut_pair<2>(e01, lane_base); a[1] = lut_pair<2>(f01, lane_base);
-                    a[2] = lut_pair<2>(e23, lane_base); a[3] = lut_pair<2>(f23, lane_base);
-                } else {
-                    a[0] = lut_pair<3>(e01, lane_base); a[1] = lut_pair<3>(f01, lane_base);
-                    a[2] = lut_pair<3>(e23, lane_base); a[3] = lut_pair<3>(f23, lane_base);
-                }
-                a[0] = hmul2(a[0], d01);
-                a[1] = hmul2(a[1], d01);
-                a[2] = hmul2(a[2], d23);
-                a[3] = hmul2(a[3], d23);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    mma16816(st.o[n][4 * j + b], a[0], a[1], a[2], a[3], pb[n][0], pb[n][1]);
+            for (int k = 0; k < 2; ++k) {
+                const __half2 h = __floats2half2_rn(p[2 * k], p[2 * k + 1]);
+                pb[q][n][k] = movmatrix(*reinterpret_cast<const uint32_t *>(&h));
             }
         }
     }
-}
-
-// Shared memory below the table: prefix sums, ancestor words, the rotated
-// queries, the warps' maxima and sums; above it the warps' partial results.
-constexpr uint32_t kLowBytes = 60 * 1024;
-
-template <int DP, int NT>
-struct AttnShared {
-    static constexpr int kRowWords = DP / 2 + 4;  // a query row, padded against bank conflicts
-    int prefix[kAttnMaxBatch + 1];
-    int scan[32];
-    uint64_t word[kAttnMaxTree];
-    int ptr[kAttnMaxTree];
-    uint32_t q[NT * 8 * kRowWords];
-    float m[16][NT * 8], l[16][NT * 8];
-};
-
-template <int DP, int NT, int WARPS>
-constexpr int attn_smem() {
-    return (int)(kLutBase + 256 * kLutStep) + WARPS * 8 * (DP + 4) * 4;
 }
 
 // Exclusive prefix of the sequences' groups into `prefix`, by the whole CTA.
@@ -448,15 +507,19 @@ __device__ __forceinline__ void scan_sequences(const AttnParams &P, int *prefix,
     __syncthreads();
 }
 
-template <int DP, int NT, int WARPS>
+// Shared memory: prefix sums below the table, which starts at kLutBase and
+// ends at kLutBase + 64 KB.
+struct AttnShared {
+    int prefix[kAttnMaxBatch + 1];
+    int scan[32];
+};
+constexpr int kAttnSmem = (int)(kLutBase + 256 * kLutStep);
+static_assert(sizeof(AttnShared) + 4096 <= kLutBase, "shared memory below the table");
+
+template <int DP, int NT, int WARPS, bool FULL>
 __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams P) {
-    using S = AttnShared<DP, NT>;
-    static_assert(sizeof(S) <= kLowBytes, "shared memory below the table");
     extern __shared__ char smem[];
-    S &sh = *reinterpret_cast<S *>(smem);
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
-    float *red = reinterpret_cast<float *>(smem + (kLutBase + 256 * kLutStep - base));
-    constexpr int kRedRow = DP + 4;
+    AttnShared &sh = *reinterpret_cast<AttnShared *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
     grid_dependents_launch();  // the joining launch may take its place; it waits for this one's end
@@ -470,10 +533,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
     const int64_t W = (int64_t)sh.prefix[P.c.batch] * per_seq;
     if (blockIdx.x == 0)
         for (int i = tid; i <= P.c.batch; i += WARPS * 32) P.prefix[i] = sh.prefix[i];
-    const int ctas = cta_count(W, P.grid, WARPS);
-    if (blockIdx.x >= ctas) return;
-    int64_t at = W * blockIdx.x / ctas;
-    const int64_t end = W * (blockIdx.x + 1) / ctas;
+    // the first warps of all CTAs come first, so that a few ranges spread over the SMs
+    const int workers = worker_count(W, P.workers);
+    const int me = warp * gridDim.x + blockIdx.x;
+    if (me >= workers) return;
+    const LaneOffsets<DP, FULL> off(P.c.head_dim, lane);
+    int64_t at = W * me / workers;
+    const int64_t end = W * (me + 1) / workers;
 
     while (at < end) {
         // the unit that holds group `at`
@@ -489,60 +555,71 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
         const int head = hr / P.row_tiles, row0 = (hr % P.row_tiles) * NT * 8;
         const int ga = (int)(in_seq - (int64_t)hr * groups);
         const int gb = (int)min((int64_t)groups, ga + (end - at));
-        const int len = min(max(P.lens[b], 0), (int)min((int64_t)INT32_MAX, (int64_t)P.c.pages_per_seq << P.c.page_shift));
+        const int len = min(max(P.lens[b], 0), P.c.pages_per_seq << P.c.page_shift);
 
         // first loads before the query is rotated
         const int32_t *table = P.c.page_table + b * P.c.table_ld;
         const int shift = P.c.page_shift - 4;  // groups of a page
         const int in_page = (1 << shift) - 1;
-        GroupRegs<DP> next;
-        bool next_page = false;
-        auto fetch = [&](int grp) {
-            const int64_t page = table[grp >> shift];
-            next_page = page >= 0 && page < P.c.pages;
-            if (next_page) load_group<DP>(P, page, head, (grp & in_page) * kGroup, lane, next);
-            else next = GroupRegs<DP>();
+        const int64_t v_rows = (int64_t)P.c.kv_heads << P.c.page_shift;  // from a key record to its value record
+        KeyRegs<DP> kr[kStepGroups];
+        ValueRegs<DP> vr[kStepGroups];
+        auto pages_of = [&](int grp, int (&page)[kStepGroups]) {
+#pragma unroll
+            for (int q = 0; q < kStepGroups; ++q) {
+                page[q] = grp + q < gb ? table[(grp + q) >> shift] : -1;
+                if (page[q] >= P.c.pages) page[q] = -1;
+            }
         };
-        int grp = ga + warp;
-        if (grp < gb) fetch(grp);
-
-        if (warp == WARPS - 1) ancestor_words(P, b, sh.word, sh.ptr, lane);
-        for (int r = warp; r < NT * 8; r += WARPS) {
-            const int row = row0 + r;
-            const int t = row / P.group_heads, h = head * P.group_heads + row % P.group_heads;
-            const bool valid = row < P.rows;
-            const int64_t off = b * P.q_batch + t * P.q_token + h * P.q_head;
-            uint32_t *dst = sh.q + r * S::kRowWords;
-            if (P.qdtype == kF32) rotate_query<kF32, DP>(P, P.q + off * 4, valid, dst, lane);
-            else if (P.qdtype == kBF16) rotate_query<kBF16, DP>(P, P.q + off * 2, valid, dst, lane);
-            else rotate_query<kF16, DP>(P, P.q + off * 2, valid, dst, lane);
+        auto record = [&](int page, int grp) {
+            return (((int64_t)page * 2 * P.c.kv_heads + head) << P.c.page_shift) + (grp & in_page) * kGroup;
+        };
+        auto fetch_keys = [&](const int (&page)[kStepGroups], int grp) {
+#pragma unroll
+            for (int q = 0; q < kStepGroups; ++q) {
+                if (page[q] >= 0) {
+                    const int64_t rec = record(page[q], grp + q);
+                    load_keys<DP, FULL>(P.c.codes + rec * (off.dim / 2), P.c.scales + rec * (off.dim / 16), off, c,
+                                        kr[q]);
+                }
+            }
+        };
+        auto fetch_values = [&](const int (&page)[kStepGroups], int grp) {
+#pragma unroll
+            for (int q = 0; q < kStepGroups; ++q) {
+                if (page[q] >= 0) {
+                    const int64_t rec = record(page[q], grp + q) + v_rows;
+                    load_values<DP, FULL>(P.c.codes + rec * (off.dim / 2), P.c.scales + rec * (off.dim / 16), off, g,
+                                          vr[q]);
+                }
+            }
+        };
+#pragma unroll
+        for (int q = 0; q < kStepGroups; ++q) {
+            kr[q] = KeyRegs<DP>();
+            vr[q] = ValueRegs<DP>();
         }
-        __syncthreads();
+        int grp = ga;
+        int page[kStepGroups], next[kStepGroups];
+        pages_of(grp, page);
+        pages_of(grp + kStepGroups, next);
+        fetch_keys(page, grp);
+        fetch_values(page, grp);
 
-        // query fragments: row g of each tile of 8, this lane's DP / 4 elements
         uint32_t qf[NT][DP / 16][2];
-        uint64_t see[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint32_t *src = sh.q + (8 * n + g) * S::kRowWords + c * (DP / 8);
-#pragma unroll
-            for (int i = 0; i < DP / 16; ++i) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(src + 2 * i);
-                qf[n][i][0] = w.x;
-                qf[n][i][1] = w.y;
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int row = row0 + 8 * n + 2 * c + k;
-                see[n][k] = row < P.rows ? sh.word[row / P.group_heads] : 0;
-            }
-        }
         AttnState<DP, NT> st;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            const int row = row0 + 8 * n + g;
+            const bool valid = row < P.rows;
+            const int t = valid ? row / P.group_heads : 0, h = head * P.group_heads + (valid ? row % P.group_heads : 0);
+            const int64_t x = b * P.q_batch + t * P.q_token + h * P.q_head;
+            if (P.qdtype == kF32) rotate_query<kF32, DP>(P, P.q + x * 4, valid, c, qf[n]);
+            else if (P.qdtype == kBF16) rotate_query<kBF16, DP>(P, P.q + x * 2, valid, c, qf[n]);
+            else rotate_query<kF16, DP>(P, P.q + x * 2, valid, c, qf[n]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                st.m[n][k] = -INFINITY;
+                st.m[n][k] = kNoMax;
                 st.l[n][k] = 0.f;
             }
 #pragma unroll
@@ -550,17 +627,55 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 #pragma unroll
                 for (int k = 0; k < 4; ++k) st.o[n][i][k] = 0.f;
         }
+
+        // keys of the next step load while this step's values are multiplied,
+        // its values while the next step's scores are
         while (grp < gb) {
-            const GroupRegs<DP> cur = next;
-            const bool has_page = next_page;
             const int token0 = grp * kGroup;
-            grp += WARPS;
-            if (grp < gb) fetch(grp);
-            const bool tail = token0 + kGroup > len || !has_page;
-            attend_group<DP, NT>(P, cur, qf, st, lane_base, lane, tail, has_page, token0, len, see, sh.word);
+            bool tail = token0 + kStepGroups * kGroup > len;
+#pragma unroll
+            for (int q = 0; q < kStepGroups; ++q) tail |= page[q] < 0;
+            float s[kStepGroups][NT][4];
+#pragma unroll
+            for (int q = 0; q < kStepGroups; ++q) group_scores<DP, NT>(kr[q], qf, s[q], lane_base);
+            fetch_keys(next, grp + kStepGroups);
+            uint32_t pb[kStepGroups][NT][2];
+            if (tail) {
+                const TreeWords words(P, b, lane);
+                uint64_t see[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int row = row0 + 8 * n + 2 * c + k;
+                        see[n][k] = words.of(min(row / P.group_heads, P.tree - 1));
+                    }
+                const uint64_t present = words.present();
+#pragma unroll
+                for (int q = 0; q < kStepGroups; ++q)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        // a record that no query sees counts as zero whatever the memory holds
+                        const int j = token0 + q * kGroup + 4 * c + t - len;
+                        if (page[q] < 0 || (j >= 0 && (j >= P.tree || !((present >> j) & 1ull)))) vr[q].d[t] = 0;
+                    }
+                step_weights<DP, NT, true>(P, s, st, pb, lane, token0, len, page, see);
+            } else {
+                const uint64_t see[NT][2] = {};
+                step_weights<DP, NT, false>(P, s, st, pb, lane, token0, len, page, see);
+            }
+#pragma unroll
+            for (int q = 0; q < kStepGroups; ++q) group_values<DP, NT>(vr[q], pb[q], st, lane_base);
+            grp += kStepGroups;
+            fetch_values(next, grp);
+#pragma unroll
+            for (int q = 0; q < kStepGroups; ++q) page[q] = next[q];
+            pages_of(grp + kStepGroups, next);
         }
 
-        // the warps' parts joined: maxima and sums first, then the values
+        // this part of the unit: maxima and sums, and DP / 8 neighbouring
+        // elements of two rows for each lane
+        const int64_t slot = (int64_t)b * per_seq + hr + me;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -568,69 +683,32 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
                 float l = st.l[n][k];
 #pragma unroll
                 for (int x = 4; x <= 16; x <<= 1) l += __shfl_xor_sync(kFull, l, x);
-                if (g == 0) {
-                    sh.m[warp][8 * n + 2 * c + k] = st.m[n][k];
-                    sh.l[warp][8 * n + 2 * c + k] = l;
-                }
-            }
-        }
-        __syncthreads();
-        const int64_t unit = (int64_t)b * per_seq + hr;
-        const int64_t slot = unit + blockIdx.x;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
                 const int r = 8 * n + 2 * c + k;
-                float mx = -INFINITY;
+                if (row0 + r < P.rows) {
+                    const int64_t at_row = slot * (NT * 8) + r;
+                    if (g == 0) reinterpret_cast<float2 *>(P.part_ml)[at_row] = make_float2(st.m[n][k], l);
+                    if (FULL || g * (DP / 8) < P.c.head_dim) {
+                        float4 *dst = reinterpret_cast<float4 *>(P.part_o + at_row * off.dim + g * (DP / 8));
 #pragma unroll
-                for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sh.m[w][r]);
-                const float f = st.m[n][k] == -INFINITY ? 0.f : ex2(st.m[n][k] - mx);
-                float *dst = red + (warp * 8 + 2 * c + k) * kRedRow + 2 * g;
-#pragma unroll
-                for (int i = 0; i < DP / 16; ++i)  // elements DP/8 g + 2 i and + 1 at 16 i + 2 g
-                    *reinterpret_cast<float2 *>(dst + 16 * i) = make_float2(st.o[n][i][k] * f, st.o[n][i][k + 2] * f);
-            }
-            __syncthreads();
-            for (int i = tid; i < 8 * DP; i += WARPS * 32) {
-                const int r = i / DP, e = i % DP;
-                const int row = row0 + 8 * n + r;
-                if (row < P.rows && e < P.c.head_dim) {
-                    const float *src = red + r * kRedRow + (e % (DP / 8)) / 2 * 16 + e / (DP / 8) * 2 + (e & 1);
-                    float sum = 0.f;
-#pragma unroll
-                    for (int w = 0; w < WARPS; ++w) sum += src[w * 8 * kRedRow];
-                    P.part_o[(slot * (NT * 8) + 8 * n + r) * P.c.head_dim + e] = sum;
+                        for (int i = 0; i < DP / 16; i += 2)
+                            dst[i / 2] = make_float4(st.o[n][i][k], st.o[n][i][k + 2], st.o[n][i + 1][k],
+                                                     st.o[n][i + 1][k + 2]);
+                    }
                 }
             }
-            if (n + 1 < NT) __syncthreads();
         }
-        for (int r = tid; r < NT * 8; r += WARPS * 32) {
-            if (row0 + r >= P.rows) continue;
-            float mx = -INFINITY, l = 0.f;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sh.m[w][r]);
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w)
-                if (sh.m[w][r] != -INFINITY) l += sh.l[w][r] * ex2(sh.m[w][r] - mx);
-            // a token that is not there answers zero
-            if (sh.word[(row0 + r) / P.group_heads] == 0) mx = -INFINITY, l = 0.f;
-            float2 *ml = reinterpret_cast<float2 *>(P.part_ml) + slot * (NT * 8) + r;
-            *ml = make_float2(mx, l);
-        }
-        __syncthreads();  // the next part overwrites queries, words and partial results
         at += gb - ga;
     }
 }
 
 // ---------------------------------------------------------------------------
 // The parts of each row joined, rotated back, divided and rounded.  One CTA of
-// four warps per row: the warps share the parts, warp 0 adds up and finishes.
+// eight warps per row: the warps share the parts, warp 0 adds up and finishes.
 // ---------------------------------------------------------------------------
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
 
 template <int OT>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P, int tile_rows, int least) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P, int tile_rows) {
     __shared__ float so[kJoinWarps][256];
     __shared__ float sl[kJoinWarps];
     grid_dependency_wait();
@@ -641,16 +719,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     const int tile = row / tile_rows, r = row % tile_rows;
     const int per_seq = P.c.kv_heads * P.row_tiles;
     const int64_t W = (int64_t)P.prefix[P.c.batch] * per_seq;
-    const int ctas = cta_count(W, P.grid, least);
+    const int workers = worker_count(W, P.workers);
     const int hr = head * P.row_tiles + tile;
     const int groups = P.prefix[b + 1] - P.prefix[b];
     const int64_t first = (int64_t)P.prefix[b] * per_seq + (int64_t)hr * groups;
-    // CTA of group x: the largest i with i W / ctas <= x
-    const int64_t i0 = ((first + 1) * ctas - 1) / W, i1 = ((first + groups) * ctas - 1) / W;
+    // the warp of group x: the largest i with i W / workers <= x
+    const int64_t i0 = ((first + 1) * workers - 1) / W, i1 = ((first + groups) * workers - 1) / W;
     const int64_t unit = (int64_t)b * per_seq + hr;
     const float2 *ml = reinterpret_cast<const float2 *>(P.part_ml);
 
-    float mx = -INFINITY;
+    float mx = kNoMax;
     for (int64_t i = i0 + lane; i <= i1; i += 32) mx = fmaxf(mx, ml[(unit + i) * tile_rows + r].x);
 #pragma unroll
     for (int k = 16; k >= 1; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, k));
@@ -660,8 +738,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     for (int64_t i = i0 + warp; i <= i1; i += kJoinWarps) {
         const int64_t s = (unit + i) * tile_rows + r;
         const float2 p = ml[s];
-        if (p.x == -INFINITY) continue;
-        const float f = ex2(p.x - mx);
+        if (p.y == 0.f) continue;  // nothing seen there
+        const float f = ex2((p.x - mx) * P.scale_log2);
         l += f * p.y;
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb) {
@@ -685,8 +763,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     l = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) l += sl[w];
-    const float inv = l > 0.f ? 0.03125f / l : 0.f;
     const int t = row / P.group_heads, h = head * P.group_heads + row % P.group_heads;
+    // a token that is not there answers zero
+    const bool there = (TreeWords(P, b, lane).present() >> t) & 1ull;
+    const float inv = there && l > 0.f ? 0.03125f / l : 0.f;
     char *out = P.out + (b * P.o_batch + t * P.o_token + h * P.o_head) * ElemSize<OT>::value;
 #pragma unroll
     for (int sb = 0; sb < 2; ++sb) {
@@ -719,28 +799,32 @@ AttnPlan plan_attention(int64_t batch, int tree, int heads, int kv_heads, int he
     p.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
     p.rows = tree * (heads / kv_heads);
     p.nt = p.rows > 8 && p.dp <= 128 ? 2 : 1;
-    p.warps = p.nt == 2 || p.dp == 256 ? 8 : 16;
+    p.warps = p.nt == 2 || p.dp == 256 ? 8 : 12;
     p.row_tiles = (p.rows + 8 * p.nt - 1) / (8 * p.nt);
     p.units = batch * kv_heads * p.row_tiles;
     return p;
 }
 
+template <int DP, int NT, int WARPS, bool FULL>
+cudaError_t launch_attend_as(const AttnParams &P, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(attend_kernel<DP, NT, WARPS, FULL>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
+    if (e != cudaSuccess) return e;
+    attend_kernel<DP, NT, WARPS, FULL><<<P.workers / WARPS, WARPS * 32, kAttnSmem, stream>>>(P);
+    return cudaGetLastError();
+}
+
 template <int DP, int NT, int WARPS>
 cudaError_t launch_attend(const AttnParams &P, cudaStream_t stream) {
-    constexpr int bytes = attn_smem<DP, NT, WARPS>();
-    static_assert(bytes <= kSmemLimit, "shared memory per CTA");
-    cudaError_t e = cudaFuncSetAttribute(attend_kernel<DP, NT, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         bytes);
-    if (e != cudaSuccess) return e;
-    attend_kernel<DP, NT, WARPS><<<P.grid, WARPS * 32, bytes, stream>>>(P);
-    return cudaGetLastError();
+    return P.c.head_dim == DP ? launch_attend_as<DP, NT, WARPS, true>(P, stream)
+                              : launch_attend_as<DP, NT, WARPS, false>(P, stream);
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t batch, int tree, int heads, int kv_heads, int head_dim, int sm_count) {
     const AttnPlan p = plan_attention(batch, tree, heads, kv_heads, head_dim);
-    const size_t slots = (size_t)(p.units + sm_count);
+    const size_t slots = (size_t)(p.units + sm_count * p.warps);
     return 256 + round_up((size_t)(batch + 1) * 4, 256) + round_up(slots * 8 * p.nt * 8, 256) +
            slots * 8 * p.nt * head_dim * 4;
 }
@@ -766,9 +850,10 @@ cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t s
     P.rows = plan.rows;
     P.row_tiles = plan.row_tiles;
     P.qdtype = j.qdtype;
-    P.scale_log2 = j.scale * 1.44269504088896340736f;
-    P.grid = sm_count;
-    const size_t slots = (size_t)(plan.units + sm_count);
+    P.scale_log2 = fabsf(j.scale) * 1.44269504088896340736f;
+    P.negative = j.scale < 0.f;
+    P.workers = sm_count * plan.warps;
+    const size_t slots = (size_t)(plan.units + sm_count * plan.warps);
     char *ws = j.workspace + 256;
     P.prefix = reinterpret_cast<int *>(ws);
     ws += round_up((size_t)(j.c.batch + 1) * 4, 256);
@@ -777,8 +862,8 @@ cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t s
     P.part_o = reinterpret_cast<float *>(ws);
 
     cudaError_t e;
-    if (plan.dp == 64) e = plan.nt == 1 ? launch_attend<64, 1, 16>(P, stream) : launch_attend<64, 2, 8>(P, stream);
-    else if (plan.dp == 128) e = plan.nt == 1 ? launch_attend<128, 1, 16>(P, stream) : launch_attend<128, 2, 8>(P, stream);
+    if (plan.dp == 64) e = plan.nt == 1 ? launch_attend<64, 1, 12>(P, stream) : launch_attend<64, 2, 8>(P, stream);
+    else if (plan.dp == 128) e = plan.nt == 1 ? launch_attend<128, 1, 12>(P, stream) : launch_attend<128, 2, 8>(P, stream);
     else e = launch_attend<256, 1, 8>(P, stream);
     if (e != cudaSuccess) return e;
 
@@ -791,10 +876,10 @@ cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t s
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const int tile_rows = 8 * plan.nt, least = plan.warps;
-    if (j.odtype == kF32) return cudaLaunchKernelEx(&cfg, join_kernel<kF32>, P, tile_rows, least);
-    if (j.odtype == kBF16) return cudaLaunchKernelEx(&cfg, join_kernel<kBF16>, P, tile_rows, least);
-    return cudaLaunchKernelEx(&cfg, join_kernel<kF16>, P, tile_rows, least);
+    const int tile_rows = 8 * plan.nt;
+    if (j.odtype == kF32) return cudaLaunchKernelEx(&cfg, join_kernel<kF32>, P, tile_rows);
+    if (j.odtype == kBF16) return cudaLaunchKernelEx(&cfg, join_kernel<kBF16>, P, tile_rows);
+    return cudaLaunchKernelEx(&cfg, join_kernel<kF16>, P, tile_rows);
 }
 
 }  // namespace tq

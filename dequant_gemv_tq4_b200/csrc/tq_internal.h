@@ -251,11 +251,11 @@ struct KvCommitJob {
 cudaError_t launch_kv_commit(const KvCommitJob &job, cudaStream_t stream);
 
 // Attention over the cache (tq_attention.cu).  A unit is (sequence, key/value
-// head, tile of kRows rows); a row is one query head of one drafted token, a
+// head, tile of 8 or 16 rows); a row is one query head of one drafted token, a
 // tile's rows share the head's keys and values.  Units are cut into groups of
-// 16 tokens, and the groups of all units into equal ranges, one per CTA; the
-// part of a unit that one CTA takes leaves a partial result in slot
-// (unit + CTA) of the workspace, and a second launch joins each unit's parts.
+// 16 tokens, and the groups of all units into equal ranges, one per warp; the
+// part of a unit that one warp takes leaves a partial result in slot
+// (unit + warp) of the workspace, and a second launch joins each unit's parts.
 struct AttentionJob {
     KvCache c;
     const int32_t *lens, *parents;

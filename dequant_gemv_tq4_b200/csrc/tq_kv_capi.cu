@@ -228,7 +228,7 @@ tq_status tq_kv_attention(const tq_kv_cache *cache, const int32_t *lens, const i
     if (q_batch_stride % 8 != 0 || out_batch_stride % 8 != 0) return TQ_ERR_ALIGNMENT;
     if ((st = check_heads_operand(q, q_token_stride, q_head_stride)) != TQ_OK) return st;
     if ((st = check_heads_operand(out, out_token_stride, out_head_stride)) != TQ_OK) return st;
-    if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return TQ_ERR_INVALID_ARG;
+    if (!(scale <= TQ_KV_MAX_SCALE && scale >= -TQ_KV_MAX_SCALE)) return TQ_ERR_INVALID_ARG;
     tq::DeviceInfo di;
     if (tq::device_info(&di) != cudaSuccess) return TQ_ERR_CUDA;
     if (!workspace || !aligned(workspace, 256) ||

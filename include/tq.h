@@ -478,6 +478,7 @@ TQ_API tq_status tq_nvfp4_gemm_batch(const tq_nvfp4_gemm_desc *descs, int count,
 #define TQ_KV_MAX_LAYERS 4096
 #define TQ_KV_MAX_TOKENS ((int64_t)1 << 24)
 #define TQ_ROPE_MAX_DIM 1024
+#define TQ_KV_MAX_SCALE 65536.0f
 
 typedef struct {
     uint8_t *codes;            /* device, 16-byte aligned */
@@ -568,6 +569,7 @@ TQ_API tq_status tq_kv_read(const tq_kv_cache *cache, const int32_t *seqs, const
  *   out      device, same shape, dtype ot, the same rules (written; must not
  *            overlap q or the cache)
  *   heads    query heads, a multiple of kv_heads
+ *   scale    any number within +-TQ_KV_MAX_SCALE
  *   workspace  device, >= tq_kv_attention_workspace_bytes(...) bytes, 256-byte
  *            aligned, exclusively owned by this call until it completes on
  *            `stream`; need not be cleared, keeps nothing between calls
