@@ -27,12 +27,7 @@
 // are scaled by 2^7.  The maximum they refer to is followed only when it grows
 // by more than 2^8 (rescaling the accumulators is the exception), so a weight
 // is at most 2^15, and weights down to 2^-31 of the largest survive.
-#include "tq_device.cuh"
-#include "tq_internal.h"
-
-#include <math.h>
-
-#include <type_traits>
+#include "tq_attention.cuh"
 
 namespace tq {
 
@@ -41,54 +36,8 @@ namespace {
 constexpr int kGroup = 16;               // tokens of a group
 constexpr uint32_t kLutBase = 0x10000u;  // shared-memory address of the centroid table
 constexpr uint32_t kLutStep = 256;       // bytes between its rows (128 used)
-constexpr float kWeightExp = 7.0f;       // softmax weights are held times 2^7
-constexpr float kLazy = 8.0f;            // log2 by which a maximum may grow before it is followed
 constexpr int kLeastGroups = 4;          // groups of a warp's range at least
-
-struct AttnParams {
-    KvCache c;
-    const int32_t *lens, *parents;  // parents null: a chain
-    int64_t parents_ld;
-    const char *q;
-    int64_t q_batch, q_token, q_head;  // elements
-    char *out;
-    int64_t o_batch, o_token, o_head;
-    int tree, heads, group_heads;  // query heads per key/value head
-    int rows, row_tiles;           // rows of a (sequence, head), tiles of them
-    int qdtype;
-    float scale_log2;  // |scale| log2(e): maxima are taken of the scores before it
-    int negative;      // the scale is negative: the queries' sign is turned
-    int *prefix;     // [batch + 1] groups before each sequence
-    float *part_ml;  // [slots][rows of a tile][2]: maximum, sum
-    float *part_o;   // [slots][rows of a tile][head_dim]
-    int workers;  // warps of the launch
-};
-
-// Tokens that sequence b attends over, drafted ones included, within its table.
-__device__ __forceinline__ int seq_tokens(const AttnParams &P, int len) {
-    const int64_t cap = (int64_t)P.c.pages_per_seq << P.c.page_shift;
-    const int64_t n = (int64_t)max(len, 0) + P.tree;
-    return (int)(n < cap ? n : cap);
-}
-
-// The split of W groups over warps: of n warps at work, warp i takes
-// [i W / n, (i + 1) W / n), kLeastGroups groups or more.
-__device__ __forceinline__ int worker_count(int64_t W, int most) {
-    const int64_t n = (W + kLeastGroups - 1) / kLeastGroups;
-    return (int)(n < most ? n : most);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
+constexpr int kTcLeastRows = 16;         // above: the tcgen05 kernel
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     uint32_t d;
@@ -121,65 +70,6 @@ __device__ __forceinline__ void fill_lut(int tid, int threads) {
         asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(a), "r"(o[0]) : "memory");
     }
 }
-
-// Which drafted tokens each drafted token sees, held by a warp: lane l has the
-// words of tokens l and l + 32.  A word is the token itself and its ancestors,
-// or 0 for a token that is not there (a parent that is neither -1 nor an
-// earlier token, its own or an ancestor's).  Six rounds of pointer doubling.
-struct TreeWords {
-    uint64_t w[2];
-    __device__ __forceinline__ TreeWords(const AttnParams &P, int b, int lane) {
-        int ptr[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int i = lane + 32 * k;
-            w[k] = i < P.tree ? (2ull << i) - 1 : 0;  // a chain
-            ptr[k] = -1;
-            if (P.parents && i < P.tree) {
-                const int par = P.parents[b * P.parents_ld + i];
-                ptr[k] = par < -1 || par >= i ? -2 : par;
-                w[k] = 1ull << i;
-            }
-        }
-        if (!P.parents || P.tree == 1) {
-            if (ptr[0] == -2) w[0] = 0;
-            return;
-        }
-        for (int hop = 1; hop < P.tree; hop <<= 1) {
-            uint64_t nw[2];
-            int np[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int from = ptr[k] & 31;
-                const uint64_t a0 = __shfl_sync(kFull, w[0], from), a1 = __shfl_sync(kFull, w[1], from);
-                const int p0 = __shfl_sync(kFull, ptr[0], from), p1 = __shfl_sync(kFull, ptr[1], from);
-                nw[k] = w[k];
-                np[k] = ptr[k];
-                if (ptr[k] >= 0) {
-                    nw[k] |= ptr[k] >= 32 ? a1 : a0;
-                    np[k] = ptr[k] >= 32 ? p1 : p0;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                w[k] = nw[k];
-                ptr[k] = np[k];
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (ptr[k] == -2) w[k] = 0;
-    }
-    // word of token t (any per lane)
-    __device__ __forceinline__ uint64_t of(int t) const {
-        const uint64_t a0 = __shfl_sync(kFull, w[0], t & 31), a1 = __shfl_sync(kFull, w[1], t & 31);
-        return t >= 32 ? a1 : a0;
-    }
-    // bit t: token t is there
-    __device__ __forceinline__ uint64_t present() const {
-        return (uint64_t)__ballot_sync(kFull, w[0] != 0) | ((uint64_t)__ballot_sync(kFull, w[1] != 0) << 32);
-    }
-};
 
 // The rotated query as operand fragments, straight from memory: lane
 // l = 4 g + c owns row g, elements DP/4 c .. of it, which for a head dimension
@@ -337,9 +227,7 @@ __device__ __forceinline__ void load_values(const uint8_t *codes, const uint16_t
 
 __device__ __forceinline__ uint32_t dup_half(uint32_t d, bool high) { return prmt(d, d, high ? 0x3232u : 0x1010u); }
 
-// Running state of a warp's rows: row 2c + k of each tile of 8.  A row without
-// a token so far has the finite maximum kNoMax and the sum 0.
-constexpr float kNoMax = -1e30f;
+// Running state of a warp's rows: row 2c + k of each tile of 8.
 template <int DP, int NT>
 struct AttnState {
     float o[NT][DP / 16][4];
@@ -481,32 +369,6 @@ __device__ __forceinline__ void step_weights(const AttnParams &P, float (&s)[kSt
     }
 }
 
-// Exclusive prefix of the sequences' groups into `prefix`, by the whole CTA.
-__device__ __forceinline__ void scan_sequences(const AttnParams &P, int *prefix, int *scan, int tid, int threads) {
-    const int per = (P.c.batch + threads - 1) / threads;
-    int sum = 0;
-    for (int i = tid * per; i < min(P.c.batch, (tid + 1) * per); ++i)
-        sum += (seq_tokens(P, P.lens[i]) + kGroup - 1) / kGroup;
-    int inc = sum;
-    const int lane = tid & 31;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-        const int o = __shfl_up_sync(kFull, inc, k);
-        if (lane >= k) inc += o;
-    }
-    if (lane == 31) scan[tid >> 5] = inc;
-    __syncthreads();
-    int base = 0;
-    for (int w = 0; w < (tid >> 5); ++w) base += scan[w];
-    int at = base + inc - sum;
-    for (int i = tid * per; i < min(P.c.batch, (tid + 1) * per); ++i) {
-        prefix[i] = at;
-        at += (seq_tokens(P, P.lens[i]) + kGroup - 1) / kGroup;
-    }
-    if (tid == threads - 1) prefix[P.c.batch] = base + inc;
-    __syncthreads();
-}
-
 // Shared memory: prefix sums below the table, which starts at kLutBase and
 // ends at kLutBase + 64 KB.
 struct AttnShared {
@@ -531,10 +393,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
     asm volatile("mov.u32 %0, %1;" : "=r"(lane_base) : "r"(kLutBase | (uint32_t)(lane * 4)) : "memory");
     const int per_seq = P.c.kv_heads * P.row_tiles;
     const int64_t W = (int64_t)sh.prefix[P.c.batch] * per_seq;
+    if (blockIdx.x == 0 && tid == 0) P.header[0] = 0u;  // no wait here that could run out
     if (blockIdx.x == 0)
         for (int i = tid; i <= P.c.batch; i += WARPS * 32) P.prefix[i] = sh.prefix[i];
     // the first warps of all CTAs come first, so that a few ranges spread over the SMs
-    const int workers = worker_count(W, P.workers);
+    const int workers = worker_count(P, W);
     const int me = warp * gridDim.x + blockIdx.x;
     if (me >= workers) return;
     const LaneOffsets<DP, FULL> off(P.c.head_dim, lane);
@@ -708,7 +571,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 constexpr int kJoinWarps = 8;
 
 template <int OT>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P, int tile_rows) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P) {
     __shared__ float so[kJoinWarps][256];
     __shared__ float sl[kJoinWarps];
     grid_dependency_wait();
@@ -716,27 +579,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     const int row = blockIdx.x % P.rows;  // grid.x: rows of (sequence, head) pairs
     const int64_t bh = blockIdx.x / P.rows;
     const int b = (int)(bh / P.c.kv_heads), head = (int)(bh % P.c.kv_heads);
-    const int tile = row / tile_rows, r = row % tile_rows;
+    const int tile = row / P.tile_rows, r = row % P.tile_rows;
     const int per_seq = P.c.kv_heads * P.row_tiles;
     const int64_t W = (int64_t)P.prefix[P.c.batch] * per_seq;
-    const int workers = worker_count(W, P.workers);
+    const int workers = worker_count(P, W);
     const int hr = head * P.row_tiles + tile;
     const int groups = P.prefix[b + 1] - P.prefix[b];
     const int64_t first = (int64_t)P.prefix[b] * per_seq + (int64_t)hr * groups;
     // the warp of group x: the largest i with i W / workers <= x
     const int64_t i0 = ((first + 1) * workers - 1) / W, i1 = ((first + groups) * workers - 1) / W;
     const int64_t unit = (int64_t)b * per_seq + hr;
+    const int64_t s0 = (unit + i0) * P.parts, s1 = (unit + i1 + 1) * P.parts;  // its slots
     const float2 *ml = reinterpret_cast<const float2 *>(P.part_ml);
 
     float mx = kNoMax;
-    for (int64_t i = i0 + lane; i <= i1; i += 32) mx = fmaxf(mx, ml[(unit + i) * tile_rows + r].x);
+    for (int64_t i = s0 + lane; i < s1; i += 32) mx = fmaxf(mx, ml[i * P.tile_rows + r].x);
 #pragma unroll
     for (int k = 16; k >= 1; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, k));
     const int D = P.c.head_dim;
     float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     float l = 0.f;
-    for (int64_t i = i0 + warp; i <= i1; i += kJoinWarps) {
-        const int64_t s = (unit + i) * tile_rows + r;
+    for (int64_t i = s0 + warp; i < s1; i += kJoinWarps) {
+        const int64_t s = i * P.tile_rows + r;
         const float2 p = ml[s];
         if (p.y == 0.f) continue;  // nothing seen there
         const float f = ex2((p.x - mx) * P.scale_log2);
@@ -787,21 +651,38 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     }
 }
 
-// Rows of a tile: 8, or 16 where a (sequence, head) has more than 8 rows and
-// the accumulators of 16 fit the registers (head dimension up to 128).
+// Which kernel runs, and how it cuts the work.
 struct AttnPlan {
-    int dp, nt, warps, rows, row_tiles;
-    int64_t units;
+    bool tc;  // the tcgen05 kernel
+    int dp, nt, warps;
+    int rows, row_tiles, tile_rows, group, workers, least, parts;
+    int64_t slots;
 };
 
-AttnPlan plan_attention(int64_t batch, int tree, int heads, int kv_heads, int head_dim) {
-    AttnPlan p;
-    p.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+AttnPlan plan_attention(int64_t batch, int tree, int heads, int kv_heads, int head_dim, int sm_count) {
+    AttnPlan p = {};
     p.rows = tree * (heads / kv_heads);
-    p.nt = p.rows > 8 && p.dp <= 128 ? 2 : 1;
-    p.warps = p.nt == 2 || p.dp == 256 ? 8 : 12;
-    p.row_tiles = (p.rows + 8 * p.nt - 1) / (8 * p.nt);
-    p.units = batch * kv_heads * p.row_tiles;
+    p.tc = p.rows > kTcLeastRows && tc_attention_fits(head_dim);
+    if (p.tc) {
+        p.tile_rows = tc_attention_tile_rows(p.rows);
+        p.parts = p.tile_rows == 128 ? 2 : 1;
+        p.group = 128;
+        p.workers = sm_count;
+        p.least = 1;
+    } else {
+        // tiles of 8 rows, or 16 where a (sequence, head) has more than 8 rows
+        // and the accumulators of 16 fit the registers (head dimension up to 128)
+        p.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+        p.nt = p.rows > 8 && p.dp <= 128 ? 2 : 1;
+        p.warps = p.nt == 2 || p.dp == 256 ? 8 : 12;
+        p.tile_rows = 8 * p.nt;
+        p.parts = 1;
+        p.group = kGroup;
+        p.workers = sm_count * p.warps;
+        p.least = kLeastGroups;
+    }
+    p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
+    p.slots = (batch * kv_heads * p.row_tiles + p.workers) * p.parts;
     return p;
 }
 
@@ -820,17 +701,37 @@ cudaError_t launch_attend(const AttnParams &P, cudaStream_t stream) {
                               : launch_attend_as<DP, NT, WARPS, false>(P, stream);
 }
 
+template <int OT>
+cudaError_t launch_join_as(const AttnParams &P, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)P.c.batch * P.c.kv_heads * P.rows));
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<OT>, P);
+}
+
 }  // namespace
 
+cudaError_t launch_join(const AttnParams &P, int odtype, cudaStream_t stream) {
+    if (odtype == kF32) return launch_join_as<kF32>(P, stream);
+    return odtype == kBF16 ? launch_join_as<kBF16>(P, stream) : launch_join_as<kF16>(P, stream);
+}
+
+// Workspace: a 256-byte header (status word), the prefix sums, the parts'
+// maxima and sums, their values.
 size_t attention_workspace_bytes(int64_t batch, int tree, int heads, int kv_heads, int head_dim, int sm_count) {
-    const AttnPlan p = plan_attention(batch, tree, heads, kv_heads, head_dim);
-    const size_t slots = (size_t)(p.units + sm_count * p.warps);
-    return 256 + round_up((size_t)(batch + 1) * 4, 256) + round_up(slots * 8 * p.nt * 8, 256) +
-           slots * 8 * p.nt * head_dim * 4;
+    const AttnPlan p = plan_attention(batch, tree, heads, kv_heads, head_dim, sm_count);
+    return 256 + round_up((size_t)(batch + 1) * 4, 256) + round_up((size_t)p.slots * p.tile_rows * 8, 256) +
+           (size_t)p.slots * p.tile_rows * head_dim * 4;
 }
 
 cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t stream) {
-    const AttnPlan plan = plan_attention(j.c.batch, j.tree, j.heads, j.c.kv_heads, j.c.head_dim);
+    const AttnPlan plan = plan_attention(j.c.batch, j.tree, j.heads, j.c.kv_heads, j.c.head_dim, sm_count);
     AttnParams P;
     P.c = j.c;
     P.lens = j.lens;
@@ -852,34 +753,26 @@ cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t s
     P.qdtype = j.qdtype;
     P.scale_log2 = fabsf(j.scale) * 1.44269504088896340736f;
     P.negative = j.scale < 0.f;
-    P.workers = sm_count * plan.warps;
-    const size_t slots = (size_t)(plan.units + sm_count * plan.warps);
+    P.group = plan.group;
+    P.workers = plan.workers;
+    P.least = plan.least;
+    P.parts = plan.parts;
+    P.tile_rows = plan.tile_rows;
+    P.header = reinterpret_cast<unsigned *>(j.workspace);
     char *ws = j.workspace + 256;
     P.prefix = reinterpret_cast<int *>(ws);
     ws += round_up((size_t)(j.c.batch + 1) * 4, 256);
     P.part_ml = reinterpret_cast<float *>(ws);
-    ws += round_up(slots * 8 * plan.nt * 8, 256);
+    ws += round_up((size_t)plan.slots * plan.tile_rows * 8, 256);
     P.part_o = reinterpret_cast<float *>(ws);
 
     cudaError_t e;
-    if (plan.dp == 64) e = plan.nt == 1 ? launch_attend<64, 1, 12>(P, stream) : launch_attend<64, 2, 8>(P, stream);
-    else if (plan.dp == 128) e = plan.nt == 1 ? launch_attend<128, 1, 12>(P, stream) : launch_attend<128, 2, 8>(P, stream);
+    if (plan.tc) e = launch_tc_attention(P, stream);
+    else if (plan.dp == 64) e = plan.nt == 1 ? launch_attend<64, 1, 12>(P, stream) : launch_attend<64, 2, 8>(P, stream);
+    else if (plan.dp == 128)
+        e = plan.nt == 1 ? launch_attend<128, 1, 12>(P, stream) : launch_attend<128, 2, 8>(P, stream);
     else e = launch_attend<256, 1, 8>(P, stream);
-    if (e != cudaSuccess) return e;
-
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)j.c.batch * j.c.kv_heads * plan.rows));
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const int tile_rows = 8 * plan.nt;
-    if (j.odtype == kF32) return cudaLaunchKernelEx(&cfg, join_kernel<kF32>, P, tile_rows);
-    if (j.odtype == kBF16) return cudaLaunchKernelEx(&cfg, join_kernel<kBF16>, P, tile_rows);
-    return cudaLaunchKernelEx(&cfg, join_kernel<kF16>, P, tile_rows);
+    return e != cudaSuccess ? e : launch_join(P, j.odtype, stream);
 }
 
 }  // namespace tq

@@ -1,0 +1,163 @@
+// tq_attention.cuh -- what the attention kernels share: the call's description,
+// the split of the work, the ancestors of drafted tokens, the joining launch.
+#pragma once
+
+#include <math.h>
+
+#include <type_traits>
+
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+constexpr float kWeightExp = 7.0f;  // softmax weights are held times 2^7
+constexpr float kLazy = 8.0f;       // log2 by which a maximum may grow before it is followed
+constexpr float kNoMax = -1e30f;    // maximum of a row without a token so far (its sum is 0)
+
+struct AttnParams {
+    KvCache c;
+    const int32_t *lens, *parents;  // parents null: a chain
+    int64_t parents_ld;
+    const char *q;
+    int64_t q_batch, q_token, q_head;  // elements
+    char *out;
+    int64_t o_batch, o_token, o_head;
+    int tree, heads, group_heads;  // query heads per key/value head
+    int rows, row_tiles;           // rows of a (sequence, head), tiles of them
+    int qdtype;
+    float scale_log2;  // |scale| log2(e): maxima are taken of the scores before it
+    int negative;      // the scale is negative: the queries' sign is turned
+    // the split and its results (workspace)
+    int group;       // tokens of a group: what ranges are counted in
+    int workers;     // ranges at most
+    int least;       // groups of a range at least
+    int parts;       // partial results that a worker leaves of a unit
+    int tile_rows;   // rows of a partial result
+    unsigned *header;  // status word
+    int *prefix;     // [batch + 1] groups before each sequence
+    float *part_ml;  // [slots][tile_rows][2]: maximum, sum
+    float *part_o;   // [slots][tile_rows][head_dim]
+};
+
+// Tokens that sequence b attends over, drafted ones included, within its table.
+__device__ __forceinline__ int seq_tokens(const AttnParams &P, int len) {
+    const int64_t cap = (int64_t)P.c.pages_per_seq << P.c.page_shift;
+    const int64_t n = (int64_t)max(len, 0) + P.tree;
+    return (int)(n < cap ? n : cap);
+}
+
+// The split of W groups: of n workers (warps or CTAs), worker i takes
+// [i W / n, (i + 1) W / n), P.least groups or more.
+__device__ __forceinline__ int worker_count(const AttnParams &P, int64_t W) {
+    const int64_t n = (W + P.least - 1) / P.least;
+    return (int)(n < P.workers ? n : P.workers);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Which drafted tokens each drafted token sees, held by a warp: lane l has the
+// words of tokens l and l + 32.  A word is the token itself and its ancestors,
+// or 0 for a token that is not there (a parent that is neither -1 nor an
+// earlier token, its own or an ancestor's).  Six rounds of pointer doubling.
+struct TreeWords {
+    uint64_t w[2];
+    __device__ __forceinline__ TreeWords(const AttnParams &P, int b, int lane) {
+        int ptr[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = lane + 32 * k;
+            w[k] = i < P.tree ? (2ull << i) - 1 : 0;  // a chain
+            ptr[k] = -1;
+            if (P.parents && i < P.tree) {
+                const int par = P.parents[b * P.parents_ld + i];
+                ptr[k] = par < -1 || par >= i ? -2 : par;
+                w[k] = 1ull << i;
+            }
+        }
+        if (!P.parents || P.tree == 1) {
+            if (ptr[0] == -2) w[0] = 0;
+            return;
+        }
+        for (int hop = 1; hop < P.tree; hop <<= 1) {
+            uint64_t nw[2];
+            int np[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int from = ptr[k] & 31;
+                const uint64_t a0 = __shfl_sync(kFull, w[0], from), a1 = __shfl_sync(kFull, w[1], from);
+                const int p0 = __shfl_sync(kFull, ptr[0], from), p1 = __shfl_sync(kFull, ptr[1], from);
+                nw[k] = w[k];
+                np[k] = ptr[k];
+                if (ptr[k] >= 0) {
+                    nw[k] |= ptr[k] >= 32 ? a1 : a0;
+                    np[k] = ptr[k] >= 32 ? p1 : p0;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                w[k] = nw[k];
+                ptr[k] = np[k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (ptr[k] == -2) w[k] = 0;
+    }
+    // word of token t (any per lane)
+    __device__ __forceinline__ uint64_t of(int t) const {
+        const uint64_t a0 = __shfl_sync(kFull, w[0], t & 31), a1 = __shfl_sync(kFull, w[1], t & 31);
+        return t >= 32 ? a1 : a0;
+    }
+    // bit t: token t is there
+    __device__ __forceinline__ uint64_t present() const {
+        return (uint64_t)__ballot_sync(kFull, w[0] != 0) | ((uint64_t)__ballot_sync(kFull, w[1] != 0) << 32);
+    }
+};
+
+// Exclusive prefix of the sequences' groups into `prefix`, by the whole CTA.
+__device__ __forceinline__ void scan_sequences(const AttnParams &P, int *prefix, int *scan, int tid, int threads) {
+    const int per = (P.c.batch + threads - 1) / threads;
+    int sum = 0;
+    for (int i = tid * per; i < min(P.c.batch, (tid + 1) * per); ++i)
+        sum += (seq_tokens(P, P.lens[i]) + P.group - 1) / P.group;
+    int inc = sum;
+    const int lane = tid & 31;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const int o = __shfl_up_sync(kFull, inc, k);
+        if (lane >= k) inc += o;
+    }
+    if (lane == 31) scan[tid >> 5] = inc;
+    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < (tid >> 5); ++w) base += scan[w];
+    int at = base + inc - sum;
+    for (int i = tid * per; i < min(P.c.batch, (tid + 1) * per); ++i) {
+        prefix[i] = at;
+        at += (seq_tokens(P, P.lens[i]) + P.group - 1) / P.group;
+    }
+    if (tid == threads - 1) prefix[P.c.batch] = base + inc;
+    __syncthreads();
+}
+
+// The launch that joins the parts of every row, rotates back, divides and
+// rounds; a programmatic dependent of the attention launch before it.
+cudaError_t launch_join(const AttnParams &P, int odtype, cudaStream_t stream);
+
+// The tcgen05 kernel (tq_tcattention.cu): tiles of 128 or 256 rows.
+bool tc_attention_fits(int head_dim);
+cudaError_t launch_tc_attention(const AttnParams &P, cudaStream_t stream);
+int tc_attention_tile_rows(int rows);
+
+}  // namespace tq

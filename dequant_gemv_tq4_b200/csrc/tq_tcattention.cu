@@ -1,0 +1,639 @@
+// tq_tcattention.cu -- attention over the TQ4_1S cache for many rows (drafted
+// trees) on the fifth-generation tensor cores.  Mathematics and the split of
+// the work: tq_attention.cu; here a group is a tile of 128 tokens, a worker a CTA.
+//
+// One CTA per SM holds two streams of work, each with 128 query rows in shared
+// memory, a 128 x 128 score accumulator and an output accumulator in tensor
+// memory.  With more than 128 rows the streams are two row tiles over the same
+// tokens (records are decoded once for 256 rows); with fewer they take even
+// and odd token tiles of one row tile and leave two partial results.
+//   decode warps   codes to fp16 centroid x scale, keys and values, into the
+//                  128-byte-swizzled operand layout (two stages each)
+//   one thread     issues S = Q K^T (both operands in shared memory, K-major)
+//                  and O += P V (P from tensor memory, V as it was written,
+//                  tokens as rows: the instruction takes it N-major)
+//   softmax warps  one thread per row: scores from tensor memory, running
+//                  maximum (followed lazily) and sum, weights as fp16 back into
+//                  the score's own columns
+// While one stream's softmax runs, the tensor cores work for the other.
+#include "tq_attention.cuh"
+
+namespace tq {
+
+namespace {
+
+constexpr int kTile = 128;      // tokens of a tile
+constexpr int kRowTile = 128;   // rows of a stream
+constexpr int kSoftWarps = 8;   // warps 0..7: four per stream
+constexpr int kDecodeWarps = 8; // warps 8..15
+constexpr int kMmaWarp = kSoftWarps + kDecodeWarps;
+constexpr int kTcaThreads = (kMmaWarp + 1) * 32;
+constexpr int kTmemCols = 512;
+constexpr uint32_t kOCol = 256;  // output accumulators; scores at 0 and 128
+constexpr uint64_t kTimeoutNs = 1000000000ull;
+constexpr unsigned kStatusTimeout = 1u;
+constexpr unsigned kStatusTmem = 4u;
+
+// Byte offsets from the 1024-aligned start of dynamic shared memory.
+template <int D>
+struct TcaShape {
+    static constexpr uint32_t kHalf = 128 * 128;        // 128 rows of 64 fp16
+    static constexpr uint32_t kOperand = kHalf * (D / 64);
+    static constexpr uint32_t kQ = 0;                   // two row tiles
+    static constexpr uint32_t kK = kQ + 2 * kOperand;   // two stages
+    static constexpr uint32_t kV = kK + 2 * kOperand;   // two stages
+    static constexpr uint32_t kBars = kV + 2 * kOperand;
+    static constexpr uint32_t kTmemSlot = kBars + 8 * 16;
+    static constexpr uint32_t kAbort = kTmemSlot + 4;
+    static constexpr uint32_t kScan = kTmemSlot + 16;
+    static constexpr uint32_t kPrefix = kScan + 32 * 4;
+    static constexpr uint32_t kEnd = kPrefix + (kAttnMaxBatch + 1) * 4;
+    static constexpr int kBytes = (int)kEnd + 1024;     // room for the alignment
+    static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+    // fp32 accumulator, fp16 operands, M = 128; bit 16: B is N-major
+    static constexpr uint32_t kIdescS = (1u << 4) | ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+    static constexpr uint32_t kIdescO =
+        (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+};
+
+// barriers
+enum : int { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kODone = 12 };
+
+// ---- PTX wrappers ------------------------------------------------------------
+__device__ __forceinline__ uint64_t a_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ void a_mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool a_mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Wait for phase `parity`; false after kTimeoutNs (or 2^30 polls).
+__device__ __noinline__ bool a_mbar_wait_slow(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = a_ns();
+    for (uint32_t it = 0; it < (1u << 30); ++it) {
+        if (a_mbar_try(bar, parity)) return true;
+        if (a_ns() - t0 > kTimeoutNs) return false;
+    }
+    return false;
+}
+__device__ __forceinline__ bool a_mbar_wait(uint32_t bar, uint32_t parity) {
+    return a_mbar_try(bar, parity) || a_mbar_wait_slow(bar, parity);
+}
+__device__ __forceinline__ bool a_mbar_wait_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(kFull, a_mbar_wait(bar, parity));
+}
+__device__ __forceinline__ void a_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void a_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void a_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void a_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void a_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void a_sts128(uint32_t a, const uint32_t (&v)[4]) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+__device__ __forceinline__ void a_named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// D (tensor memory) [+]= A (shared memory) x B (shared memory)
+__device__ __forceinline__ void a_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D (tensor memory) [+]= A (tensor memory) x B (shared memory)
+__device__ __forceinline__ void a_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// 32 consecutive 32-bit columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void a_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void a_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void a_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Operand descriptor, 128-byte swizzle, version 1.  K-major: 8-row groups
+// 1024 bytes apart (lbo unused).  N-major: 64-element groups along N `lbo`
+// apart, 8-row (k) groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t a_desc(uint32_t addr, uint32_t lbo) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Address of 16-byte chunk `chunk` (0..7) of row r in a 128-byte-swizzled half.
+__device__ __forceinline__ uint32_t swizzled(uint32_t half, int r, int chunk) {
+    return half + (uint32_t)r * 128u + (uint32_t)((chunk ^ (r & 7)) << 4);
+}
+
+// A worker's part of a unit: tiles [ta, tb) of a (sequence, head, row tile).
+struct Part {
+    int b, head, row0, len, n, ta, tb;
+    int64_t unit;
+};
+
+template <int D>
+struct Walk {  // the parts of a worker's range, the same for every warp
+    const int *prefix;
+    int per_seq;
+    int64_t at, end;
+    __device__ __forceinline__ bool next(const AttnParams &P, Part &p) {
+        if (at >= end) return false;
+        int lo = 0, hi = P.c.batch - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((int64_t)prefix[mid] * per_seq <= at) lo = mid;
+            else hi = mid - 1;
+        }
+        const int tiles = prefix[lo + 1] - prefix[lo];
+        const int64_t in_seq = at - (int64_t)prefix[lo] * per_seq;
+        const int hr = (int)(in_seq / tiles);
+        p.b = lo;
+        p.head = hr / P.row_tiles;
+        p.row0 = hr % P.row_tiles * P.tile_rows;
+        p.ta = (int)(in_seq - (int64_t)hr * tiles);
+        p.tb = (int)min((int64_t)tiles, p.ta + (end - at));
+        p.unit = (int64_t)lo * per_seq + hr;
+        const int len = P.lens[lo];
+        p.n = seq_tokens(P, len);
+        p.len = min(max(len, 0), P.c.pages_per_seq << P.c.page_shift);
+        at += p.tb - p.ta;
+        return true;
+    }
+};
+
+// ---- decode: codes of one token's D / 2 elements to swizzled fp16 ------------
+// Thread td of the 256 owns token td % 128 of every tile and the half td / 128
+// of its head vector: D / 64 blocks of 32 elements.
+template <int D>
+struct TokenRegs {
+    uint4 w[D / 64];
+    uint32_t d[D / 64];
+};
+
+template <int D>
+__device__ __forceinline__ void load_token(const AttnParams &P, int64_t rec, int part, bool valid, TokenRegs<D> &r) {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        r.w[i] = make_uint4(0u, 0u, 0u, 0u);
+        r.d[i] = 0;
+    }
+    if (valid) {
+        const int blk = part * (D / 64);
+        const uint4 *codes = reinterpret_cast<const uint4 *>(P.c.codes + rec * (D / 2)) + blk;
+        const uint32_t *scales = reinterpret_cast<const uint32_t *>(P.c.scales + rec * (D / 16)) + blk;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            r.w[i] = __ldg(codes + i);
+            r.d[i] = __ldg(scales + i);
+        }
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void decode_token(const TokenRegs<D> &r, uint32_t operand, int row, int part) {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        const int blk = part * (D / 64) + i;
+        const uint32_t half = operand + (uint32_t)(blk >> 1) * TcaShape<D>::kHalf;
+        const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // eight elements, 16 bytes
+            const uint32_t d2 = prmt(r.d[i], r.d[i], j < 2 ? 0x1010u : 0x3232u);
+            uint32_t o[4];
+            decode_word(w[j], o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = hmul2(o[k], d2);
+            a_sts128(swizzled(half, row, (blk & 1) * 4 + j), o);
+        }
+    }
+}
+
+// ---- query rows: rotated, fp16, swizzled ---------------------------------------
+template <int DT, int D>
+__device__ __forceinline__ void rotate_row(const AttnParams &P, const char *x, bool valid, uint32_t operand, int row,
+                                           int blk0, int blk1) {
+    const float f = P.negative ? -0.03125f : 0.03125f;
+    for (int blk = blk0; blk < blk1; ++blk) {
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                float t[4];
+                load4<DT>(x + (int64_t)(32 * blk + i) * ElemSize<DT>::value, t);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[i + k] = flip(t[k], sign_mask(32 * blk + i + k));
+            }
+        }
+#pragma unroll
+        for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if ((i & h) == 0) {
+                    const float a = v[i], b = v[i + h];
+                    v[i] = a + b;
+                    v[i + h] = a - b;
+                }
+        const uint32_t half = operand + (uint32_t)(blk >> 1) * TcaShape<D>::kHalf;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __half2 h = __floats2half2_rn(v[8 * j + 2 * k] * f, v[8 * j + 2 * k + 1] * f);
+                o[k] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            a_sts128(swizzled(half, row, (blk & 1) * 4 + j), o);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnParams P) {
+    using S = TcaShape<D>;
+    extern __shared__ char smem_raw[];
+    const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    char *smem = smem_raw + (base - raw);
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(kFull, tid >> 5, 0);
+    int *prefix = reinterpret_cast<int *>(smem + S::kPrefix);
+    volatile int *aborted = reinterpret_cast<volatile int *>(smem + S::kAbort);
+    auto bar = [&](int i) { return base + S::kBars + 8u * (uint32_t)i; };
+    grid_dependents_launch();  // the joining launch; it waits for this one's end
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            a_mbar_init(bar(kKFull + i), kDecodeWarps);
+            a_mbar_init(bar(kKEmpty + i), 1);
+            a_mbar_init(bar(kVFull + i), kDecodeWarps);
+            a_mbar_init(bar(kVEmpty + i), 1);
+            a_mbar_init(bar(kSFull + i), 1);
+            a_mbar_init(bar(kPReady + i), kSoftWarps / 2);
+        }
+        a_mbar_init(bar(kODone), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *aborted = 0;
+        if (blockIdx.x == 0) P.header[0] = 0u;  // status of this call: set, if at all, a second from now
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + S::kTmemSlot),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    a_fence_before();
+    scan_sequences(P, prefix, reinterpret_cast<int *>(smem + S::kScan), tid, kTcaThreads);
+    a_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + S::kTmemSlot);
+    const bool tmem_ok = tmem == 0u;  // all 512 columns: the base is lane 0, column 0 (checked, never expected)
+    if (!tmem_ok && tid == 0) atomicOr(P.header, kStatusTmem);
+
+    Walk<D> walk;
+    walk.prefix = prefix;
+    walk.per_seq = P.c.kv_heads * P.row_tiles;
+    const int64_t W = (int64_t)prefix[P.c.batch] * walk.per_seq;
+    if (blockIdx.x == 0)
+        for (int i = tid; i <= P.c.batch; i += kTcaThreads) P.prefix[i] = prefix[i];
+    const int workers = worker_count(P, W);
+    const int me = blockIdx.x;
+    walk.at = me < workers ? W * me / workers : 0;
+    walk.end = me < workers ? W * (me + 1) / workers : 0;
+    const bool pair = P.tile_rows == 2 * kRowTile;  // the streams are two row tiles
+    bool ok = tmem_ok;
+    auto give_up = [&]() {
+        ok = false;
+        *aborted = 1;
+        atomicOr(P.header, kStatusTimeout);
+    };
+    Part p;
+
+    if (warp < kSoftWarps) {
+        // ---- softmax: thread = row of a stream ----------------------------------
+        const int s = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lanes + 128u * s, t_o = tmem + lanes + kOCol + 128u * s;
+        uint32_t jobs_done = 0, parts_done = 0;
+        const int shift = P.c.page_shift;
+        while (walk.next(P, p)) {
+            // the query rows: this stream's tile, or half of the common one's blocks
+            {
+                const int q_row = p.row0 + (pair ? s * kRowTile : 0) + row;
+                const bool valid = q_row < P.rows;
+                const int t = valid ? q_row / P.group_heads : 0;
+                const int h = p.head * P.group_heads + (valid ? q_row % P.group_heads : 0);
+                const int64_t x = p.b * P.q_batch + t * P.q_token + h * P.q_head;
+                const uint32_t operand = base + S::kQ + (pair ? s : 0) * S::kOperand;
+                constexpr int kBlocks = D / 32;
+                const int b0 = pair ? 0 : s * (kBlocks / 2), b1 = pair ? kBlocks : (s + 1) * (kBlocks / 2);
+                if (P.qdtype == kF32) rotate_row<kF32, D>(P, P.q + x * 4, valid, operand, row, b0, b1);
+                else if (P.qdtype == kBF16) rotate_row<kBF16, D>(P, P.q + x * 2, valid, operand, row, b0, b1);
+                else rotate_row<kF16, D>(P, P.q + x * 2, valid, operand, row, b0, b1);
+                a_proxy_fence();
+            }
+            a_named_sync(1, (kSoftWarps + 1) * 32);
+
+            const int out_row = pair ? s * kRowTile + row : row;  // of the partial result
+            const int unit_row = p.row0 + out_row;
+            const TreeWords words(P, p.b, lane);
+            const uint64_t see = words.of(min(unit_row / P.group_heads, P.tree - 1));
+            const int32_t *table = P.c.page_table + p.b * P.c.table_ld;
+            const int tiles = p.tb - p.ta, jobs = pair ? 2 * tiles : tiles;
+            float m = kNoMax, l = 0.f;
+            int seen_jobs = 0;
+            for (int i = s; i < jobs && ok; i += 2, ++seen_jobs) {
+                const int tile = p.ta + (pair ? i >> 1 : i);
+                // which groups of 16 tokens have a page
+                int page = -1;
+                const int place = tile * kTile + (lane & 7) * 16;
+                if (place < p.n) page = table[place >> shift];
+                const uint32_t groups = __ballot_sync(kFull, page >= 0 && page < P.c.pages) & 0xFFu;
+                const bool tail = tile * kTile + kTile > p.len || groups != 0xFFu;
+                uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
+                if (tail) {
+                    const int full = p.len - tile * kTile;  // columns of the context, may be < 0 or > 128
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int f = full - 32 * k;  // the context's columns from this word's start
+                        uint32_t w = f >= 32 ? ~0u : 0u;
+                        if (f < 32) {
+                            const int sh = -f;  // drafted token at bit 0
+                            if (sh >= 64) w = 0;
+                            else if (sh >= 0) w = (uint32_t)(see >> sh);
+                            else w = ((uint32_t)see << f) | ((1u << f) - 1u);
+                        }
+                        uint32_t pg = 0;
+                        if (groups & (1u << (2 * k))) pg |= 0xFFFFu;
+                        if (groups & (1u << (2 * k + 1))) pg |= 0xFFFF0000u;
+                        mask[k] = w & pg;
+                    }
+                }
+                if (!a_mbar_wait_warp(bar(kSFull + s), jobs_done & 1u)) {
+                    give_up();
+                    break;
+                }
+                a_fence_after();
+                float mx = m;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t v[32];
+                    a_ld32(t_s + 32u * k, v);
+                    if (tail) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((mask[k] >> e) & 1u)) v[e] = __float_as_uint(kNoMax);
+                    }
+                    float x[4] = {mx, kNoMax, kNoMax, kNoMax};
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[e]));
+                    mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                }
+                if (__any_sync(kFull, (mx - m) * P.scale_log2 > kLazy)) {
+                    const float f = ex2((m - mx) * P.scale_log2);
+                    m = mx;
+                    l *= f;
+                    if (seen_jobs > 0) {
+                        // the score's commit followed this stream's last product: its sums are complete
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 16) {
+                            uint32_t v[16];
+                            asm volatile(
+                                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+                                "%13,%14,%15}, [%16];"
+                                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+                                  "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+                                  "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                                : "r"(t_o + (uint32_t)k));
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                            a_st16(t_o + (uint32_t)k, v);
+                        }
+                    }
+                }
+                const float off = kWeightExp - m * P.scale_log2;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t v[32], w[16];
+                    a_ld32(t_s + 32u * k, v);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float p0 = ex2(fmaf(__uint_as_float(v[e]), P.scale_log2, off));
+                        float p1 = ex2(fmaf(__uint_as_float(v[e + 1]), P.scale_log2, off));
+                        if (tail) {
+                            if (!((mask[k] >> e) & 1u)) p0 = 0.f;
+                            if (!((mask[k] >> (e + 1)) & 1u)) p1 = 0.f;
+                        }
+                        sum[e & 2] += p0;
+                        sum[(e & 2) + 1] += p1;
+                        const __half2 h = __floats2half2_rn(p0, p1);
+                        w[e / 2] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    // weights of columns 32k .. take columns 16k .. of the score, read by now
+                    a_st16(t_s + 16u * k, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                a_wait_st();
+                a_fence_before();
+                __syncwarp();
+                if (lane == 0) a_arrive(bar(kPReady + s));
+                ++jobs_done;
+            }
+            // the part's result
+            if (ok && !a_mbar_wait_warp(bar(kODone), parts_done & 1u)) give_up();
+            ++parts_done;
+            if (ok) {
+                a_fence_after();
+                const bool store = unit_row < P.rows;
+                const int64_t slot = (p.unit + me) * P.parts + (pair ? 0 : s);
+                const int64_t at_row = slot * P.tile_rows + out_row;
+                if (store) reinterpret_cast<float2 *>(P.part_ml)[at_row] = make_float2(m, l);
+                if (seen_jobs > 0) {
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 32) {
+                        uint32_t v[32];
+                        a_ld32(t_o + (uint32_t)k, v);
+                        if (store) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(P.part_o + at_row * D + k);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        }
+                    }
+                }
+                a_fence_before();
+            }
+            a_named_sync(1, (kSoftWarps + 1) * 32);  // the queries may be replaced
+        }
+    } else if (warp < kMmaWarp) {
+        // ---- decode ------------------------------------------------------------------
+        const int td = tid - kSoftWarps * 32, row = td & (kTile - 1), half = td / kTile;
+        const int shift = P.c.page_shift, in_page = (1 << shift) - 1;
+        const int64_t v_rows = (int64_t)P.c.kv_heads << shift;
+        uint32_t tile_no = 0;
+        while (ok && walk.next(P, p)) {
+            const int32_t *table = P.c.page_table + p.b * P.c.table_ld;
+            uint64_t present = 0;
+            if (p.tb * kTile > p.len) present = TreeWords(P, p.b, lane).present();
+            // a record that no row sees counts as zero whatever the memory holds
+            auto page_of = [&](int tile) {
+                const int place = tile * kTile + row, j = place - p.len;
+                if (tile >= p.tb || place >= p.n || (j >= 0 && !((present >> j) & 1ull))) return -1;
+                const int page = table[place >> shift];
+                return page < P.c.pages ? page : -1;
+            };
+            auto record = [&](int page, int tile) {
+                return (((int64_t)page * 2 * P.c.kv_heads + p.head) << shift) + ((tile * kTile + row) & in_page);
+            };
+            TokenRegs<D> k, v;
+            int page = page_of(p.ta), next = page_of(p.ta + 1);
+            load_token<D>(P, record(page, p.ta), half, page >= 0, k);
+            load_token<D>(P, record(page, p.ta) + v_rows, half, page >= 0, v);
+            for (int tile = p.ta; tile < p.tb; ++tile, ++tile_no) {
+                const uint32_t st = tile_no & 1u, parity = ((tile_no >> 1) & 1u) ^ 1u;
+                if (!a_mbar_wait_warp(bar(kKEmpty + st), parity)) {
+                    give_up();
+                    break;
+                }
+                decode_token<D>(k, base + S::kK + st * S::kOperand, row, half);
+                a_proxy_fence();
+                __syncwarp();
+                if (lane == 0) a_arrive(bar(kKFull + st));
+                load_token<D>(P, record(next, tile + 1), half, next >= 0, k);
+                if (!a_mbar_wait_warp(bar(kVEmpty + st), parity)) {
+                    give_up();
+                    break;
+                }
+                decode_token<D>(v, base + S::kV + st * S::kOperand, row, half);
+                a_proxy_fence();
+                __syncwarp();
+                if (lane == 0) a_arrive(bar(kVFull + st));
+                load_token<D>(P, record(next, tile + 1) + v_rows, half, next >= 0, v);
+                next = page_of(tile + 2);
+            }
+        }
+    } else {
+        // ---- tensor-core issue -----------------------------------------------------
+        uint32_t tile_no = 0, jobs_done[2] = {0, 0};  // before this part
+        while (walk.next(P, p)) {
+            a_named_sync(1, (kSoftWarps + 1) * 32);  // the queries are in place
+            const int tiles = p.tb - p.ta, jobs = pair ? 2 * tiles : tiles;
+            if (lane == 0) {
+                auto stage = [&](int i) { return tile_no + (uint32_t)(pair ? i >> 1 : i); };
+                auto score = [&](int i) {
+                    const int s = i & 1;
+                    const uint32_t t = stage(i), st = t & 1u;
+                    if (!a_mbar_wait(bar(kKFull + st), (t >> 1) & 1u)) {
+                        give_up();
+                        return;
+                    }
+                    a_fence_after();
+                    const uint32_t q = base + S::kQ + (pair ? s : 0) * S::kOperand, k = base + S::kK + st * S::kOperand;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {  // 16 elements: 32 bytes along the swizzled row
+                        const uint32_t o = (uint32_t)(kk >> 2) * S::kHalf + 32u * (kk & 3);
+                        a_mma_ss(tmem + 128u * s, a_desc(q + o, 16), a_desc(k + o, 16), S::kIdescS, kk != 0);
+                    }
+                    a_commit(bar(kSFull + s));
+                    if (!pair || s == 1) a_commit(bar(kKEmpty + st));
+                };
+                for (int i = 0; i < 2 && i < jobs && ok; ++i) score(i);
+                for (int i = 0; i < jobs && ok; ++i) {
+                    const int s = i & 1;
+                    const uint32_t t = stage(i), st = t & 1u;
+                    if (!a_mbar_wait(bar(kPReady + s), (jobs_done[s] + (uint32_t)(i >> 1)) & 1u) ||
+                        !a_mbar_wait(bar(kVFull + st), (t >> 1) & 1u)) {
+                        give_up();
+                        break;
+                    }
+                    a_fence_after();
+                    const uint32_t v = base + S::kV + st * S::kOperand;
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)  // 16 tokens: 8 columns of P, 16 rows of V
+                        a_mma_ts(tmem + kOCol + 128u * s, tmem + 128u * s + 8u * kk, a_desc(v + 2048u * kk, S::kHalf),
+                                 S::kIdescO, i >= 2 || kk != 0);
+                    if (!pair || s == 1) a_commit(bar(kVEmpty + st));
+                    if (i + 2 < jobs) score(i + 2);
+                }
+                a_commit(bar(kODone));  // all of this part's products
+            }
+            __syncwarp();
+            tile_no += (uint32_t)tiles;
+            jobs_done[0] += (uint32_t)((jobs + 1) / 2);
+            jobs_done[1] += (uint32_t)(jobs / 2);
+            a_named_sync(1, (kSoftWarps + 1) * 32);  // results are read
+        }
+    }
+    // ---- teardown ---------------------------------------------------------------
+    a_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        if (*aborted && lane == 0) {  // nothing may be in flight; bounded like every wait
+            a_fence_after();
+            a_mbar_init(bar(14), 1);
+            a_commit(bar(14));
+            a_mbar_wait(bar(14), 0u);
+        }
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+template <int D>
+cudaError_t launch_as(const AttnParams &P, cudaStream_t stream) {
+    cudaError_t e =
+        cudaFuncSetAttribute(tc_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcaShape<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    tc_attend_kernel<D><<<P.workers, kTcaThreads, TcaShape<D>::kBytes, stream>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool tc_attention_fits(int head_dim) { return head_dim == 64 || head_dim == 128; }
+
+int tc_attention_tile_rows(int rows) { return rows > kRowTile ? 2 * kRowTile : kRowTile; }
+
+cudaError_t launch_tc_attention(const AttnParams &P, cudaStream_t stream) {
+    return P.c.head_dim == 64 ? launch_as<64>(P, stream) : launch_as<128>(P, stream);
+}
+
+}  // namespace tq
