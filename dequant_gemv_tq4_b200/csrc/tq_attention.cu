@@ -565,20 +565,29 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 }
 
 // ---------------------------------------------------------------------------
-// The parts of each row joined, rotated back, divided and rounded.  One CTA of
-// eight warps per row: the warps share the parts, warp 0 adds up and finishes.
+// The parts of each row joined, rotated back, divided and rounded.  CTAs of
+// eight warps: RW of them share a row's parts, and the first of those adds up
+// and finishes.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 
-template <int OT>
+// a / b of non-negative numbers, in 32 bits where both fit
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+template <int OT, int RW>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P) {
-    __shared__ float so[kJoinWarps][256];
+    __shared__ float so[RW == 1 ? 1 : kJoinWarps][256];
     __shared__ float sl[kJoinWarps];
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.x % P.rows;  // grid.x: rows of (sequence, head) pairs
-    const int64_t bh = blockIdx.x / P.rows;
-    const int b = (int)(bh / P.c.kv_heads), head = (int)(bh % P.c.kv_heads);
+    const int64_t all_rows = (int64_t)P.c.batch * P.c.kv_heads * P.rows;
+    const int64_t index = (int64_t)blockIdx.x * (kJoinWarps / RW) + warp / RW;
+    if (index >= all_rows) return;  // (whole CTAs where RW > 1: one row each)
+    const int row = (int)(index % P.rows);
+    const int bh = (int)(index / P.rows);
+    const int b = bh / P.c.kv_heads, head = bh % P.c.kv_heads;
     const int tile = row / P.tile_rows, r = row % P.tile_rows;
     const int per_seq = P.c.kv_heads * P.row_tiles;
     const int64_t W = (int64_t)P.prefix[P.c.batch] * per_seq;
@@ -586,8 +595,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     const int hr = head * P.row_tiles + tile;
     const int groups = P.prefix[b + 1] - P.prefix[b];
     const int64_t first = (int64_t)P.prefix[b] * per_seq + (int64_t)hr * groups;
-    // the warp of group x: the largest i with i W / workers <= x
-    const int64_t i0 = ((first + 1) * workers - 1) / W, i1 = ((first + groups) * workers - 1) / W;
+    // the worker of group x: the largest i with i W / workers <= x
+    const int64_t i0 = quotient((first + 1) * workers - 1, W), i1 = quotient((first + groups) * workers - 1, W);
     const int64_t unit = (int64_t)b * per_seq + hr;
     const int64_t s0 = (unit + i0) * P.parts, s1 = (unit + i1 + 1) * P.parts;  // its slots
     const float2 *ml = reinterpret_cast<const float2 *>(P.part_ml);
@@ -599,7 +608,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     const int D = P.c.head_dim;
     float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     float l = 0.f;
-    for (int64_t i = s0 + warp; i < s1; i += kJoinWarps) {
+#pragma unroll 4
+    for (int64_t i = s0 + warp % RW; i < s1; i += RW) {
         const int64_t s = i * P.tile_rows + r;
         const float2 p = ml[s];
         if (p.y == 0.f) continue;  // nothing seen there
@@ -617,19 +627,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
             }
         }
     }
+    if (RW > 1) {
 #pragma unroll
-    for (int sb = 0; sb < 2; ++sb)
-        *reinterpret_cast<float4 *>(&so[warp][sb * 128 + 4 * lane]) =
-            make_float4(acc[sb][0], acc[sb][1], acc[sb][2], acc[sb][3]);
-    if (lane == 0) sl[warp] = l;
-    __syncthreads();
-    if (warp != 0) return;
-    l = 0.f;
+        for (int sb = 0; sb < 2; ++sb)
+            *reinterpret_cast<float4 *>(&so[warp][sb * 128 + 4 * lane]) =
+                make_float4(acc[sb][0], acc[sb][1], acc[sb][2], acc[sb][3]);
+        if (lane == 0) sl[warp] = l;
+        __syncthreads();
+        if (warp != 0) return;
+        l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) l += sl[w];
+        for (int w = 0; w < RW; ++w) l += sl[w];
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[sb][i] = 0.f;
+#pragma unroll
+                for (int w = 0; w < RW; ++w) acc[sb][i] += so[w][sb * 128 + 4 * lane + i];
+            }
+    }
     const int t = row / P.group_heads, h = head * P.group_heads + row % P.group_heads;
     // a token that is not there answers zero
-    const bool there = (TreeWords(P, b, lane).present() >> t) & 1ull;
+    const bool there = !P.parents || ((TreeWords(P, b, lane).present() >> t) & 1ull);
     const float inv = there && l > 0.f ? 0.03125f / l : 0.f;
     char *out = P.out + (b * P.o_batch + t * P.o_token + h * P.o_head) * ElemSize<OT>::value;
 #pragma unroll
@@ -638,12 +658,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
         if (sb * 128 >= D) break;
         float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) v[i] += so[w][e + i];
-            v[i] *= inv;
-        }
+        for (int i = 0; i < 4; ++i) v[i] = acc[sb][i] * inv;
         fwht32_warp(v, lane & 7);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = flip(v[i], sign_mask(e + i));
@@ -701,10 +716,11 @@ cudaError_t launch_attend(const AttnParams &P, cudaStream_t stream) {
                               : launch_attend_as<DP, NT, WARPS, false>(P, stream);
 }
 
-template <int OT>
+template <int OT, int RW>
 cudaError_t launch_join_as(const AttnParams &P, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)P.c.batch * P.c.kv_heads * P.rows));
+    const int64_t rows = (int64_t)P.c.batch * P.c.kv_heads * P.rows;
+    cfg.gridDim = dim3((unsigned)((rows * RW + kJoinWarps - 1) / kJoinWarps));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -712,14 +728,24 @@ cudaError_t launch_join_as(const AttnParams &P, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<OT>, P);
+    return cudaLaunchKernelEx(&cfg, join_kernel<OT, RW>, P);
+}
+
+
+// A unit has about workers / units + 1 parts: eight warps share a row where
+// these are many, a warp takes a row where they are few.
+template <int OT>
+cudaError_t launch_join_by(const AttnParams &P, cudaStream_t stream) {
+    const int64_t units = (int64_t)P.c.batch * P.c.kv_heads * P.row_tiles;
+    return (int64_t)P.workers * P.parts > 6 * units ? launch_join_as<OT, 8>(P, stream)
+                                                    : launch_join_as<OT, 1>(P, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_join(const AttnParams &P, int odtype, cudaStream_t stream) {
-    if (odtype == kF32) return launch_join_as<kF32>(P, stream);
-    return odtype == kBF16 ? launch_join_as<kBF16>(P, stream) : launch_join_as<kF16>(P, stream);
+    if (odtype == kF32) return launch_join_by<kF32>(P, stream);
+    return odtype == kBF16 ? launch_join_by<kBF16>(P, stream) : launch_join_by<kF16>(P, stream);
 }
 
 // Workspace: a 256-byte header (status word), the prefix sums, the parts'

@@ -25,9 +25,13 @@ namespace {
 constexpr int kTile = 128;      // tokens of a tile
 constexpr int kRowTile = 128;   // rows of a stream
 constexpr int kSoftWarps = 8;   // warps 0..7: four per stream
-constexpr int kDecodeWarps = 8; // warps 8..15
+constexpr int kDecodeWarps = 4; // warps 8..11
 constexpr int kMmaWarp = kSoftWarps + kDecodeWarps;
-constexpr int kTcaThreads = (kMmaWarp + 1) * 32;
+constexpr int kTcaThreads = 512;  // four warpgroups; warps 13..15 only release their registers
+// Registers a thread: 128 at launch; the softmax holds a whole row of scores.
+// Shares of the launch's 65536: 256 * 184 + 128 * 104 + 128 * 40 = 65536.
+constexpr int kSoftRegs = 184, kDecodeRegs = 104, kIssueRegs = 40;
+static_assert(256 * kSoftRegs + 128 * kDecodeRegs + 128 * kIssueRegs <= kTcaThreads * 128, "register shares");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kOCol = 256;  // output accumulators; scores at 0 and 128
 constexpr uint64_t kTimeoutNs = 1000000000ull;
@@ -60,6 +64,14 @@ struct TcaShape {
 enum : int { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kODone = 12 };
 
 // ---- PTX wrappers ------------------------------------------------------------
+template <int N>
+__device__ __forceinline__ void a_regs_more() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void a_regs_fewer() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ uint64_t a_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -80,7 +92,7 @@ __device__ __forceinline__ bool a_mbar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 // Wait for phase `parity`; false after kTimeoutNs (or 2^30 polls).
-__device__ __noinline__ bool a_mbar_wait_slow(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool a_mbar_wait_slow(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = a_ns();
     for (uint32_t it = 0; it < (1u << 30); ++it) {
         if (a_mbar_try(bar, parity)) return true;
@@ -126,8 +138,9 @@ __device__ __forceinline__ void a_mma_ts(uint32_t d, uint32_t a, uint64_t b, uin
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// 32 consecutive 32-bit columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void a_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+// 32 consecutive 32-bit columns of this thread's tensor-memory lane; the
+// registers are defined after the next a_wait_ld.
+__device__ __forceinline__ void a_ld32(uint32_t taddr, uint32_t *v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -136,9 +149,9 @@ __device__ __forceinline__ void a_ld32(uint32_t taddr, uint32_t (&v)[32]) {
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void a_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+__device__ __forceinline__ void a_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void a_st16(uint32_t taddr, const uint32_t *v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
             taddr),
@@ -198,43 +211,43 @@ struct Walk {  // the parts of a worker's range, the same for every warp
 };
 
 // ---- decode: codes of one token's D / 2 elements to swizzled fp16 ------------
-// Thread td of the 256 owns token td % 128 of every tile and the half td / 128
-// of its head vector: D / 64 blocks of 32 elements.
+// Thread td of the 128 owns token td of every tile: D / 32 blocks of 32 elements.
 template <int D>
 struct TokenRegs {
-    uint4 w[D / 64];
-    uint32_t d[D / 64];
+    uint4 w[D / 32];
+    uint32_t d[D / 32];
 };
 
 template <int D>
-__device__ __forceinline__ void load_token(const AttnParams &P, int64_t rec, int part, bool valid, TokenRegs<D> &r) {
+__device__ __forceinline__ void load_token(const AttnParams &P, int64_t rec, bool valid, TokenRegs<D> &r) {
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
+    for (int i = 0; i < D / 32; ++i) {
         r.w[i] = make_uint4(0u, 0u, 0u, 0u);
         r.d[i] = 0;
     }
     if (valid) {
-        const int blk = part * (D / 64);
-        const uint4 *codes = reinterpret_cast<const uint4 *>(P.c.codes + rec * (D / 2)) + blk;
-        const uint32_t *scales = reinterpret_cast<const uint32_t *>(P.c.scales + rec * (D / 16)) + blk;
+        const uint4 *codes = reinterpret_cast<const uint4 *>(P.c.codes + rec * (D / 2));
+        const uint2 *scales = reinterpret_cast<const uint2 *>(P.c.scales + rec * (D / 16));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) r.w[i] = __ldg(codes + i);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-            r.w[i] = __ldg(codes + i);
-            r.d[i] = __ldg(scales + i);
+            const uint2 d = __ldg(scales + i);
+            r.d[2 * i] = d.x;
+            r.d[2 * i + 1] = d.y;
         }
     }
 }
 
 template <int D>
-__device__ __forceinline__ void decode_token(const TokenRegs<D> &r, uint32_t operand, int row, int part) {
+__device__ __forceinline__ void decode_token(const TokenRegs<D> &r, uint32_t operand, int row) {
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        const int blk = part * (D / 64) + i;
+    for (int blk = 0; blk < D / 32; ++blk) {
         const uint32_t half = operand + (uint32_t)(blk >> 1) * TcaShape<D>::kHalf;
-        const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+        const uint32_t w[4] = {r.w[blk].x, r.w[blk].y, r.w[blk].z, r.w[blk].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // eight elements, 16 bytes
-            const uint32_t d2 = prmt(r.d[i], r.d[i], j < 2 ? 0x1010u : 0x3232u);
+            const uint32_t d2 = prmt(r.d[blk], r.d[blk], j < 2 ? 0x1010u : 0x3232u);
             uint32_t o[4];
             decode_word(w[j], o);
 #pragma unroll
@@ -283,6 +296,166 @@ __device__ __forceinline__ void rotate_row(const AttnParams &P, const char *x, b
             a_sts128(swizzled(half, row, (blk & 1) * 4 + j), o);
         }
     }
+}
+
+// ---- softmax of one row's 128 scores ---------------------------------------------
+// Packed fp32 pairs (each half one IEEE operation).
+__device__ __forceinline__ uint64_t a_pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void a_unpack(uint64_t r, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+}
+__device__ __forceinline__ uint64_t a_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t a_add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Output sums of this thread's row times f.
+template <int D>
+__device__ __forceinline__ void rescale_row(uint32_t t_o, float f) {
+#pragma unroll 1
+    for (int k = 0; k < D; k += 32) {
+        uint32_t v[32];
+        a_ld32(t_o + (uint32_t)k, v);
+        a_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+        a_st16(t_o + (uint32_t)k, v);
+        a_st16(t_o + (uint32_t)k + 16, v + 16);
+    }
+}
+
+// The maximum of 64 scores v and mx.
+__device__ __forceinline__ float max64(const uint32_t *v, float mx) {
+    float x[4] = {mx, kNoMax, kNoMax, kNoMax};
+#pragma unroll
+    for (int e = 0; e < 64; e += 2)
+        x[(e >> 1) & 3] = fmaxf(x[(e >> 1) & 3], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+}
+
+// Weights of 2 N scores into N columns at t_p, their sum onto `sum`.
+template <int N>
+__device__ __forceinline__ void weights(uint32_t *v, uint64_t scale2, uint64_t off2, uint32_t t_p,
+                                        uint64_t (&sum)[2]) {
+#pragma unroll
+    for (int e = 0; e < 2 * N; e += 2) {
+        float a, b;
+        a_unpack(a_fma2(a_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), scale2, off2), a, b);
+        a = ex2(a);
+        b = ex2(b);
+        sum[(e >> 1) & 1] = a_add2(sum[(e >> 1) & 1], a_pack(a, b));
+        const __half2 h = __floats2half2_rn(a, b);
+        v[e / 2] = *reinterpret_cast<const uint32_t *>(&h);
+        if ((e & 31) == 30) a_st16(t_p + (e >> 5) * 16u, v + (e >> 5) * 16);
+    }
+}
+
+// The maximum follows to mx where it grew by more than kLazy for a row of the
+// warp.  `have`: the output sums hold earlier products.
+template <int D>
+__device__ __forceinline__ void follow(uint32_t t_o, float scale, bool have, float mx, float &m, float &l) {
+    if (__any_sync(kFull, (mx - m) * scale > kLazy)) {
+        const float f = ex2((m - mx) * scale);
+        m = mx;
+        l *= f;
+        // the scores' commit followed this stream's last product: its sums are complete
+        if (have) rescale_row<D>(t_o, f);
+    }
+}
+
+__device__ __forceinline__ float sum_of(const uint64_t (&sum)[2]) {
+    float s0, s1, s2, s3;
+    a_unpack(sum[0], s0, s1);
+    a_unpack(sum[1], s2, s3);
+    return (s0 + s1) + (s2 + s3);
+}
+
+// Scores at t_s to weights: those of columns 0..63 in columns 0..31, of 64..127
+// in 64..95, so that the upper half, which is in registers when the maximum is
+// known, can be written while the lower is still to be read again.
+template <int D>
+__device__ __forceinline__ void softmax_row(uint32_t t_s, uint32_t t_o, float scale, bool have, float &m, float &l) {
+    uint32_t v[64];
+    a_ld32(t_s, v);
+    a_ld32(t_s + 32, v + 32);
+    a_wait_ld();
+    float mx = max64(v, m);
+    a_ld32(t_s + 64, v);
+    a_ld32(t_s + 96, v + 32);
+    a_wait_ld();
+    mx = max64(v, mx);
+    follow<D>(t_o, scale, have, mx, m, l);
+    const float off = kWeightExp - m * scale;
+    const uint64_t scale2 = a_pack(scale, scale), off2 = a_pack(off, off);
+    uint64_t sum[2] = {0, 0};
+    weights<32>(v, scale2, off2, t_s + 64, sum);
+    a_ld32(t_s, v);
+    a_ld32(t_s + 32, v + 32);
+    a_wait_ld();
+    weights<32>(v, scale2, off2, t_s, sum);
+    l += sum_of(sum);
+    a_wait_st();
+}
+
+// Which of a tile's columns a row sees: the context's `full` columns, then
+// drafted token j where bit j of `see` is set; bit g of `groups`: columns
+// 16 g .. have a page.  Word k: columns 32 k ...
+__device__ __forceinline__ uint32_t column_word(int k, int full, uint64_t see, uint32_t groups) {
+    const int f = full - 32 * k;  // the context's columns from this word's start
+    uint32_t w;
+    if (f >= 32) w = ~0u;
+    else if (f > 0) w = ((uint32_t)see << f) | ((1u << f) - 1u);
+    else w = f > -64 ? (uint32_t)(see >> -f) : 0u;
+    const uint32_t g = groups >> (2 * k);
+    return w & ((g & 1u ? 0xFFFFu : 0u) | (g & 2u ? 0xFFFF0000u : 0u));
+}
+
+// The same for a tile with columns that do not count (a sequence's last one or
+// two tiles), 32 columns at a time.
+template <int D>
+__device__ __forceinline__ void softmax_row_masked(uint32_t t_s, uint32_t t_o, float scale, bool have, int full,
+                                                   uint64_t see, uint32_t groups, float &m, float &l) {
+    float mx = m;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        uint32_t v[32];
+        a_ld32(t_s + 32u * k, v);
+        const uint32_t w = column_word(k, full, see, groups);
+        a_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) mx = (w >> e) & 1u ? fmaxf(mx, __uint_as_float(v[e])) : mx;
+    }
+    follow<D>(t_o, scale, have, mx, m, l);
+    const float off = kWeightExp - m * scale;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        uint32_t v[32];
+        a_ld32(t_s + 32u * k, v);
+        const uint32_t w = column_word(k, full, see, groups);
+        a_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+            float a = ex2(fmaf(__uint_as_float(v[e]), scale, off));
+            float b = ex2(fmaf(__uint_as_float(v[e + 1]), scale, off));
+            if (!((w >> e) & 1u)) a = 0.f;
+            if (!((w >> (e + 1)) & 1u)) b = 0.f;
+            l += a + b;
+            const __half2 h = __floats2half2_rn(a, b);
+            v[e / 2] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        a_st16(t_s + (k < 2 ? 16u * k : 32u + 16u * k), v);  // over scores that are read by now
+    }
+    a_wait_st();
 }
 
 template <int D>
@@ -347,6 +520,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
 
     if (warp < kSoftWarps) {
         // ---- softmax: thread = row of a stream ----------------------------------
+        a_regs_more<kSoftRegs>();
         const int s = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + 128u * s, t_o = tmem + lanes + kOCol + 128u * s;
@@ -386,92 +560,16 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                 if (place < p.n) page = table[place >> shift];
                 const uint32_t groups = __ballot_sync(kFull, page >= 0 && page < P.c.pages) & 0xFFu;
                 const bool tail = tile * kTile + kTile > p.len || groups != 0xFFu;
-                uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
-                if (tail) {
-                    const int full = p.len - tile * kTile;  // columns of the context, may be < 0 or > 128
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int f = full - 32 * k;  // the context's columns from this word's start
-                        uint32_t w = f >= 32 ? ~0u : 0u;
-                        if (f < 32) {
-                            const int sh = -f;  // drafted token at bit 0
-                            if (sh >= 64) w = 0;
-                            else if (sh >= 0) w = (uint32_t)(see >> sh);
-                            else w = ((uint32_t)see << f) | ((1u << f) - 1u);
-                        }
-                        uint32_t pg = 0;
-                        if (groups & (1u << (2 * k))) pg |= 0xFFFFu;
-                        if (groups & (1u << (2 * k + 1))) pg |= 0xFFFF0000u;
-                        mask[k] = w & pg;
-                    }
-                }
                 if (!a_mbar_wait_warp(bar(kSFull + s), jobs_done & 1u)) {
                     give_up();
                     break;
                 }
                 a_fence_after();
-                float mx = m;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t v[32];
-                    a_ld32(t_s + 32u * k, v);
-                    if (tail) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((mask[k] >> e) & 1u)) v[e] = __float_as_uint(kNoMax);
-                    }
-                    float x[4] = {mx, kNoMax, kNoMax, kNoMax};
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e & 3] = fmaxf(x[e & 3], __uint_as_float(v[e]));
-                    mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-                }
-                if (__any_sync(kFull, (mx - m) * P.scale_log2 > kLazy)) {
-                    const float f = ex2((m - mx) * P.scale_log2);
-                    m = mx;
-                    l *= f;
-                    if (seen_jobs > 0) {
-                        // the score's commit followed this stream's last product: its sums are complete
-#pragma unroll 1
-                        for (int k = 0; k < D; k += 16) {
-                            uint32_t v[16];
-                            asm volatile(
-                                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-                                "%13,%14,%15}, [%16];"
-                                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-                                  "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
-                                  "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-                                : "r"(t_o + (uint32_t)k));
-                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                            a_st16(t_o + (uint32_t)k, v);
-                        }
-                    }
-                }
-                const float off = kWeightExp - m * P.scale_log2;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t v[32], w[16];
-                    a_ld32(t_s + 32u * k, v);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float p0 = ex2(fmaf(__uint_as_float(v[e]), P.scale_log2, off));
-                        float p1 = ex2(fmaf(__uint_as_float(v[e + 1]), P.scale_log2, off));
-                        if (tail) {
-                            if (!((mask[k] >> e) & 1u)) p0 = 0.f;
-                            if (!((mask[k] >> (e + 1)) & 1u)) p1 = 0.f;
-                        }
-                        sum[e & 2] += p0;
-                        sum[(e & 2) + 1] += p1;
-                        const __half2 h = __floats2half2_rn(p0, p1);
-                        w[e / 2] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                    // weights of columns 32k .. take columns 16k .. of the score, read by now
-                    a_st16(t_s + 16u * k, w);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                a_wait_st();
+                if (tail)
+                    softmax_row_masked<D>(t_s, t_o, P.scale_log2, seen_jobs > 0, p.len - tile * kTile, see, groups, m,
+                                          l);
+                else
+                    softmax_row<D>(t_s, t_o, P.scale_log2, seen_jobs > 0, m, l);
                 a_fence_before();
                 __syncwarp();
                 if (lane == 0) a_arrive(bar(kPReady + s));
@@ -491,6 +589,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                     for (int k = 0; k < D; k += 32) {
                         uint32_t v[32];
                         a_ld32(t_o + (uint32_t)k, v);
+                        a_wait_ld();
                         if (store) {
                             uint4 *dst = reinterpret_cast<uint4 *>(P.part_o + at_row * D + k);
 #pragma unroll
@@ -505,7 +604,8 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
         }
     } else if (warp < kMmaWarp) {
         // ---- decode ------------------------------------------------------------------
-        const int td = tid - kSoftWarps * 32, row = td & (kTile - 1), half = td / kTile;
+        a_regs_fewer<kDecodeRegs>();
+        const int row = tid - kSoftWarps * 32;
         const int shift = P.c.page_shift, in_page = (1 << shift) - 1;
         const int64_t v_rows = (int64_t)P.c.kv_heads << shift;
         uint32_t tile_no = 0;
@@ -525,33 +625,36 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
             };
             TokenRegs<D> k, v;
             int page = page_of(p.ta), next = page_of(p.ta + 1);
-            load_token<D>(P, record(page, p.ta), half, page >= 0, k);
-            load_token<D>(P, record(page, p.ta) + v_rows, half, page >= 0, v);
+            load_token<D>(P, record(page, p.ta), page >= 0, k);
+            load_token<D>(P, record(page, p.ta) + v_rows, page >= 0, v);
             for (int tile = p.ta; tile < p.tb; ++tile, ++tile_no) {
                 const uint32_t st = tile_no & 1u, parity = ((tile_no >> 1) & 1u) ^ 1u;
                 if (!a_mbar_wait_warp(bar(kKEmpty + st), parity)) {
                     give_up();
                     break;
                 }
-                decode_token<D>(k, base + S::kK + st * S::kOperand, row, half);
+                decode_token<D>(k, base + S::kK + st * S::kOperand, row);
                 a_proxy_fence();
                 __syncwarp();
                 if (lane == 0) a_arrive(bar(kKFull + st));
-                load_token<D>(P, record(next, tile + 1), half, next >= 0, k);
+                load_token<D>(P, record(next, tile + 1), next >= 0, k);
                 if (!a_mbar_wait_warp(bar(kVEmpty + st), parity)) {
                     give_up();
                     break;
                 }
-                decode_token<D>(v, base + S::kV + st * S::kOperand, row, half);
+                decode_token<D>(v, base + S::kV + st * S::kOperand, row);
                 a_proxy_fence();
                 __syncwarp();
                 if (lane == 0) a_arrive(bar(kVFull + st));
-                load_token<D>(P, record(next, tile + 1) + v_rows, half, next >= 0, v);
+                load_token<D>(P, record(next, tile + 1) + v_rows, next >= 0, v);
                 next = page_of(tile + 2);
             }
         }
+    } else if (warp != kMmaWarp) {
+        a_regs_fewer<kIssueRegs>();
     } else {
         // ---- tensor-core issue -----------------------------------------------------
+        a_regs_fewer<kIssueRegs>();
         uint32_t tile_no = 0, jobs_done[2] = {0, 0};  // before this part
         while (walk.next(P, p)) {
             a_named_sync(1, (kSoftWarps + 1) * 32);  // the queries are in place
@@ -587,8 +690,8 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                     a_fence_after();
                     const uint32_t v = base + S::kV + st * S::kOperand;
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)  // 16 tokens: 8 columns of P, 16 rows of V
-                        a_mma_ts(tmem + kOCol + 128u * s, tmem + 128u * s + 8u * kk, a_desc(v + 2048u * kk, S::kHalf),
+                    for (int kk = 0; kk < kTile / 16; ++kk)  // 16 tokens: 8 columns of weights, 16 rows of V
+                        a_mma_ts(tmem + kOCol + 128u * s, tmem + 128u * s + 8u * kk + (kk >= 4 ? 32u : 0u), a_desc(v + 2048u * kk, S::kHalf),
                                  S::kIdescO, i >= 2 || kk != 0);
                     if (!pair || s == 1) a_commit(bar(kVEmpty + st));
                     if (i + 2 < jobs) score(i + 2);
