@@ -29,12 +29,12 @@ constexpr int kDecodeWarps = 4; // warps 8..11
 constexpr int kMmaWarp = kSoftWarps + kDecodeWarps;
 constexpr int kTcaThreads = 512;  // four warpgroups; warps 13..15 only release their registers
 // Registers a thread: 128 at launch; the softmax holds a whole row of scores.
-// Shares of the launch's 65536: 256 * 184 + 128 * 104 + 128 * 40 = 65536.
-constexpr int kSoftRegs = 184, kDecodeRegs = 104, kIssueRegs = 40;
+// Shares of the launch's 65536: 256 * 184 + 128 * 88 + 128 * 56 = 65536.
+constexpr int kSoftRegs = 184, kDecodeRegs = 88, kIssueRegs = 56;
 static_assert(256 * kSoftRegs + 128 * kDecodeRegs + 128 * kIssueRegs <= kTcaThreads * 128, "register shares");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kOCol = 256;  // output accumulators; scores at 0 and 128
-constexpr uint64_t kTimeoutNs = 1000000000ull;
+constexpr long long kTimeoutCycles = 2000000000ll;  // about a second
 constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusTmem = 4u;
 
@@ -72,11 +72,6 @@ template <int N>
 __device__ __forceinline__ void a_regs_fewer() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-__device__ __forceinline__ uint64_t a_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
 __device__ __forceinline__ void a_mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -91,17 +86,17 @@ __device__ __forceinline__ bool a_mbar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// Wait for phase `parity`; false after kTimeoutNs (or 2^30 polls).
-__device__ __forceinline__ bool a_mbar_wait_slow(uint32_t bar, uint32_t parity) {
-    const uint64_t t0 = a_ns();
+// Wait for phase `parity`; false after kTimeoutCycles (or 2^30 polls).  The
+// limit is read from the SM's own clock and only now and then: reading the
+// global timer between polls delayed every wait of the pipeline.
+__device__ __forceinline__ bool a_mbar_wait(uint32_t bar, uint32_t parity) {
+    if (a_mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
     for (uint32_t it = 0; it < (1u << 30); ++it) {
         if (a_mbar_try(bar, parity)) return true;
-        if (a_ns() - t0 > kTimeoutNs) return false;
+        if ((it & 63u) == 63u && clock64() - t0 > kTimeoutCycles) return false;
     }
     return false;
-}
-__device__ __forceinline__ bool a_mbar_wait(uint32_t bar, uint32_t parity) {
-    return a_mbar_try(bar, parity) || a_mbar_wait_slow(bar, parity);
 }
 __device__ __forceinline__ bool a_mbar_wait_warp(uint32_t bar, uint32_t parity) {
     return __all_sync(kFull, a_mbar_wait(bar, parity));
@@ -118,6 +113,19 @@ __device__ __forceinline__ void a_commit(uint32_t bar) {
 __device__ __forceinline__ void a_sts128(uint32_t a, const uint32_t (&v)[4]) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                  : "memory");
+}
+__device__ __forceinline__ uint4 a_lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+// One lane of the (whole) warp, the same one every time.
+__device__ __forceinline__ bool a_elect() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void a_named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -148,6 +156,13 @@ __device__ __forceinline__ void a_ld32(uint32_t taddr, uint32_t *v) {
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void a_ld16(uint32_t taddr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(taddr));
 }
 __device__ __forceinline__ void a_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -258,43 +273,82 @@ __device__ __forceinline__ void decode_token(const TokenRegs<D> &r, uint32_t ope
 }
 
 // ---- query rows: rotated, fp16, swizzled ---------------------------------------
-template <int DT, int D>
-__device__ __forceinline__ void rotate_row(const AttnParams &P, const char *x, bool valid, uint32_t operand, int row,
-                                           int blk0, int blk1) {
+// Blocks [B0, B1) of a row: all loads first; the signs are compile-time
+// constants and vanish into the first butterflies.
+template <int DT, int D, int B0, int B1>
+__device__ __forceinline__ void rotate_row(const AttnParams &P, const char *x, bool valid, uint32_t operand, int row) {
     const float f = P.negative ? -0.03125f : 0.03125f;
-    for (int blk = blk0; blk < blk1; ++blk) {
-        float v[32];
+    constexpr int E = ElemSize<DT>::value, kLoads = 2 * E;  // 16-byte loads of a block
+    constexpr int kAtOnce = DT == kF32 ? 1 : B1 - B0;       // blocks loaded ahead
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.f;
-        if (valid) {
+    for (int g0 = B0; g0 < B1; g0 += kAtOnce) {
+        uint4 raw[kAtOnce][kLoads];
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                float t[4];
-                load4<DT>(x + (int64_t)(32 * blk + i) * ElemSize<DT>::value, t);
+        for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[i + k] = flip(t[k], sign_mask(32 * blk + i + k));
-            }
-        }
+            for (int j = 0; j < kLoads; ++j)
+                raw[i][j] = valid ? __ldg(reinterpret_cast<const uint4 *>(x + (g0 + i) * 32 * E) + j)
+                                  : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int h = 1; h < 32; h <<= 1)
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int blk = g0 + i;
+            float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if ((i & h) == 0) {
-                    const float a = v[i], b = v[i + h];
-                    v[i] = a + b;
-                    v[i + h] = a - b;
+            for (int j = 0; j < kLoads; ++j) {
+                const uint32_t w[4] = {raw[i][j].x, raw[i][j].y, raw[i][j].z, raw[i][j].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (DT == kF32) {
+                        v[4 * j + k] = __uint_as_float(w[k]);
+                    } else if (DT == kBF16) {
+                        v[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
+                        v[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                    } else {
+                        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                        v[8 * j + 2 * k] = h.x;
+                        v[8 * j + 2 * k + 1] = h.y;
+                    }
                 }
-        const uint32_t half = operand + (uint32_t)(blk >> 1) * TcaShape<D>::kHalf;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t o[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const __half2 h = __floats2half2_rn(v[8 * j + 2 * k] * f, v[8 * j + 2 * k + 1] * f);
-                o[k] = *reinterpret_cast<const uint32_t *>(&h);
             }
-            a_sts128(swizzled(half, row, (blk & 1) * 4 + j), o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if (sign_mask((uint32_t)(32 * blk + e))) v[e] = -v[e];
+#pragma unroll
+            for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if ((e & h) == 0) {
+                        const float a = v[e], b = v[e + h];
+                        v[e] = a + b;
+                        v[e + h] = a - b;
+                    }
+            const uint32_t half = operand + (uint32_t)(blk >> 1) * TcaShape<D>::kHalf;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __half2 h = __floats2half2_rn(v[8 * j + 2 * k] * f, v[8 * j + 2 * k + 1] * f);
+                    o[k] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                a_sts128(swizzled(half, row, (blk & 1) * 4 + j), o);
+            }
         }
+    }
+}
+
+template <int DT, int D>
+__device__ __forceinline__ void rotate_part(const AttnParams &P, int64_t x, bool valid, uint32_t operand, int row,
+                                            bool pair, int s) {
+    const char *at = P.q + x * ElemSize<DT>::value;
+    constexpr int kBlocks = D / 32;
+    if (pair) {
+        rotate_row<DT, D, 0, kBlocks / 2>(P, at, valid, operand, row);
+        rotate_row<DT, D, kBlocks / 2, kBlocks>(P, at, valid, operand, row);
+    } else if (s == 0) {
+        rotate_row<DT, D, 0, kBlocks / 2>(P, at, valid, operand, row);
+    } else {
+        rotate_row<DT, D, kBlocks / 2, kBlocks>(P, at, valid, operand, row);
     }
 }
 
@@ -323,32 +377,30 @@ __device__ __forceinline__ uint64_t a_add2(uint64_t a, uint64_t b) {
 template <int D>
 __device__ __forceinline__ void rescale_row(uint32_t t_o, float f) {
 #pragma unroll 1
-    for (int k = 0; k < D; k += 32) {
-        uint32_t v[32];
-        a_ld32(t_o + (uint32_t)k, v);
+    for (int k = 0; k < D; k += 16) {  // (a whole row of scores is in registers meanwhile)
+        uint32_t v[16];
+        a_ld16(t_o + (uint32_t)k, v);
         a_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
         a_st16(t_o + (uint32_t)k, v);
-        a_st16(t_o + (uint32_t)k + 16, v + 16);
     }
 }
 
-// The maximum of 64 scores v and mx.
-__device__ __forceinline__ float max64(const uint32_t *v, float mx) {
+// The maximum of 128 scores v and mx.
+__device__ __forceinline__ float max128(const uint32_t *v, float mx) {
     float x[4] = {mx, kNoMax, kNoMax, kNoMax};
 #pragma unroll
-    for (int e = 0; e < 64; e += 2)
+    for (int e = 0; e < 128; e += 2)
         x[(e >> 1) & 3] = fmaxf(x[(e >> 1) & 3], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
     return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
 }
 
-// Weights of 2 N scores into N columns at t_p, their sum onto `sum`.
-template <int N>
-__device__ __forceinline__ void weights(uint32_t *v, uint64_t scale2, uint64_t off2, uint32_t t_p,
-                                        uint64_t (&sum)[2]) {
+// Weights of 128 scores into 64 columns at t_p, their sum onto `sum`.
+__device__ __forceinline__ void weights128(uint32_t *v, uint64_t scale2, uint64_t off2, uint32_t t_p,
+                                           uint64_t (&sum)[2]) {
 #pragma unroll
-    for (int e = 0; e < 2 * N; e += 2) {
+    for (int e = 0; e < 128; e += 2) {
         float a, b;
         a_unpack(a_fma2(a_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), scale2, off2), a, b);
         a = ex2(a);
@@ -380,29 +432,19 @@ __device__ __forceinline__ float sum_of(const uint64_t (&sum)[2]) {
     return (s0 + s1) + (s2 + s3);
 }
 
-// Scores at t_s to weights: those of columns 0..63 in columns 0..31, of 64..127
-// in 64..95, so that the upper half, which is in registers when the maximum is
-// known, can be written while the lower is still to be read again.
+// Scores at t_s to weights in the first half of their columns; the whole row is
+// in registers between.
 template <int D>
 __device__ __forceinline__ void softmax_row(uint32_t t_s, uint32_t t_o, float scale, bool have, float &m, float &l) {
-    uint32_t v[64];
-    a_ld32(t_s, v);
-    a_ld32(t_s + 32, v + 32);
+    uint32_t v[128];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a_ld32(t_s + 32u * k, v + 32 * k);
     a_wait_ld();
-    float mx = max64(v, m);
-    a_ld32(t_s + 64, v);
-    a_ld32(t_s + 96, v + 32);
-    a_wait_ld();
-    mx = max64(v, mx);
-    follow<D>(t_o, scale, have, mx, m, l);
+    follow<D>(t_o, scale, have, max128(v, m), m, l);
     const float off = kWeightExp - m * scale;
     const uint64_t scale2 = a_pack(scale, scale), off2 = a_pack(off, off);
     uint64_t sum[2] = {0, 0};
-    weights<32>(v, scale2, off2, t_s + 64, sum);
-    a_ld32(t_s, v);
-    a_ld32(t_s + 32, v + 32);
-    a_wait_ld();
-    weights<32>(v, scale2, off2, t_s, sum);
+    weights128(v, scale2, off2, t_s, sum);
     l += sum_of(sum);
     a_wait_st();
 }
@@ -453,7 +495,7 @@ __device__ __forceinline__ void softmax_row_masked(uint32_t t_s, uint32_t t_o, f
             const __half2 h = __floats2half2_rn(a, b);
             v[e / 2] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        a_st16(t_s + (k < 2 ? 16u * k : 32u + 16u * k), v);  // over scores that are read by now
+        a_st16(t_s + 16u * k, v);  // over scores that are read by now
     }
     a_wait_st();
 }
@@ -535,17 +577,16 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                 const int h = p.head * P.group_heads + (valid ? q_row % P.group_heads : 0);
                 const int64_t x = p.b * P.q_batch + t * P.q_token + h * P.q_head;
                 const uint32_t operand = base + S::kQ + (pair ? s : 0) * S::kOperand;
-                constexpr int kBlocks = D / 32;
-                const int b0 = pair ? 0 : s * (kBlocks / 2), b1 = pair ? kBlocks : (s + 1) * (kBlocks / 2);
-                if (P.qdtype == kF32) rotate_row<kF32, D>(P, P.q + x * 4, valid, operand, row, b0, b1);
-                else if (P.qdtype == kBF16) rotate_row<kBF16, D>(P, P.q + x * 2, valid, operand, row, b0, b1);
-                else rotate_row<kF16, D>(P, P.q + x * 2, valid, operand, row, b0, b1);
+                if (P.qdtype == kF32) rotate_part<kF32, D>(P, x, valid, operand, row, pair, s);
+                else if (P.qdtype == kBF16) rotate_part<kBF16, D>(P, x, valid, operand, row, pair, s);
+                else rotate_part<kF16, D>(P, x, valid, operand, row, pair, s);
                 a_proxy_fence();
             }
             a_named_sync(1, (kSoftWarps + 1) * 32);
 
             const int out_row = pair ? s * kRowTile + row : row;  // of the partial result
             const int unit_row = p.row0 + out_row;
+            const bool any_rows = unit_row - lane < P.rows;
             const TreeWords words(P, p.b, lane);
             const uint64_t see = words.of(min(unit_row / P.group_heads, P.tree - 1));
             const int32_t *table = P.c.page_table + p.b * P.c.table_ld;
@@ -565,7 +606,9 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                     break;
                 }
                 a_fence_after();
-                if (tail)
+                if (!any_rows) {
+                    // no row of this warp is asked for: whatever stands in its lanes stays there
+                } else if (tail)
                     softmax_row_masked<D>(t_s, t_o, P.scale_log2, seen_jobs > 0, p.len - tile * kTile, see, groups, m,
                                           l);
                 else
@@ -580,23 +623,33 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
             ++parts_done;
             if (ok) {
                 a_fence_after();
-                const bool store = unit_row < P.rows;
                 const int64_t slot = (p.unit + me) * P.parts + (pair ? 0 : s);
-                const int64_t at_row = slot * P.tile_rows + out_row;
-                if (store) reinterpret_cast<float2 *>(P.part_ml)[at_row] = make_float2(m, l);
-                if (seen_jobs > 0) {
+                const int64_t row0 = slot * P.tile_rows + out_row - lane;  // of this warp
+                if (unit_row < P.rows) reinterpret_cast<float2 *>(P.part_ml)[row0 + lane] = make_float2(m, l);
+                // rows leave through this warp's quarter of its stream's query
+                // tile (every product has read it), 32 elements of 32 rows at a
+                // time, so that a store covers whole 128-byte lines of four rows
+                const uint32_t stage = base + S::kQ + (uint32_t)s * S::kOperand + (uint32_t)(warp & 3) * 4096u;
+                const int rows = min(32, P.rows - (unit_row - lane));
 #pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t v[32];
-                        a_ld32(t_o + (uint32_t)k, v);
-                        a_wait_ld();
-                        if (store) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(P.part_o + at_row * D + k);
+                for (int k = 0; k < D && seen_jobs > 0 && any_rows; k += 32) {
+                    uint32_t v[32];
+                    a_ld32(t_o + (uint32_t)k, v);
+                    a_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                        }
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t w[4] = {v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+                        a_sts128(swizzled(stage, lane, j), w);
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = 4 * j + (lane >> 3);
+                        if (r < rows)
+                            *reinterpret_cast<uint4 *>(P.part_o + (row0 + r) * D + k + 4 * (lane & 7)) =
+                                a_lds128(swizzled(stage, r, lane & 7));
+                    }
+                    __syncwarp();
                 }
                 a_fence_before();
             }
@@ -612,11 +665,16 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
         while (ok && walk.next(P, p)) {
             const int32_t *table = P.c.page_table + p.b * P.c.table_ld;
             uint64_t present = 0;
-            if (p.tb * kTile > p.len) present = TreeWords(P, p.b, lane).present();
+            bool known = false;
             // a record that no row sees counts as zero whatever the memory holds
             auto page_of = [&](int tile) {
+                if (tile >= p.tb) return -1;
+                if (!known && tile * kTile + kTile > p.len) {
+                    present = TreeWords(P, p.b, lane).present();
+                    known = true;
+                }
                 const int place = tile * kTile + row, j = place - p.len;
-                if (tile >= p.tb || place >= p.n || (j >= 0 && !((present >> j) & 1ull))) return -1;
+                if (place >= p.n || (j >= 0 && !((present >> j) & 1ull))) return -1;
                 const int page = table[place >> shift];
                 return page < P.c.pages ? page : -1;
             };
@@ -624,9 +682,10 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                 return (((int64_t)page * 2 * P.c.kv_heads + p.head) << shift) + ((tile * kTile + row) & in_page);
             };
             TokenRegs<D> k, v;
-            int page = page_of(p.ta), next = page_of(p.ta + 1);
+            const int page = page_of(p.ta);
             load_token<D>(P, record(page, p.ta), page >= 0, k);
             load_token<D>(P, record(page, p.ta) + v_rows, page >= 0, v);
+            int next = page_of(p.ta + 1);
             for (int tile = p.ta; tile < p.tb; ++tile, ++tile_no) {
                 const uint32_t st = tile_no & 1u, parity = ((tile_no >> 1) & 1u) ^ 1u;
                 if (!a_mbar_wait_warp(bar(kKEmpty + st), parity)) {
@@ -655,49 +714,55 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
     } else {
         // ---- tensor-core issue -----------------------------------------------------
         a_regs_fewer<kIssueRegs>();
+        // The whole warp walks and waits, one elected lane issues: descriptors
+        // stay warp-uniform that way (uniform registers are what the
+        // instruction reads).  Broadcasts say so where values come from memory.
         uint32_t tile_no = 0, jobs_done[2] = {0, 0};  // before this part
+        const bool elected = a_elect();
+        const uint64_t q_desc = a_desc(base + S::kQ, 16), k_desc = a_desc(base + S::kK, 16);
+        const uint64_t v_desc = a_desc(base + S::kV, S::kHalf);
         while (walk.next(P, p)) {
             a_named_sync(1, (kSoftWarps + 1) * 32);  // the queries are in place
-            const int tiles = p.tb - p.ta, jobs = pair ? 2 * tiles : tiles;
-            if (lane == 0) {
-                auto stage = [&](int i) { return tile_no + (uint32_t)(pair ? i >> 1 : i); };
-                auto score = [&](int i) {
-                    const int s = i & 1;
-                    const uint32_t t = stage(i), st = t & 1u;
-                    if (!a_mbar_wait(bar(kKFull + st), (t >> 1) & 1u)) {
-                        give_up();
-                        return;
-                    }
-                    a_fence_after();
-                    const uint32_t q = base + S::kQ + (pair ? s : 0) * S::kOperand, k = base + S::kK + st * S::kOperand;
+            const int tiles = __shfl_sync(kFull, p.tb - p.ta, 0), jobs = pair ? 2 * tiles : tiles;
+            auto score = [&](int i) {
+                const uint32_t s = (uint32_t)i & 1u, t = tile_no + (uint32_t)(pair ? i >> 1 : i), st = t & 1u;
+                if (!a_mbar_wait_warp(bar(kKFull + st), (t >> 1) & 1u)) {
+                    give_up();
+                    return;
+                }
+                a_fence_after();
+                const uint64_t q = q_desc + (pair ? s : 0u) * (S::kOperand >> 4), k = k_desc + st * (S::kOperand >> 4);
+                if (elected) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {  // 16 elements: 32 bytes along the swizzled row
-                        const uint32_t o = (uint32_t)(kk >> 2) * S::kHalf + 32u * (kk & 3);
-                        a_mma_ss(tmem + 128u * s, a_desc(q + o, 16), a_desc(k + o, 16), S::kIdescS, kk != 0);
+                        const uint32_t o = ((uint32_t)(kk >> 2) * S::kHalf + 32u * (kk & 3)) >> 4;
+                        a_mma_ss(128u * s, q + o, k + o, S::kIdescS, kk != 0);
                     }
                     a_commit(bar(kSFull + s));
                     if (!pair || s == 1) a_commit(bar(kKEmpty + st));
-                };
-                for (int i = 0; i < 2 && i < jobs && ok; ++i) score(i);
-                for (int i = 0; i < jobs && ok; ++i) {
-                    const int s = i & 1;
-                    const uint32_t t = stage(i), st = t & 1u;
-                    if (!a_mbar_wait(bar(kPReady + s), (jobs_done[s] + (uint32_t)(i >> 1)) & 1u) ||
-                        !a_mbar_wait(bar(kVFull + st), (t >> 1) & 1u)) {
-                        give_up();
-                        break;
-                    }
-                    a_fence_after();
-                    const uint32_t v = base + S::kV + st * S::kOperand;
+                }
+                __syncwarp();
+            };
+            for (int i = 0; i < 2 && i < jobs && ok; ++i) score(i);
+            for (int i = 0; i < jobs && ok; ++i) {
+                const uint32_t s = (uint32_t)i & 1u, t = tile_no + (uint32_t)(pair ? i >> 1 : i), st = t & 1u;
+                if (!a_mbar_wait_warp(bar(kPReady + s), (jobs_done[s] + (uint32_t)(i >> 1)) & 1u) ||
+                    !a_mbar_wait_warp(bar(kVFull + st), (t >> 1) & 1u)) {
+                    give_up();
+                    break;
+                }
+                a_fence_after();
+                const uint64_t v = v_desc + st * (S::kOperand >> 4);
+                if (elected) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)  // 16 tokens: 8 columns of weights, 16 rows of V
-                        a_mma_ts(tmem + kOCol + 128u * s, tmem + 128u * s + 8u * kk + (kk >= 4 ? 32u : 0u), a_desc(v + 2048u * kk, S::kHalf),
-                                 S::kIdescO, i >= 2 || kk != 0);
+                        a_mma_ts(kOCol + 128u * s, 128u * s + 8u * kk, v + 128u * kk, S::kIdescO, i >= 2 || kk != 0);
                     if (!pair || s == 1) a_commit(bar(kVEmpty + st));
-                    if (i + 2 < jobs) score(i + 2);
                 }
-                a_commit(bar(kODone));  // all of this part's products
+                __syncwarp();
+                if (i + 2 < jobs) score(i + 2);
             }
+            if (elected) a_commit(bar(kODone));  // all of this part's products
             __syncwarp();
             tile_no += (uint32_t)tiles;
             jobs_done[0] += (uint32_t)((jobs + 1) / 2);
@@ -709,7 +774,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
     a_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
-        if (*aborted && lane == 0) {  // nothing may be in flight; bounded like every wait
+        if (*aborted && a_elect()) {  // nothing may be in flight; bounded like every wait
             a_fence_after();
             a_mbar_init(bar(14), 1);
             a_commit(bar(14));
