@@ -401,8 +401,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
     const int me = warp * gridDim.x + blockIdx.x;
     if (me >= workers) return;
     const LaneOffsets<DP, FULL> off(P.c.head_dim, lane);
-    int64_t at = W * me / workers;
-    const int64_t end = W * (me + 1) / workers;
+    int64_t at = quotient(W * me, workers);
+    const int64_t end = quotient(W * (me + 1), workers);
 
     while (at < end) {
         // the unit that holds group `at`
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
         }
         const int b = lo, groups = sh.prefix[b + 1] - sh.prefix[b];
         const int64_t in_seq = at - (int64_t)sh.prefix[b] * per_seq;
-        const int hr = (int)(in_seq / groups);
+        const int hr = (int)quotient(in_seq, groups);
         const int head = hr / P.row_tiles, row0 = (hr % P.row_tiles) * NT * 8;
         const int ga = (int)(in_seq - (int64_t)hr * groups);
         const int gb = (int)min((int64_t)groups, ga + (end - at));
@@ -539,6 +539,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
         // this part of the unit: maxima and sums, and DP / 8 neighbouring
         // elements of two rows for each lane
         const int64_t slot = (int64_t)b * per_seq + hr + me;
+        uint64_t present = ~0ull;
+        if (P.parents) present = TreeWords(P, b, lane).present();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -547,6 +549,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 #pragma unroll
                 for (int x = 4; x <= 16; x <<= 1) l += __shfl_xor_sync(kFull, l, x);
                 const int r = 8 * n + 2 * c + k;
+                // a token that is not there answers zero
+                if (row0 + r < P.rows && !((present >> ((row0 + r) / P.group_heads)) & 1ull)) l = 0.f;
                 if (row0 + r < P.rows) {
                     const int64_t at_row = slot * (NT * 8) + r;
                     if (g == 0) reinterpret_cast<float2 *>(P.part_ml)[at_row] = make_float2(st.m[n][k], l);
@@ -566,27 +570,25 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 
 // ---------------------------------------------------------------------------
 // The parts of each row joined, rotated back, divided and rounded.  CTAs of
-// eight warps: RW of them share a row's parts, and the first of those adds up
-// and finishes.
+// eight warps.  RW = 8: the warps share one row's parts, and the first adds up
+// and finishes.  RW = 1: a warp takes kJoinRows neighbouring rows, which have
+// the same parts, so that finding them and waiting for them is paid once.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
-
-// a / b of non-negative numbers, in 32 bits where both fit
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
+constexpr int kJoinRows = 4;
 
 template <int OT, int RW>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P) {
+    constexpr int R = RW == 1 ? kJoinRows : 1;
     __shared__ float so[RW == 1 ? 1 : kJoinWarps][256];
     __shared__ float sl[kJoinWarps];
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t all_rows = (int64_t)P.c.batch * P.c.kv_heads * P.rows;
+    const int quads = (P.rows + R - 1) / R;  // (a tile's rows are a multiple of R)
     const int64_t index = (int64_t)blockIdx.x * (kJoinWarps / RW) + warp / RW;
-    if (index >= all_rows) return;  // (whole CTAs where RW > 1: one row each)
-    const int row = (int)(index % P.rows);
-    const int bh = (int)(index / P.rows);
+    if (index >= (int64_t)P.c.batch * P.c.kv_heads * quads) return;  // (whole CTAs where RW > 1)
+    const int row = (int)(index % quads) * R;
+    const int bh = (int)(index / quads);
     const int b = bh / P.c.kv_heads, head = bh % P.c.kv_heads;
     const int tile = row / P.tile_rows, r = row % P.tile_rows;
     const int per_seq = P.c.kv_heads * P.row_tiles;
@@ -599,31 +601,50 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     const int64_t i0 = quotient((first + 1) * workers - 1, W), i1 = quotient((first + groups) * workers - 1, W);
     const int64_t unit = (int64_t)b * per_seq + hr;
     const int64_t s0 = (unit + i0) * P.parts, s1 = (unit + i1 + 1) * P.parts;  // its slots
-    const float2 *ml = reinterpret_cast<const float2 *>(P.part_ml);
-
-    float mx = kNoMax;
-    for (int64_t i = s0 + lane; i < s1; i += 32) mx = fmaxf(mx, ml[i * P.tile_rows + r].x);
-#pragma unroll
-    for (int k = 16; k >= 1; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, k));
+    const float2 *ml = reinterpret_cast<const float2 *>(P.part_ml) + r;
     const int D = P.c.head_dim;
-    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    float l = 0.f;
-#pragma unroll 4
-    for (int64_t i = s0 + warp % RW; i < s1; i += RW) {
-        const int64_t s = i * P.tile_rows + r;
-        const float2 p = ml[s];
-        if (p.y == 0.f) continue;  // nothing seen there
-        const float f = ex2((p.x - mx) * P.scale_log2);
-        l += f * p.y;
+
+    // (rows past the last are read, within the tile, and dropped)
+    float mx[R];
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb) {
-            const int e = sb * 128 + 4 * lane;
-            if (e < D) {
-                const float4 o = *reinterpret_cast<const float4 *>(P.part_o + s * D + e);
-                acc[sb][0] += f * o.x;
-                acc[sb][1] += f * o.y;
-                acc[sb][2] += f * o.z;
-                acc[sb][3] += f * o.w;
+    for (int k = 0; k < R; ++k) mx[k] = kNoMax;
+    if (RW == 1) {
+        for (int64_t i = s0; i < s1; ++i)
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                if (row + k < P.rows) mx[k] = fmaxf(mx[k], ml[i * P.tile_rows + k].x);
+    } else {
+        for (int64_t i = s0 + lane; i < s1; i += 32) mx[0] = fmaxf(mx[0], ml[i * P.tile_rows].x);
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) mx[0] = fmaxf(mx[0], __shfl_xor_sync(kFull, mx[0], k));
+    }
+    float acc[R][2][4], l[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        l[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[k][0][i] = acc[k][1][i] = 0.f;
+    }
+#pragma unroll 2
+    for (int64_t i = s0 + warp % RW; i < s1; i += RW) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (row + k >= P.rows) break;
+            const float2 p = ml[i * P.tile_rows + k];
+            if (p.y == 0.f) continue;  // nothing seen there (its values may never have been written)
+            const float f = ex2((p.x - mx[k]) * P.scale_log2);
+            l[k] += f * p.y;
+            const float *src = P.part_o + (i * P.tile_rows + r + k) * D;
+#pragma unroll
+            for (int sb = 0; sb < 2; ++sb) {
+                const int e = sb * 128 + 4 * lane;
+                if (e < D) {
+                    const float4 o = *reinterpret_cast<const float4 *>(src + e);
+                    acc[k][sb][0] += f * o.x;
+                    acc[k][sb][1] += f * o.y;
+                    acc[k][sb][2] += f * o.z;
+                    acc[k][sb][3] += f * o.w;
+                }
             }
         }
     }
@@ -631,38 +652,43 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb)
             *reinterpret_cast<float4 *>(&so[warp][sb * 128 + 4 * lane]) =
-                make_float4(acc[sb][0], acc[sb][1], acc[sb][2], acc[sb][3]);
-        if (lane == 0) sl[warp] = l;
+                make_float4(acc[0][sb][0], acc[0][sb][1], acc[0][sb][2], acc[0][sb][3]);
+        if (lane == 0) sl[warp] = l[0];
         __syncthreads();
         if (warp != 0) return;
-        l = 0.f;
+        l[0] = 0.f;
 #pragma unroll
-        for (int w = 0; w < RW; ++w) l += sl[w];
+        for (int w = 0; w < RW; ++w) l[0] += sl[w];
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                acc[sb][i] = 0.f;
+                acc[0][sb][i] = 0.f;
 #pragma unroll
-                for (int w = 0; w < RW; ++w) acc[sb][i] += so[w][sb * 128 + 4 * lane + i];
+                for (int w = 0; w < RW; ++w) acc[0][sb][i] += so[w][sb * 128 + 4 * lane + i];
             }
     }
-    const int t = row / P.group_heads, h = head * P.group_heads + row % P.group_heads;
-    // a token that is not there answers zero
-    const bool there = !P.parents || ((TreeWords(P, b, lane).present() >> t) & 1ull);
-    const float inv = there && l > 0.f ? 0.03125f / l : 0.f;
-    char *out = P.out + (b * P.o_batch + t * P.o_token + h * P.o_head) * ElemSize<OT>::value;
+    uint32_t flips[2];
 #pragma unroll
-    for (int sb = 0; sb < 2; ++sb) {
-        const int e = sb * 128 + 4 * lane;
-        if (sb * 128 >= D) break;
-        float v[4];
+    for (int sb = 0; sb < 2; ++sb) flips[sb] = c_sign_words.w[sb * 4 + lane / 8] >> (4 * (lane & 7));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = acc[sb][i] * inv;
-        fwht32_warp(v, lane & 7);
+    for (int k = 0; k < R; ++k) {
+        if (row + k >= P.rows) break;
+        const int t = (row + k) / P.group_heads, h = head * P.group_heads + (row + k) % P.group_heads;
+        const float inv = l[k] > 0.f ? 0.03125f / l[k] : 0.f;
+        char *out = P.out + (b * P.o_batch + t * P.o_token + h * P.o_head) * ElemSize<OT>::value;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = flip(v[i], sign_mask(e + i));
-        if (e < D) store4<OT>(out + (int64_t)e * ElemSize<OT>::value, v);
+        for (int sb = 0; sb < 2; ++sb) {
+            if (sb * 128 >= D) break;
+            const int e = sb * 128 + 4 * lane;
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = acc[k][sb][i] * inv;
+            fwht32_warp(v, lane & 7);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = flip(v[i], (flips[sb] << (31 - i)) & 0x80000000u);
+            if (e < D) store4<OT>(out + (int64_t)e * ElemSize<OT>::value, v);
+        }
     }
 }
 
@@ -719,8 +745,9 @@ cudaError_t launch_attend(const AttnParams &P, cudaStream_t stream) {
 template <int OT, int RW>
 cudaError_t launch_join_as(const AttnParams &P, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    const int64_t rows = (int64_t)P.c.batch * P.c.kv_heads * P.rows;
-    cfg.gridDim = dim3((unsigned)((rows * RW + kJoinWarps - 1) / kJoinWarps));
+    constexpr int R = RW == 1 ? kJoinRows : 1;
+    const int64_t items = (int64_t)P.c.batch * P.c.kv_heads * ((P.rows + R - 1) / R);
+    cfg.gridDim = dim3((unsigned)((items * RW + kJoinWarps - 1) / kJoinWarps));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr;

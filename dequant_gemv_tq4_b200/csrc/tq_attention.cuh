@@ -11,6 +11,23 @@
 
 namespace tq {
 
+// The codec's signs of the head's columns, a bit per column (1 = negative).
+struct SignWords {
+    uint32_t w[8];
+};
+constexpr SignWords sign_words() {
+    SignWords s = {};
+    for (uint32_t k = 0; k < 256; ++k) {
+        uint32_t h = k * 0x9E3779B9u;
+        h ^= h >> 16;
+        h *= 0x85EBCA6Bu;
+        h ^= h >> 13;
+        s.w[k / 32] |= (h >> 31) << (k % 32);
+    }
+    return s;
+}
+static __constant__ SignWords c_sign_words = sign_words();
+
 constexpr float kWeightExp = 7.0f;  // softmax weights are held times 2^7
 constexpr float kLazy = 8.0f;       // log2 by which a maximum may grow before it is followed
 constexpr float kNoMax = -1e30f;    // maximum of a row without a token so far (its sum is 0)
@@ -52,6 +69,11 @@ __device__ __forceinline__ int seq_tokens(const AttnParams &P, int len) {
 __device__ __forceinline__ int worker_count(const AttnParams &P, int64_t W) {
     const int64_t n = (W + P.least - 1) / P.least;
     return (int)(n < P.workers ? n : P.workers);
+}
+
+// a / b of non-negative numbers, in 32 bits where both fit
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -7,9 +7,10 @@
 // memory.  With more than 128 rows the streams are two row tiles over the same
 // tokens (records are decoded once for 256 rows); with fewer they take even
 // and odd token tiles of one row tile and leave two partial results.
-//   decode warps   codes to fp16 centroid x scale, keys and values, into the
-//                  128-byte-swizzled operand layout (two stages each)
-//   one thread     issues S = Q K^T (both operands in shared memory, K-major)
+//   decode warps   codes to fp16 centroid x scale into the 128-byte-swizzled
+//                  operand layout, two stages of 128 tokens for keys and for
+//                  values; seven warps take pieces of 32 tokens in turn
+//   one warp       issues S = Q K^T (both operands in shared memory, K-major)
 //                  and O += P V (P from tensor memory, V as it was written,
 //                  tokens as rows: the instruction takes it N-major)
 //   softmax warps  one thread per row: scores from tensor memory, running
@@ -25,13 +26,14 @@ namespace {
 constexpr int kTile = 128;      // tokens of a tile
 constexpr int kRowTile = 128;   // rows of a stream
 constexpr int kSoftWarps = 8;   // warps 0..7: four per stream
-constexpr int kDecodeWarps = 4; // warps 8..11
-constexpr int kMmaWarp = kSoftWarps + kDecodeWarps;
-constexpr int kTcaThreads = 512;  // four warpgroups; warps 13..15 only release their registers
+constexpr int kDecodeWarps = 7; // warps 8..11 and 13..15
+constexpr int kMmaWarp = 12;    // issue
+constexpr int kTcaThreads = 512;
+constexpr int kPieces = 8;      // of a tile: 32 tokens' keys or values
 // Registers a thread: 128 at launch; the softmax holds a whole row of scores.
-// Shares of the launch's 65536: 256 * 184 + 128 * 88 + 128 * 56 = 65536.
-constexpr int kSoftRegs = 184, kDecodeRegs = 88, kIssueRegs = 56;
-static_assert(256 * kSoftRegs + 128 * kDecodeRegs + 128 * kIssueRegs <= kTcaThreads * 128, "register shares");
+// Shares of the launch's 65536: 256 * 184 + 256 * 72 = 65536.
+constexpr int kSoftRegs = 184, kOtherRegs = 72;
+static_assert(256 * kSoftRegs + 256 * kOtherRegs <= kTcaThreads * 128, "register shares");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kOCol = 256;  // output accumulators; scores at 0 and 128
 constexpr long long kTimeoutCycles = 2000000000ll;  // about a second
@@ -48,7 +50,6 @@ struct TcaShape {
     static constexpr uint32_t kV = kK + 2 * kOperand;   // two stages
     static constexpr uint32_t kBars = kV + 2 * kOperand;
     static constexpr uint32_t kTmemSlot = kBars + 8 * 16;
-    static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kScan = kTmemSlot + 16;
     static constexpr uint32_t kPrefix = kScan + 32 * 4;
     static constexpr uint32_t kEnd = kPrefix + (kAttnMaxBatch + 1) * 4;
@@ -61,7 +62,7 @@ struct TcaShape {
 };
 
 // barriers
-enum : int { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kODone = 12 };
+enum : int { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kODone = 12, kLast = 13 };
 
 // ---- PTX wrappers ------------------------------------------------------------
 template <int N>
@@ -210,7 +211,7 @@ struct Walk {  // the parts of a worker's range, the same for every warp
         }
         const int tiles = prefix[lo + 1] - prefix[lo];
         const int64_t in_seq = at - (int64_t)prefix[lo] * per_seq;
-        const int hr = (int)(in_seq / tiles);
+        const int hr = (int)quotient(in_seq, tiles);
         p.b = lo;
         p.head = hr / P.row_tiles;
         p.row0 = hr % P.row_tiles * P.tile_rows;
@@ -226,7 +227,7 @@ struct Walk {  // the parts of a worker's range, the same for every warp
 };
 
 // ---- decode: codes of one token's D / 2 elements to swizzled fp16 ------------
-// Thread td of the 128 owns token td of every tile: D / 32 blocks of 32 elements.
+// A lane owns one token of a piece: D / 32 blocks of 32 elements.
 template <int D>
 struct TokenRegs {
     uint4 w[D / 32];
@@ -273,82 +274,45 @@ __device__ __forceinline__ void decode_token(const TokenRegs<D> &r, uint32_t ope
 }
 
 // ---- query rows: rotated, fp16, swizzled ---------------------------------------
-// Blocks [B0, B1) of a row: all loads first; the signs are compile-time
-// constants and vanish into the first butterflies.
-template <int DT, int D, int B0, int B1>
-__device__ __forceinline__ void rotate_row(const AttnParams &P, const char *x, bool valid, uint32_t operand, int row) {
+// Blocks [b0, b1) of a row, one at a time: what runs once per part costs the
+// fetch of its code more than its arithmetic.
+template <int DT, int D>
+__device__ __forceinline__ void rotate_row(const AttnParams &P, int64_t x, bool valid, uint32_t operand, int row,
+                                           int b0, int b1) {
+    constexpr int E = ElemSize<DT>::value;
+    const char *at = P.q + x * E;
     const float f = P.negative ? -0.03125f : 0.03125f;
-    constexpr int E = ElemSize<DT>::value, kLoads = 2 * E;  // 16-byte loads of a block
-    constexpr int kAtOnce = DT == kF32 ? 1 : B1 - B0;       // blocks loaded ahead
+#pragma unroll 1
+    for (int blk = b0; blk < b1; ++blk) {
+        const uint32_t bits = c_sign_words.w[blk];
+        float v[32];
 #pragma unroll
-    for (int g0 = B0; g0 < B1; g0 += kAtOnce) {
-        uint4 raw[kAtOnce][kLoads];
+        for (int i = 0; i < 32; i += 4) {
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            if (valid) load4<DT>(at + (int64_t)(32 * blk + i) * E, t);
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i)
+            for (int k = 0; k < 4; ++k) v[i + k] = flip(t[k], (bits << (31 - i - k)) & 0x80000000u);
+        }
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j)
-                raw[i][j] = valid ? __ldg(reinterpret_cast<const uint4 *>(x + (g0 + i) * 32 * E) + j)
-                                  : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const int blk = g0 + i;
-            float v[32];
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const uint32_t w[4] = {raw[i][j].x, raw[i][j].y, raw[i][j].z, raw[i][j].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (DT == kF32) {
-                        v[4 * j + k] = __uint_as_float(w[k]);
-                    } else if (DT == kBF16) {
-                        v[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
-                        v[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-                    } else {
-                        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
-                        v[8 * j + 2 * k] = h.x;
-                        v[8 * j + 2 * k + 1] = h.y;
-                    }
-                }
-            }
+        for (int h = 1; h < 32; h <<= 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-                if (sign_mask((uint32_t)(32 * blk + e))) v[e] = -v[e];
-#pragma unroll
-            for (int h = 1; h < 32; h <<= 1)
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if ((e & h) == 0) {
-                        const float a = v[e], b = v[e + h];
-                        v[e] = a + b;
-                        v[e + h] = a - b;
-                    }
-            const uint32_t half = operand + (uint32_t)(blk >> 1) * TcaShape<D>::kHalf;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __half2 h = __floats2half2_rn(v[8 * j + 2 * k] * f, v[8 * j + 2 * k + 1] * f);
-                    o[k] = *reinterpret_cast<const uint32_t *>(&h);
+                if ((e & h) == 0) {
+                    const float a = v[e], b = v[e + h];
+                    v[e] = a + b;
+                    v[e + h] = a - b;
                 }
-                a_sts128(swizzled(half, row, (blk & 1) * 4 + j), o);
+        const uint32_t half = operand + (uint32_t)(blk >> 1) * TcaShape<D>::kHalf;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __half2 h = __floats2half2_rn(v[8 * j + 2 * k] * f, v[8 * j + 2 * k + 1] * f);
+                o[k] = *reinterpret_cast<const uint32_t *>(&h);
             }
+            a_sts128(swizzled(half, row, (blk & 1) * 4 + j), o);
         }
-    }
-}
-
-template <int DT, int D>
-__device__ __forceinline__ void rotate_part(const AttnParams &P, int64_t x, bool valid, uint32_t operand, int row,
-                                            bool pair, int s) {
-    const char *at = P.q + x * ElemSize<DT>::value;
-    constexpr int kBlocks = D / 32;
-    if (pair) {
-        rotate_row<DT, D, 0, kBlocks / 2>(P, at, valid, operand, row);
-        rotate_row<DT, D, kBlocks / 2, kBlocks>(P, at, valid, operand, row);
-    } else if (s == 0) {
-        rotate_row<DT, D, 0, kBlocks / 2>(P, at, valid, operand, row);
-    } else {
-        rotate_row<DT, D, kBlocks / 2, kBlocks>(P, at, valid, operand, row);
     }
 }
 
@@ -510,22 +474,21 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(kFull, tid >> 5, 0);
     int *prefix = reinterpret_cast<int *>(smem + S::kPrefix);
-    volatile int *aborted = reinterpret_cast<volatile int *>(smem + S::kAbort);
     auto bar = [&](int i) { return base + S::kBars + 8u * (uint32_t)i; };
     grid_dependents_launch();  // the joining launch; it waits for this one's end
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            a_mbar_init(bar(kKFull + i), kDecodeWarps);
+            a_mbar_init(bar(kKFull + i), kPieces / 2);
             a_mbar_init(bar(kKEmpty + i), 1);
-            a_mbar_init(bar(kVFull + i), kDecodeWarps);
+            a_mbar_init(bar(kVFull + i), kPieces / 2);
             a_mbar_init(bar(kVEmpty + i), 1);
             a_mbar_init(bar(kSFull + i), 1);
             a_mbar_init(bar(kPReady + i), kSoftWarps / 2);
         }
         a_mbar_init(bar(kODone), 1);
+        a_mbar_init(bar(kLast), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *aborted = 0;
         if (blockIdx.x == 0) P.header[0] = 0u;  // status of this call: set, if at all, a second from now
     }
     if (warp == kMmaWarp) {
@@ -549,13 +512,12 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
         for (int i = tid; i <= P.c.batch; i += kTcaThreads) P.prefix[i] = prefix[i];
     const int workers = worker_count(P, W);
     const int me = blockIdx.x;
-    walk.at = me < workers ? W * me / workers : 0;
-    walk.end = me < workers ? W * (me + 1) / workers : 0;
+    walk.at = me < workers ? quotient(W * me, workers) : 0;
+    walk.end = me < workers ? quotient(W * (me + 1), workers) : 0;
     const bool pair = P.tile_rows == 2 * kRowTile;  // the streams are two row tiles
     bool ok = tmem_ok;
     auto give_up = [&]() {
         ok = false;
-        *aborted = 1;
         atomicOr(P.header, kStatusTimeout);
     };
     Part p;
@@ -577,9 +539,11 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                 const int h = p.head * P.group_heads + (valid ? q_row % P.group_heads : 0);
                 const int64_t x = p.b * P.q_batch + t * P.q_token + h * P.q_head;
                 const uint32_t operand = base + S::kQ + (pair ? s : 0) * S::kOperand;
-                if (P.qdtype == kF32) rotate_part<kF32, D>(P, x, valid, operand, row, pair, s);
-                else if (P.qdtype == kBF16) rotate_part<kBF16, D>(P, x, valid, operand, row, pair, s);
-                else rotate_part<kF16, D>(P, x, valid, operand, row, pair, s);
+                constexpr int kBlocks = D / 32;
+                const int b0 = pair ? 0 : s * (kBlocks / 2), b1 = pair ? kBlocks : b0 + kBlocks / 2;
+                if (P.qdtype == kF32) rotate_row<kF32, D>(P, x, valid, operand, row, b0, b1);
+                else if (P.qdtype == kBF16) rotate_row<kBF16, D>(P, x, valid, operand, row, b0, b1);
+                else rotate_row<kF16, D>(P, x, valid, operand, row, b0, b1);
                 a_proxy_fence();
             }
             a_named_sync(1, (kSoftWarps + 1) * 32);
@@ -625,7 +589,9 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                 a_fence_after();
                 const int64_t slot = (p.unit + me) * P.parts + (pair ? 0 : s);
                 const int64_t row0 = slot * P.tile_rows + out_row - lane;  // of this warp
-                if (unit_row < P.rows) reinterpret_cast<float2 *>(P.part_ml)[row0 + lane] = make_float2(m, l);
+                // a token that is not there answers zero
+                if (unit_row < P.rows)
+                    reinterpret_cast<float2 *>(P.part_ml)[row0 + lane] = make_float2(m, see == 0 ? 0.f : l);
                 // rows leave through this warp's quarter of its stream's query
                 // tile (every product has read it), 32 elements of 32 rows at a
                 // time, so that a store covers whole 128-byte lines of four rows
@@ -655,65 +621,67 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
             }
             a_named_sync(1, (kSoftWarps + 1) * 32);  // the queries may be replaced
         }
-    } else if (warp < kMmaWarp) {
+    } else if (warp != kMmaWarp) {
         // ---- decode ------------------------------------------------------------------
-        a_regs_fewer<kDecodeRegs>();
-        const int row = tid - kSoftWarps * 32;
+        a_regs_fewer<kOtherRegs>();
+        const int first = warp < kMmaWarp ? warp - kSoftWarps : warp - kSoftWarps - 1;  // of this warp's pieces
         const int shift = P.c.page_shift, in_page = (1 << shift) - 1;
-        const int64_t v_rows = (int64_t)P.c.kv_heads << shift;
-        uint32_t tile_no = 0;
+        const int v_rows = P.c.kv_heads << shift;
+        uint32_t tile_no = 0, piece = (uint32_t)first;  // of the walk
         while (ok && walk.next(P, p)) {
             const int32_t *table = P.c.page_table + p.b * P.c.table_ld;
+            const uint32_t end = (tile_no + (uint32_t)(p.tb - p.ta)) * kPieces;
             uint64_t present = 0;
             bool known = false;
-            // a record that no row sees counts as zero whatever the memory holds
-            auto page_of = [&](int tile) {
-                if (tile >= p.tb) return -1;
-                if (!known && tile * kTile + kTile > p.len) {
+            // piece i: tile i / 8 of the walk, its keys or values, 32 rows
+            auto place_of = [&](uint32_t i) {
+                return (p.ta + (int)(i / kPieces - tile_no)) * kTile + (int)(i & 3u) * 32 + lane;
+            };
+            // Page of this lane's token; none for a record that no row sees, which
+            // then counts as zero whatever the memory holds.
+            auto page_of = [&](uint32_t i) {
+                if (i >= end) return -1;
+                const int place = place_of(i), j = place - p.len;
+                if (!known && place - lane + 32 > p.len) {
                     present = TreeWords(P, p.b, lane).present();
                     known = true;
                 }
-                const int place = tile * kTile + row, j = place - p.len;
                 if (place >= p.n || (j >= 0 && !((present >> j) & 1ull))) return -1;
                 const int page = table[place >> shift];
                 return page < P.c.pages ? page : -1;
             };
-            auto record = [&](int page, int tile) {
-                return (((int64_t)page * 2 * P.c.kv_heads + p.head) << shift) + ((tile * kTile + row) & in_page);
-            };
-            TokenRegs<D> k, v;
-            const int page = page_of(p.ta);
-            load_token<D>(P, record(page, p.ta), page >= 0, k);
-            load_token<D>(P, record(page, p.ta) + v_rows, page >= 0, v);
-            int next = page_of(p.ta + 1);
-            for (int tile = p.ta; tile < p.tb; ++tile, ++tile_no) {
-                const uint32_t st = tile_no & 1u, parity = ((tile_no >> 1) & 1u) ^ 1u;
-                if (!a_mbar_wait_warp(bar(kKEmpty + st), parity)) {
-                    give_up();
-                    break;
+            TokenRegs<D> r;
+            int page = page_of(piece);
+#pragma unroll 1
+            for (bool begun = false; piece < end || !begun; begun = true) {
+                // the record of this piece is decoded, the next one's loaded, the page of
+                // the one after looked up (the first step only loads)
+                if (begun) {
+                    const uint32_t t = piece / kPieces, st = t & 1u;
+                    const bool values = piece & 4u;
+                    if (!a_mbar_wait_warp(bar((values ? kVEmpty : kKEmpty) + (int)st), ((t >> 1) & 1u) ^ 1u)) {
+                        give_up();
+                        break;
+                    }
+                    decode_token<D>(r, base + (values ? S::kV : S::kK) + st * S::kOperand,
+                                    (int)(piece & 3u) * 32 + lane);
+                    a_proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) a_arrive(bar((values ? kVFull : kKFull) + (int)st));
+                    piece += kDecodeWarps;
                 }
-                decode_token<D>(k, base + S::kK + st * S::kOperand, row);
-                a_proxy_fence();
-                __syncwarp();
-                if (lane == 0) a_arrive(bar(kKFull + st));
-                load_token<D>(P, record(next, tile + 1), next >= 0, k);
-                if (!a_mbar_wait_warp(bar(kVEmpty + st), parity)) {
-                    give_up();
-                    break;
+                if (piece < end) {
+                    const int64_t rec = (((int64_t)page * 2 * P.c.kv_heads + p.head) << shift) +
+                                        (piece & 4u ? v_rows : 0) + (place_of(piece) & in_page);
+                    load_token<D>(P, rec, page >= 0, r);
                 }
-                decode_token<D>(v, base + S::kV + st * S::kOperand, row);
-                a_proxy_fence();
-                __syncwarp();
-                if (lane == 0) a_arrive(bar(kVFull + st));
-                load_token<D>(P, record(next, tile + 1) + v_rows, next >= 0, v);
-                next = page_of(tile + 2);
+                page = page_of(piece + kDecodeWarps);
             }
+            tile_no = end / kPieces;
         }
-    } else if (warp != kMmaWarp) {
-        a_regs_fewer<kIssueRegs>();
     } else {
         // ---- tensor-core issue -----------------------------------------------------
-        a_regs_fewer<kIssueRegs>();
+        a_regs_fewer<kOtherRegs>();
         // The whole warp walks and waits, one elected lane issues: descriptors
         // stay warp-uniform that way (uniform registers are what the
         // instruction reads).  Broadcasts say so where values come from memory.
@@ -726,7 +694,8 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
             const int tiles = __shfl_sync(kFull, p.tb - p.ta, 0), jobs = pair ? 2 * tiles : tiles;
             auto score = [&](int i) {
                 const uint32_t s = (uint32_t)i & 1u, t = tile_no + (uint32_t)(pair ? i >> 1 : i), st = t & 1u;
-                if (!a_mbar_wait_warp(bar(kKFull + st), (t >> 1) & 1u)) {
+                // (the second stream of a pair finds the keys that the first waited for)
+                if (!(pair && s) && !a_mbar_wait_warp(bar(kKFull + st), (t >> 1) & 1u)) {
                     give_up();
                     return;
                 }
@@ -746,8 +715,9 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
             for (int i = 0; i < 2 && i < jobs && ok; ++i) score(i);
             for (int i = 0; i < jobs && ok; ++i) {
                 const uint32_t s = (uint32_t)i & 1u, t = tile_no + (uint32_t)(pair ? i >> 1 : i), st = t & 1u;
-                if (!a_mbar_wait_warp(bar(kPReady + s), (jobs_done[s] + (uint32_t)(i >> 1)) & 1u) ||
-                    !a_mbar_wait_warp(bar(kVFull + st), (t >> 1) & 1u)) {
+                const uint32_t parity = ((s ? jobs_done[1] : jobs_done[0]) + (uint32_t)(i >> 1)) & 1u;
+                if ((!(pair && s) && !a_mbar_wait_warp(bar(kVFull + st), (t >> 1) & 1u)) ||
+                    !a_mbar_wait_warp(bar(kPReady + s), parity)) {
                     give_up();
                     break;
                 }
@@ -769,17 +739,18 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
             jobs_done[1] += (uint32_t)(jobs / 2);
             a_named_sync(1, (kSoftWarps + 1) * 32);  // results are read
         }
+        if (!ok) {  // nothing may be in flight at the end; bounded like every wait
+            if (elected) {
+                a_commit(bar(kLast));
+                a_mbar_wait(bar(kLast), 0u);
+            }
+            __syncwarp();
+        }
     }
     // ---- teardown ---------------------------------------------------------------
     a_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
-        if (*aborted && a_elect()) {  // nothing may be in flight; bounded like every wait
-            a_fence_after();
-            a_mbar_init(bar(14), 1);
-            a_commit(bar(14));
-            a_mbar_wait(bar(14), 0u);
-        }
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
