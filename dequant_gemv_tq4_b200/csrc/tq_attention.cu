@@ -581,71 +581,81 @@ template <int OT, int RW>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P) {
     constexpr int R = RW == 1 ? kJoinRows : 1;
     __shared__ float so[RW == 1 ? 1 : kJoinWarps][256];
-    __shared__ float sl[kJoinWarps];
+    __shared__ float sl[kJoinWarps], sm[kJoinWarps];
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int quads = (P.rows + R - 1) / R;  // (a tile's rows are a multiple of R)
-    const int64_t index = (int64_t)blockIdx.x * (kJoinWarps / RW) + warp / RW;
-    if (index >= (int64_t)P.c.batch * P.c.kv_heads * quads) return;  // (whole CTAs where RW > 1)
-    const int row = (int)(index % quads) * R;
-    const int bh = (int)(index / quads);
+    const int index = (int)blockIdx.x * (kJoinWarps / RW) + warp / RW;
+    if (index >= P.c.batch * P.c.kv_heads * quads) return;  // (whole CTAs where RW > 1)
+    const int bh = index / quads, row = index % quads * R;
     const int b = bh / P.c.kv_heads, head = bh % P.c.kv_heads;
     const int tile = row / P.tile_rows, r = row % P.tile_rows;
     const int per_seq = P.c.kv_heads * P.row_tiles;
+    const int at = P.prefix[b], groups = P.prefix[b + 1] - at;
     const int64_t W = (int64_t)P.prefix[P.c.batch] * per_seq;
     const int workers = worker_count(P, W);
     const int hr = head * P.row_tiles + tile;
-    const int groups = P.prefix[b + 1] - P.prefix[b];
-    const int64_t first = (int64_t)P.prefix[b] * per_seq + (int64_t)hr * groups;
+    const int64_t first = (int64_t)at * per_seq + (int64_t)hr * groups;
     // the worker of group x: the largest i with i W / workers <= x
     const int64_t i0 = quotient((first + 1) * workers - 1, W), i1 = quotient((first + groups) * workers - 1, W);
-    const int64_t unit = (int64_t)b * per_seq + hr;
-    const int64_t s0 = (unit + i0) * P.parts, s1 = (unit + i1 + 1) * P.parts;  // its slots
-    const float2 *ml = reinterpret_cast<const float2 *>(P.part_ml) + r;
+    const int64_t s0 = ((int64_t)b * per_seq + hr + i0) * P.parts;  // the unit's first slot
+    const int n = (int)(i1 - i0 + 1) * P.parts, w = warp % RW;      // and how many
     const int D = P.c.head_dim;
 
-    // (rows past the last are read, within the tile, and dropped)
-    float mx[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) mx[k] = kNoMax;
-    if (RW == 1) {
-        for (int64_t i = s0; i < s1; ++i)
-#pragma unroll
-            for (int k = 0; k < R; ++k)
-                if (row + k < P.rows) mx[k] = fmaxf(mx[k], ml[i * P.tile_rows + k].x);
-    } else {
-        for (int64_t i = s0 + lane; i < s1; i += 32) mx[0] = fmaxf(mx[0], ml[i * P.tile_rows].x);
-#pragma unroll
-        for (int k = 16; k >= 1; k >>= 1) mx[0] = fmaxf(mx[0], __shfl_xor_sync(kFull, mx[0], k));
-    }
-    float acc[R][2][4], l[R];
+    float acc[R][2][4], m[R], l[R];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
+        m[k] = kNoMax;
         l[k] = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[k][0][i] = acc[k][1][i] = 0.f;
     }
-#pragma unroll 2
-    for (int64_t i = s0 + warp % RW; i < s1; i += RW) {
+    // this warp's share of the parts, up to 32 at a time: a lane takes one
+    // part's maxima and sums, then all lanes its values
+    const int share = n * (w + 1) / RW;
+    for (int c = n * w / RW; c < share; c += 32) {
+        float f[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (row + k >= P.rows) break;
-            const float2 p = ml[i * P.tile_rows + k];
-            if (p.y == 0.f) continue;  // nothing seen there (its values may never have been written)
-            const float f = ex2((p.x - mx[k]) * P.scale_log2);
-            l[k] += f * p.y;
-            const float *src = P.part_o + (i * P.tile_rows + r + k) * D;
+            float2 p = make_float2(kNoMax, 0.f);
+            if (c + lane < share && row + k < P.rows)
+                p = reinterpret_cast<const float2 *>(P.part_ml)[(s0 + c + lane) * P.tile_rows + r + k];
+            float mx = fmaxf(m[k], p.y > 0.f ? p.x : kNoMax);
 #pragma unroll
-            for (int sb = 0; sb < 2; ++sb) {
-                const int e = sb * 128 + 4 * lane;
-                if (e < D) {
-                    const float4 o = *reinterpret_cast<const float4 *>(src + e);
-                    acc[k][sb][0] += f * o.x;
-                    acc[k][sb][1] += f * o.y;
-                    acc[k][sb][2] += f * o.z;
-                    acc[k][sb][3] += f * o.w;
+            for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
+            f[k] = p.y > 0.f ? ex2((p.x - mx) * P.scale_log2) : 0.f;
+            float sum = f[k] * p.y;
+#pragma unroll
+            for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
+            const float old = ex2((m[k] - mx) * P.scale_log2);
+            l[k] = l[k] * old + sum;
+            m[k] = mx;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[k][0][i] *= old;
+                acc[k][1][i] *= old;
+            }
+        }
+        const int count = min(32, share - c);
+        const float *src = P.part_o + ((s0 + c) * P.tile_rows + r) * D + 4 * lane;
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                // (a part without a token may never have been written: its values do not count)
+                const float fk = __shfl_sync(kFull, f[k], j);
+#pragma unroll
+                for (int sb = 0; sb < 2; ++sb) {
+                    if (sb * 128 + 4 * lane < D && fk != 0.f) {
+                        const float4 o = *reinterpret_cast<const float4 *>(src + (size_t)k * D + sb * 128);
+                        acc[k][sb][0] += fk * o.x;
+                        acc[k][sb][1] += fk * o.y;
+                        acc[k][sb][2] += fk * o.z;
+                        acc[k][sb][3] += fk * o.w;
+                    }
                 }
             }
+            src += (size_t)P.tile_rows * D;
         }
     }
     if (RW > 1) {
@@ -653,20 +663,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
         for (int sb = 0; sb < 2; ++sb)
             *reinterpret_cast<float4 *>(&so[warp][sb * 128 + 4 * lane]) =
                 make_float4(acc[0][sb][0], acc[0][sb][1], acc[0][sb][2], acc[0][sb][3]);
-        if (lane == 0) sl[warp] = l[0];
+        if (lane == 0) {
+            sl[warp] = l[0];
+            sm[warp] = m[0];
+        }
         __syncthreads();
         if (warp != 0) return;
+        float mx = kNoMax;
+#pragma unroll
+        for (int x = 0; x < RW; ++x) mx = fmaxf(mx, sm[x]);
         l[0] = 0.f;
 #pragma unroll
-        for (int w = 0; w < RW; ++w) l[0] += sl[w];
+        for (int i = 0; i < 4; ++i) acc[0][0][i] = acc[0][1][i] = 0.f;
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb)
+        for (int x = 0; x < RW; ++x) {
+            const float f = ex2((sm[x] - mx) * P.scale_log2);
+            l[0] += f * sl[x];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[0][sb][i] = 0.f;
+            for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-                for (int w = 0; w < RW; ++w) acc[0][sb][i] += so[w][sb * 128 + 4 * lane + i];
-            }
+                for (int i = 0; i < 4; ++i) acc[0][sb][i] += f * so[x][sb * 128 + 4 * lane + i];
+        }
     }
     uint32_t flips[2];
 #pragma unroll
