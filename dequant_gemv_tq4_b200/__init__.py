@@ -597,42 +597,34 @@ def nvfp4_gemm_batch(items, m: int = 1, ws=None, stream=None, descs=None):
 # ---------------------------------------------------------------------------
 # key/value cache (tensor helpers)
 # ---------------------------------------------------------------------------
-class _on:
-    """Makes a tensor's device the current one for a call, where it is not already."""
-
-    def __init__(self, t: torch.Tensor):
-        if not t.is_cuda:
-            raise ValueError("expected CUDA tensors")
-        i = t.device.index
-        self.guard = None if i == torch.cuda.current_device() else torch.cuda.device(i)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _bad(name: str, t: torch.Tensor, what: str):
+    raise ValueError(f"{name}: expected {what}, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
 
-def _ints(t: torch.Tensor, name: str, device, *shape) -> int:
-    """Address of a contiguous int32 tensor of this shape (None: any extent)."""
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous int32 tensor on {device}")
-    if t.dim() != len(shape) or any(want is not None and want != got for want, got in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+def _ints(t: torch.Tensor, name: str, device, shape) -> int:
+    """Address of a contiguous int32 tensor of this shape."""
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        _bad(name, t, f"a contiguous int32 tensor of shape {tuple(shape)} on {device}")
     return t.data_ptr()
 
 
-def _heads(t: torch.Tensor, name: str, device, *shape):
-    """(address, strides of all but the last dimension) of a head operand."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name}: expected unit stride in the last dimension")
-    return (t.data_ptr(), *t.stride()[:-1])
+def _heads(t: torch.Tensor, name: str, device, shape):
+    """Strides of a head operand, whose last one is 1."""
+    st = t.stride()
+    if t.shape != shape or t.device != device or (st[-1] != 1 and shape[-1] > 1):
+        _bad(name, t, f"shape {tuple(shape)} on {device} with unit stride in the last dimension")
+    return st
+
+
+def _off_device(device) -> bool:
+    """Whether a device is not the current one (the library launches on the current one)."""
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    return device.index != torch.cuda.current_device()
+
+
+def _raw_stream(stream, device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, layers: int | None = None, device=None):
@@ -651,30 +643,31 @@ def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, laye
 
 def _cache(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, layers: bool = False) -> KvCache:
     """The C description of one layer's cache (of layer 0, with ``layers``)."""
-    shape = tuple(codes.shape[1:] if layers else codes.shape)
-    if codes.dtype != torch.uint8 or len(shape) != 5 or shape[1] != 2:
-        raise ValueError("codes: expected uint8 [pages, 2, kv_heads, page_size, head_dim / 2]")
+    shape = codes.shape[1:] if layers else codes.shape
+    if len(shape) != 5 or shape[1] != 2 or codes.dtype is not torch.uint8:
+        _bad("codes", codes, "uint8 [pages, 2, kv_heads, page_size, head_dim / 2]")
     pages, _, kv_heads, page_size, half = shape
-    if scales.dtype != torch.int16 or tuple(scales.shape) != (*codes.shape[:-1], half // 8):
-        raise ValueError("scales: expected int16 [pages, 2, kv_heads, page_size, head_dim / 16]")
-    inner = codes[0] if layers and codes.shape[0] else codes
-    inner_s = scales[0] if layers and scales.shape[0] else scales
-    if not inner.is_contiguous() or not inner_s.is_contiguous() or scales.device != codes.device:
-        raise ValueError("codes and scales: expected contiguous tensors on one device")
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != codes.device or (
-            page_table.stride(1) != 1 and page_table.shape[1] > 1):
-        raise ValueError("page_table: expected int32 [batch, pages of a sequence] on the cache's device")
+    device = codes.device
+    if scales.dtype is not torch.int16 or scales.shape != (*codes.shape[:-1], half // 8) or scales.device != device:
+        _bad("scales", scales, f"int16 [pages, 2, kv_heads, page_size, head_dim / 16] on {device}")
+    for name, t in (("codes", codes), ("scales", scales)):
+        if not (t[0] if layers and t.shape[0] else t).is_contiguous():
+            _bad(name, t, "a contiguous tensor")
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.device != device:
+        _bad("page_table", page_table, f"int32 [batch, pages of a sequence] on {device}")
     batch, per_seq = page_table.shape
+    ld, one = page_table.stride()
+    if one != 1 and per_seq > 1:
+        _bad("page_table", page_table, "unit stride in the last dimension")
     return KvCache(codes.data_ptr(), scales.data_ptr(), pages, page_table.data_ptr(), batch, per_seq,
-                   max(page_table.stride(0), per_seq) if batch < 2 else page_table.stride(0), kv_heads, 2 * half,
-                   page_size)
+                   ld if batch > 1 else per_seq, kv_heads, 2 * half, page_size)
 
 
 def _rope_desc(inv_freq: torch.Tensor, device, interleaved=False, scale=1.0, inverse=False) -> RopeDesc:
-    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or \
-            inv_freq.device != device:
-        raise ValueError(f"inv_freq: expected a contiguous float32 vector on {device}")
-    return RopeDesc(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(interleaved), int(inverse), scale)
+    if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or inv_freq.device != device or \
+            not inv_freq.is_contiguous():
+        _bad("inv_freq", inv_freq, f"a contiguous float32 vector on {device}")
+    return RopeDesc(inv_freq.data_ptr(), 2 * inv_freq.shape[0], interleaved, inverse, scale)
 
 
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, factor: float = 1.0, scaling: str = "none",
@@ -716,18 +709,22 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, inter
     elements of each head rotated by positions[token] * inv_freq, the rest
     unchanged.  ``inverse`` rotates back (the gradient).  ``out`` may be x."""
     if x.dim() != 3:
-        raise ValueError("x: expected [tokens, heads, dim]")
-    with _on(x):
-        if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        if out.dtype != x.dtype:
-            raise ValueError("out: expected x's dtype")
-        n, heads, dim = x.shape
-        desc = _rope_desc(inv_freq, x.device, interleaved, scale, inverse)
-        xp, xt, xh = _heads(x, "x", x.device, n, heads, dim)
-        op, ot, oh = _heads(out, "out", x.device, n, heads, dim)
-        _check(tq_rope(xp, op, _dt(x.dtype), n, heads, dim, xt, xh, ot, oh,
-                       _ints(positions, "positions", x.device, n), desc, _stream(stream)), "tq_rope")
+        _bad("x", x, "[tokens, heads, dim]")
+    dev = x.device
+    if _off_device(dev):
+        with torch.cuda.device(dev):
+            return rope(x, positions, inv_freq, interleaved, scale, inverse, out, stream)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    elif out.dtype is not x.dtype:
+        _bad("out", out, f"{x.dtype}")
+    shape = x.shape
+    xs, os_ = _heads(x, "x", dev, shape), _heads(out, "out", dev, shape)
+    st = tq_rope(x.data_ptr(), out.data_ptr(), _dt(x.dtype), shape[0], shape[1], shape[2], xs[0], xs[1], os_[0],
+                 os_[1], _ints(positions, "positions", dev, shape[:1]),
+                 _rope_desc(inv_freq, dev, interleaved, scale, inverse), _raw_stream(stream, dev))
+    if st:
+        _check(st, "tq_rope")
     return out
 
 
@@ -737,41 +734,50 @@ def kv_append(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tenso
     """Writes the records of keys k and values v [n, kv_heads, head_dim]: token i
     goes to place places[i] of sequence seqs[i].  ``rope`` = (positions,
     inv_freq) rotates the keys on their way in."""
-    cache = _cache(codes, scales, page_table)
     dev = codes.device
-    with _on(codes):
-        n = seqs.numel()
-        if k.dtype != v.dtype:
-            raise ValueError("k and v: expected one dtype")
-        kp, kt, kh = _heads(k, "k", dev, n, cache.kv_heads, cache.head_dim)
-        vp, vt, vh = _heads(v, "v", dev, n, cache.kv_heads, cache.head_dim)
-        desc, pos = None, None
-        if rope is not None:
-            pos = _ints(rope[0], "positions", dev, n)
-            desc = _rope_desc(rope[1], dev, interleaved, rope_scale)
-        _check(tq_kv_append(cache, _ints(seqs, "seqs", dev, n), _ints(places, "places", dev, n), n, kp, kt, kh, vp,
-                            vt, vh, _dt(k.dtype), pos, desc, _stream(stream)), "tq_kv_append")
+    if _off_device(dev):
+        with torch.cuda.device(dev):
+            return kv_append(codes, scales, page_table, seqs, places, k, v, rope, interleaved, rope_scale, stream)
+    cache = _cache(codes, scales, page_table)
+    one = seqs.shape
+    n = seqs.numel()
+    shape = (n, cache.kv_heads, cache.head_dim)
+    if k.dtype is not v.dtype:
+        _bad("v", v, f"{k.dtype}")
+    ks, vs = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
+    pos = desc = None
+    if rope is not None:
+        pos, desc = _ints(rope[0], "positions", dev, (n,)), _rope_desc(rope[1], dev, interleaved, rope_scale)
+    st = tq_kv_append(cache, _ints(seqs, "seqs", dev, (n,)), _ints(places, "places", dev, one), n, k.data_ptr(), ks[0],
+                      ks[1], v.data_ptr(), vs[0], vs[1], _dt(k.dtype), pos, desc, _raw_stream(stream, dev))
+    if st:
+        _check(st, "tq_kv_append")
 
 
 def kv_read(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, seqs: torch.Tensor,
             places: torch.Tensor, dtype=torch.bfloat16, k: torch.Tensor | None = None,
             v: torch.Tensor | None = None, stream=None):
     """(keys, values) [n, kv_heads, head_dim] of the tokens at places[i] of seqs[i]."""
-    cache = _cache(codes, scales, page_table)
     dev = codes.device
-    with _on(codes):
-        n = seqs.numel()
-        shape = (n, cache.kv_heads, cache.head_dim)
-        if k is None:
-            k = torch.empty(shape, dtype=dtype, device=dev)
-        if v is None:
-            v = torch.empty(shape, dtype=k.dtype, device=dev)
-        if k.dtype != v.dtype:
-            raise ValueError("k and v: expected one dtype")
-        kp, kt, kh = _heads(k, "k", dev, *shape)
-        vp, vt, vh = _heads(v, "v", dev, *shape)
-        _check(tq_kv_read(cache, _ints(seqs, "seqs", dev, n), _ints(places, "places", dev, n), n, kp, kt, kh, vp, vt,
-                          vh, _dt(k.dtype), _stream(stream)), "tq_kv_read")
+    if _off_device(dev):
+        with torch.cuda.device(dev):
+            return kv_read(codes, scales, page_table, seqs, places, dtype, k, v, stream)
+    cache = _cache(codes, scales, page_table)
+    n = seqs.numel()
+    shape = (n, cache.kv_heads, cache.head_dim)
+    if k is None and v is None:
+        k, v = torch.empty((2, *shape), dtype=dtype, device=dev)
+    elif k is None:
+        k = torch.empty(shape, dtype=v.dtype, device=dev)
+    elif v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=dev)
+    if k.dtype is not v.dtype:
+        _bad("v", v, f"{k.dtype}")
+    ks, vs = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
+    st = tq_kv_read(cache, _ints(seqs, "seqs", dev, (n,)), _ints(places, "places", dev, (n,)), n, k.data_ptr(), ks[0],
+                    ks[1], v.data_ptr(), vs[0], vs[1], _dt(k.dtype), _raw_stream(stream, dev))
+    if st:
+        _check(st, "tq_kv_read")
     return k, v
 
 
@@ -791,25 +797,33 @@ def kv_attention(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Te
     sees the lens[b] tokens of its sequence, its own drafted token (record at
     place lens[b] + i) and that token's ancestors by ``parents`` [batch, tree]
     (None: a chain).  ``scale`` defaults to head_dim^-0.5, ``dtype`` to q's."""
-    cache = _cache(codes, scales, page_table)
     dev = codes.device
+    if _off_device(dev):
+        with torch.cuda.device(dev):
+            return kv_attention(codes, scales, page_table, lens, q, parents, scale, dtype, out, ws, stream)
+    cache = _cache(codes, scales, page_table)
     if q.dim() != 4:
-        raise ValueError("q: expected [batch, tree, heads, head_dim]")
+        _bad("q", q, "[batch, tree, heads, head_dim]")
     batch, tree, heads, dim = q.shape
-    with _on(codes):
-        if out is None:
-            out = torch.empty(q.shape, dtype=dtype or q.dtype, device=dev)
-        shape = (cache.batch, tree, heads, cache.head_dim)
-        qp, qb, qt, qh = _heads(q, "q", dev, *shape)
-        op, ob, ot, oh = _heads(out, "out", dev, *shape)
-        par = None if parents is None else _ints(parents, "parents", dev, batch, tree)
-        if ws is None:
-            ws = kv_attention_workspace(batch, tree, heads, cache.kv_heads, dim, dev)
-        elif ws.device != dev:
-            raise ValueError(f"ws: expected a tensor on {dev}")
-        _check(tq_kv_attention(cache, _ints(lens, "lens", dev, batch), par, tree, qp, _dt(q.dtype), qb, qt, qh, op,
-                               _dt(out.dtype), ob, ot, oh, tree, heads, dim ** -0.5 if scale is None else scale,
-                               ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)), "tq_kv_attention")
+    shape = (cache.batch, tree, heads, cache.head_dim)
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype or q.dtype, device=dev)
+    qs, os_ = _heads(q, "q", dev, shape), _heads(out, "out", dev, shape)
+    if ws is None:
+        nbytes = tq_kv_attention_workspace_bytes(batch, tree, heads, cache.kv_heads, dim)
+        if nbytes == 0:
+            raise ValueError("kv_attention: invalid sizes (heads is a multiple of kv_heads, up to 64 drafted tokens)")
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        if ws.device != dev or not ws.is_contiguous():
+            _bad("ws", ws, f"a contiguous tensor on {dev}")
+        nbytes = ws.numel() * ws.element_size()
+    par = None if parents is None else _ints(parents, "parents", dev, (batch, tree))
+    st = tq_kv_attention(cache, _ints(lens, "lens", dev, (batch,)), par, tree, q.data_ptr(), _dt(q.dtype), qs[0],
+                         qs[1], qs[2], out.data_ptr(), _dt(out.dtype), os_[0], os_[1], os_[2], tree, heads,
+                         dim ** -0.5 if scale is None else scale, ws.data_ptr(), nbytes, _raw_stream(stream, dev))
+    if st:
+        _check(st, "tq_kv_attention")
     return out
 
 
@@ -819,12 +833,15 @@ def kv_commit(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tenso
     lens[b] + path[b, i] to place lens[b] + i, for increasing path[b] up to its
     first entry that does not increase (-1).  codes and scales of one layer, or
     with a leading dimension of layers that share the page table."""
+    dev = codes.device
+    if _off_device(dev):
+        with torch.cuda.device(dev):
+            return kv_commit(codes, scales, page_table, lens, path, stream)
     layered = codes.dim() == 6
     cache = _cache(codes, scales, page_table, layered)
-    dev = codes.device
-    layers = codes.shape[0] if layered else 1
-    with _on(codes):
-        batch, steps = cache.batch, path.shape[-1]
-        _check(tq_kv_commit(cache, layers, codes.stride(0) if layered else 0, scales.stride(0) if layered else 0,
-                            _ints(lens, "lens", dev, batch), _ints(path, "path", dev, batch, steps), steps, steps,
-                            _stream(stream)), "tq_kv_commit")
+    layers, cs, ss = (codes.shape[0], codes.stride(0), scales.stride(0)) if layered else (1, 0, 0)
+    batch, steps = cache.batch, path.shape[-1]
+    st = tq_kv_commit(cache, layers, cs, ss, _ints(lens, "lens", dev, (batch,)),
+                      _ints(path, "path", dev, (batch, steps)), steps, steps, _raw_stream(stream, dev))
+    if st:
+        _check(st, "tq_kv_commit")

@@ -83,6 +83,7 @@ __device__ __forceinline__ void rotate_query(const AttnParams &P, const char *x,
 #pragma unroll
     for (int blk = 0; blk < DP / 4 / N; ++blk) {
         const int e0 = c * (DP / 4) + blk * N;
+        const uint32_t bits = c_sign_words.w[e0 / 32] >> (e0 % 32);
         float v[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = 0.f;
@@ -92,7 +93,7 @@ __device__ __forceinline__ void rotate_query(const AttnParams &P, const char *x,
                 float t[4];
                 load4<DT>(x + (int64_t)(e0 + i) * ElemSize<DT>::value, t);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[i + k] = flip(t[k], sign_mask(e0 + i + k));
+                for (int k = 0; k < 4; ++k) v[i + k] = flip(t[k], (bits << (31 - i - k)) & 0x80000000u);
             }
         }
 #pragma unroll
@@ -384,9 +385,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
     AttnShared &sh = *reinterpret_cast<AttnShared *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
-    grid_dependents_launch();  // the joining launch may take its place; it waits for this one's end
-
     fill_lut(tid, WARPS * 32);
+    grid_dependency_wait();
+    grid_dependents_launch();  // the joining launch may take its place; it waits for this one's end
     scan_sequences(P, sh.prefix, sh.scan, tid, WARPS * 32);
     // defined behind the barrier, so that no lookup is moved in front of it
     uint32_t lane_base;
@@ -462,6 +463,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
             kr[q] = KeyRegs<DP>();
             vr[q] = ValueRegs<DP>();
         }
+        const TreeParents tree(P, b, lane);
         int grp = ga;
         int page[kStepGroups], next[kStepGroups];
         pages_of(grp, page);
@@ -504,7 +506,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
             fetch_keys(next, grp + kStepGroups);
             uint32_t pb[kStepGroups][NT][2];
             if (tail) {
-                const TreeWords words(P, b, lane);
+                const TreeWords words(P, tree, lane);
                 uint64_t see[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -540,7 +542,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
         // elements of two rows for each lane
         const int64_t slot = (int64_t)b * per_seq + hr + me;
         uint64_t present = ~0ull;
-        if (P.parents) present = TreeWords(P, b, lane).present();
+        if (P.parents) present = TreeWords(P, tree, lane).present();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -583,6 +585,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     __shared__ float so[RW == 1 ? 1 : kJoinWarps][256];
     __shared__ float sl[kJoinWarps], sm[kJoinWarps];
     grid_dependency_wait();
+    grid_dependents_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int quads = (P.rows + R - 1) / R;  // (a tile's rows are a multiple of R)
     const int index = (int)blockIdx.x * (kJoinWarps / RW) + warp / RW;
@@ -746,11 +749,10 @@ AttnPlan plan_attention(int64_t batch, int tree, int heads, int kv_heads, int he
 
 template <int DP, int NT, int WARPS, bool FULL>
 cudaError_t launch_attend_as(const AttnParams &P, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(attend_kernel<DP, NT, WARPS, FULL>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
+    static SharedMemoryLimit limit;
+    const cudaError_t e = limit.raise(attend_kernel<DP, NT, WARPS, FULL>, kAttnSmem);
     if (e != cudaSuccess) return e;
-    attend_kernel<DP, NT, WARPS, FULL><<<P.workers / WARPS, WARPS * 32, kAttnSmem, stream>>>(P);
-    return cudaGetLastError();
+    return launch_dependent(attend_kernel<DP, NT, WARPS, FULL>, P.workers / WARPS, WARPS * 32, kAttnSmem, stream, P);
 }
 
 template <int DP, int NT, int WARPS>
@@ -761,28 +763,20 @@ cudaError_t launch_attend(const AttnParams &P, cudaStream_t stream) {
 
 template <int OT, int RW>
 cudaError_t launch_join_as(const AttnParams &P, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
     constexpr int R = RW == 1 ? kJoinRows : 1;
     const int64_t items = (int64_t)P.c.batch * P.c.kv_heads * ((P.rows + R - 1) / R);
-    cfg.gridDim = dim3((unsigned)((items * RW + kJoinWarps - 1) / kJoinWarps));
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<OT, RW>, P);
+    return launch_dependent(join_kernel<OT, RW>, (unsigned)((items * RW + kJoinWarps - 1) / kJoinWarps),
+                            kJoinWarps * 32, 0, stream, P);
 }
 
-
-// A unit has about workers / units + 1 parts: eight warps share a row where
-// these are many, a warp takes a row where they are few.
+// A warp takes four rows where that gives at least eight warps an SM and the
+// parts are few (about workers / units + 1 of them); else eight warps share a row.
 template <int OT>
 cudaError_t launch_join_by(const AttnParams &P, cudaStream_t stream) {
-    const int64_t units = (int64_t)P.c.batch * P.c.kv_heads * P.row_tiles;
-    return (int64_t)P.workers * P.parts > 6 * units ? launch_join_as<OT, 8>(P, stream)
-                                                    : launch_join_as<OT, 1>(P, stream);
+    const int64_t pairs = (int64_t)P.c.batch * P.c.kv_heads;
+    const bool few = (int64_t)P.workers * P.parts <= 6 * pairs * P.row_tiles;
+    return few && pairs * ((P.rows + kJoinRows - 1) / kJoinRows) >= 148 * 8 ? launch_join_as<OT, 1>(P, stream)
+                                                                           : launch_join_as<OT, 8>(P, stream);
 }
 
 }  // namespace

@@ -4,6 +4,8 @@
 
 #include <math.h>
 
+#include <atomic>
+
 #include <type_traits>
 
 #include "tq_device.cuh"
@@ -92,9 +94,20 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 // words of tokens l and l + 32.  A word is the token itself and its ancestors,
 // or 0 for a token that is not there (a parent that is neither -1 nor an
 // earlier token, its own or an ancestor's).  Six rounds of pointer doubling.
+struct TreeParents {
+    int at[2];  // of tokens `lane` and `lane` + 32
+    __device__ __forceinline__ TreeParents(const AttnParams &P, int b, int lane) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = lane + 32 * k;
+            at[k] = P.parents && i < P.tree ? P.parents[b * P.parents_ld + i] : i - 1;
+        }
+    }
+};
+
 struct TreeWords {
     uint64_t w[2];
-    __device__ __forceinline__ TreeWords(const AttnParams &P, int b, int lane) {
+    __device__ __forceinline__ TreeWords(const AttnParams &P, const TreeParents &tree, int lane) {
         int ptr[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -102,7 +115,7 @@ struct TreeWords {
             w[k] = i < P.tree ? (2ull << i) - 1 : 0;  // a chain
             ptr[k] = -1;
             if (P.parents && i < P.tree) {
-                const int par = P.parents[b * P.parents_ld + i];
+                const int par = tree.at[k];
                 ptr[k] = par < -1 || par >= i ? -2 : par;
                 w[k] = 1ull << i;
             }
@@ -172,6 +185,25 @@ __device__ __forceinline__ void scan_sequences(const AttnParams &P, int *prefix,
     if (tid == threads - 1) prefix[P.c.batch] = base + inc;
     __syncthreads();
 }
+
+// Raises a kernel's dynamic shared memory limit, once on each device.
+class SharedMemoryLimit {
+    std::atomic<uint64_t> done[4] = {};  // a bit per device
+
+public:
+    template <typename K>
+    cudaError_t raise(K kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 256) return cudaErrorInvalidDevice;
+        const uint64_t bit = 1ull << (dev & 63);
+        if (done[dev >> 6].load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
 
 // The launch that joins the parts of every row, rotates back, divides and
 // rounds; a programmatic dependent of the attention launch before it.

@@ -194,6 +194,25 @@ cudaError_t launch_nvfp4_quantize(const void *w, int dtype, int64_t n, int64_t k
 cudaError_t launch_nvfp4_dequantize(const uint8_t *codes, const uint8_t *scales, const float *tensor_scale,
                                     int64_t n, int64_t k, void *w_out, int dtype, int64_t ldo, cudaStream_t stream);
 
+// Launch as a programmatic dependent: the kernel may become resident while the
+// one before it in the stream still runs, and calls grid_dependency_wait()
+// before it touches memory.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                                    cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- key/value cache -----------------------------------------------------------
 // Largest scale of a cache record: 2.7326 * 23968 is the largest fp16 product
 // of a centroid and a scale that stays finite.

@@ -107,6 +107,8 @@ __device__ __forceinline__ void store_v(char *p, const float (&v)[V]) {
 template <int DT, int V>
 __global__ void __launch_bounds__(kKvThreads) rope_kernel(const RopeParams P) {
     constexpr int E = ElemSize<DT>::value;
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int64_t item = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
     if (item >= P.items) return;
     const int slot = (int)(item % P.slots);
@@ -208,6 +210,8 @@ __device__ __forceinline__ uint32_t cache_code(float y, const float (&t)[7]) {
 template <int DT>
 __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendParams P) {
     constexpr int E = ElemSize<DT>::value;
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int64_t item = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) >> 3;
     const int p = threadIdx.x & 7;
     // lanes past the last item follow along without storing (the shuffles need whole warps)
@@ -327,6 +331,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const ReadParams P)
     if (threadIdx.x < 16)
         table[threadIdx.x] = __uint_as_float(c_kv_mag_bits[threadIdx.x & 7] ^ ((threadIdx.x & 8u) << 28));
     __syncthreads();
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int64_t item = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) >> 3;
     const int p = threadIdx.x & 7;
     const int64_t it = item < P.items ? item : P.items - 1;
@@ -414,6 +420,8 @@ __device__ __forceinline__ void move_branch(const CommitParams &P, char *plane0,
 }
 
 __global__ void __launch_bounds__(kKvThreads) kv_commit_kernel(const CommitParams P) {
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int64_t item = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
     if (item >= P.items) return;
     const int piece = (int)(item % P.pieces);
@@ -476,16 +484,17 @@ cudaError_t launch_rope(const RopeJob &j, cudaStream_t stream) {
     P.chunks = (j.heads + P.hchunk - 1) / P.hchunk;
     P.items = j.tokens * P.chunks * P.slots;
     const unsigned grid = blocks_of(P.items);
+    cudaError_t e = cudaSuccess;
     auto run = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         constexpr int W = 16 / ElemSize<DT>::value;
-        if (wide) rope_kernel<DT, W><<<grid, kKvThreads, 0, stream>>>(P);
-        else rope_kernel<DT, 1><<<grid, kKvThreads, 0, stream>>>(P);
+        if (wide) e = launch_dependent(rope_kernel<DT, W>, grid, kKvThreads, 0, stream, P);
+        else e = launch_dependent(rope_kernel<DT, 1>, grid, kKvThreads, 0, stream, P);
     };
     if (j.dtype == kF32) run(std::integral_constant<int, kF32>());
     else if (j.dtype == kBF16) run(std::integral_constant<int, kBF16>());
     else run(std::integral_constant<int, kF16>());
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_kv_append(const KvAppendJob &j, cudaStream_t stream) {
@@ -508,10 +517,11 @@ cudaError_t launch_kv_append(const KvAppendJob &j, cudaStream_t stream) {
     P.chunks = (j.c.kv_heads + P.hchunk - 1) / P.hchunk;
     P.items = j.tokens * 2 * P.chunks * P.blocks;
     const unsigned grid = blocks_of(P.items * 8);
-    if (j.dtype == kF32) kv_append_kernel<kF32><<<grid, kKvThreads, 0, stream>>>(P);
-    else if (j.dtype == kBF16) kv_append_kernel<kBF16><<<grid, kKvThreads, 0, stream>>>(P);
-    else kv_append_kernel<kF16><<<grid, kKvThreads, 0, stream>>>(P);
-    return cudaGetLastError();
+    cudaError_t e;
+    if (j.dtype == kF32) e = launch_dependent(kv_append_kernel<kF32>, grid, kKvThreads, 0, stream, P);
+    else if (j.dtype == kBF16) e = launch_dependent(kv_append_kernel<kBF16>, grid, kKvThreads, 0, stream, P);
+    else e = launch_dependent(kv_append_kernel<kF16>, grid, kKvThreads, 0, stream, P);
+    return e;
 }
 
 cudaError_t launch_kv_read(const KvReadJob &j, cudaStream_t stream) {
@@ -529,10 +539,11 @@ cudaError_t launch_kv_read(const KvReadJob &j, cudaStream_t stream) {
     P.chunks = (j.c.kv_heads + P.hchunk - 1) / P.hchunk;
     P.items = j.tokens * 2 * P.chunks * P.blocks;
     const unsigned grid = blocks_of(P.items * 8);
-    if (j.dtype == kF32) kv_read_kernel<kF32><<<grid, kKvThreads, 0, stream>>>(P);
-    else if (j.dtype == kBF16) kv_read_kernel<kBF16><<<grid, kKvThreads, 0, stream>>>(P);
-    else kv_read_kernel<kF16><<<grid, kKvThreads, 0, stream>>>(P);
-    return cudaGetLastError();
+    cudaError_t e;
+    if (j.dtype == kF32) e = launch_dependent(kv_read_kernel<kF32>, grid, kKvThreads, 0, stream, P);
+    else if (j.dtype == kBF16) e = launch_dependent(kv_read_kernel<kBF16>, grid, kKvThreads, 0, stream, P);
+    else e = launch_dependent(kv_read_kernel<kF16>, grid, kKvThreads, 0, stream, P);
+    return e;
 }
 
 cudaError_t launch_kv_commit(const KvCommitJob &j, cudaStream_t stream) {
@@ -547,8 +558,7 @@ cudaError_t launch_kv_commit(const KvCommitJob &j, cudaStream_t stream) {
     P.code_pieces = j.c.head_dim / 32;
     P.pieces = P.code_pieces + j.c.head_dim / 32;
     P.items = j.layers * j.c.batch * 2 * j.c.kv_heads * P.pieces;
-    kv_commit_kernel<<<blocks_of(P.items), kKvThreads, 0, stream>>>(P);
-    return cudaGetLastError();
+    return launch_dependent(kv_commit_kernel, blocks_of(P.items), kKvThreads, 0, stream, P);
 }
 
 }  // namespace tq

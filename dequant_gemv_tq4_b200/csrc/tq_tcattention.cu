@@ -475,8 +475,6 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
     const int warp = __shfl_sync(kFull, tid >> 5, 0);
     int *prefix = reinterpret_cast<int *>(smem + S::kPrefix);
     auto bar = [&](int i) { return base + S::kBars + 8u * (uint32_t)i; };
-    grid_dependents_launch();  // the joining launch; it waits for this one's end
-
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             a_mbar_init(bar(kKFull + i), kPieces / 2);
@@ -489,7 +487,6 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
         a_mbar_init(bar(kODone), 1);
         a_mbar_init(bar(kLast), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        if (blockIdx.x == 0) P.header[0] = 0u;  // status of this call: set, if at all, a second from now
     }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + S::kTmemSlot),
@@ -497,6 +494,9 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    grid_dependency_wait();
+    grid_dependents_launch();  // the joining launch; it waits for this one's end
+    if (blockIdx.x == 0 && tid == 0) P.header[0] = 0u;  // status of this call: set, if at all, a second from now
     a_fence_before();
     scan_sequences(P, prefix, reinterpret_cast<int *>(smem + S::kScan), tid, kTcaThreads);
     a_fence_after();
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
             const int out_row = pair ? s * kRowTile + row : row;  // of the partial result
             const int unit_row = p.row0 + out_row;
             const bool any_rows = unit_row - lane < P.rows;
-            const TreeWords words(P, p.b, lane);
+            const TreeWords words(P, TreeParents(P, p.b, lane), lane);
             const uint64_t see = words.of(min(unit_row / P.group_heads, P.tree - 1));
             const int32_t *table = P.c.page_table + p.b * P.c.table_ld;
             const int tiles = p.tb - p.ta, jobs = pair ? 2 * tiles : tiles;
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                 if (i >= end) return -1;
                 const int place = place_of(i), j = place - p.len;
                 if (!known && place - lane + 32 > p.len) {
-                    present = TreeWords(P, p.b, lane).present();
+                    present = TreeWords(P, TreeParents(P, p.b, lane), lane).present();
                     known = true;
                 }
                 if (place >= p.n || (j >= 0 && !((present >> j) & 1ull))) return -1;
@@ -758,11 +758,10 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
 
 template <int D>
 cudaError_t launch_as(const AttnParams &P, cudaStream_t stream) {
-    cudaError_t e =
-        cudaFuncSetAttribute(tc_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcaShape<D>::kBytes);
+    static SharedMemoryLimit limit;
+    const cudaError_t e = limit.raise(tc_attend_kernel<D>, TcaShape<D>::kBytes);
     if (e != cudaSuccess) return e;
-    tc_attend_kernel<D><<<P.workers, kTcaThreads, TcaShape<D>::kBytes, stream>>>(P);
-    return cudaGetLastError();
+    return launch_dependent(tc_attend_kernel<D>, P.workers, kTcaThreads, TcaShape<D>::kBytes, stream, P);
 }
 
 }  // namespace

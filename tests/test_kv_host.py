@@ -180,11 +180,11 @@ def test_tensor_helpers_refuse_what_does_not_fit(tq):
         tq.rope(torch.zeros(2, 64), torch.zeros(2, dtype=torch.int32), torch.ones(32))
     cpu = torch.device("cpu")
     with pytest.raises(ValueError, match="int32"):
-        tq._ints(torch.zeros(3, dtype=torch.int64), "x", cpu, 3)
+        tq._ints(torch.zeros(3, dtype=torch.int64), "x", cpu, (3,))
     with pytest.raises(ValueError, match="shape"):
-        tq._ints(torch.zeros(3, dtype=torch.int32), "x", cpu, 4)
+        tq._ints(torch.zeros(3, dtype=torch.int32), "x", cpu, (4,))
     with pytest.raises(ValueError, match="unit stride"):
-        tq._heads(torch.zeros(2, 4, 8).transpose(1, 2), "x", cpu, 2, 8, 4)
+        tq._heads(torch.zeros(2, 4, 8).transpose(1, 2), "x", cpu, (2, 8, 4))
 
 
 def test_rope_frequencies(tq):
