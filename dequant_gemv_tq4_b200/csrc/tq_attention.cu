@@ -36,7 +36,7 @@ namespace {
 constexpr int kGroup = 16;               // tokens of a group
 constexpr uint32_t kLutBase = 0x10000u;  // shared-memory address of the centroid table
 constexpr uint32_t kLutStep = 256;       // bytes between its rows (128 used)
-constexpr int kLeastGroups = 4;          // groups of a warp's range at least
+constexpr int kLeastGroups = 1;          // groups of a warp's range at least
 constexpr int kTcLeastRows = 16;         // above: the tcgen05 kernel
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
@@ -118,10 +118,10 @@ __device__ __forceinline__ void rotate_query(const AttnParams &P, const char *x,
 }
 
 // What a lane (l = 4 g + c) holds of a group of 16 tokens.  Key rows: tokens
-// 4 (g / 2) + g % 2 and that + 2, elements DP/4 * c ...; value rows: tokens
-// 4 c .. 4 c + 3, elements DP/8 * g ...  This is the order in which S^T's
-// accumulator, transposed by movmatrix, is the weights operand of the second
-// product.
+// g / 2 + 4 (g % 2) and that + 8, elements DP/4 * c ...; value rows: tokens
+// c, c + 4, c + 8, c + 12, elements DP/8 * g ...  In this order S^T's accumulator,
+// transposed by movmatrix, is the weights operand of the second product, and
+// every load of the warp covers whole neighbouring rows.
 template <int DP>
 struct KeyRegs {
     static constexpr int W = DP / 32;  // code words of a row (DP / 4 elements)
@@ -137,38 +137,38 @@ struct ValueRegs {
     uint32_t d[4];  // one or two half-block scales
 };
 
-// Where this lane's rows begin within a group, in bytes of the codes and in
-// scales; with FULL the head dimension is DP itself and no piece is missing.
+// Where this lane's rows begin within a group (added to warp-uniform bases); with FULL the head dimension is DP itself and no piece is missing.
 template <int DP, bool FULL>
 struct LaneOffsets {
-    int dim, kc, ks, vc, vs;
+    int dim;
+    uint32_t kc, ks, vc, vs;  // bytes
     __device__ __forceinline__ LaneOffsets(int head_dim, int lane) {
         const int g = lane >> 2, c = lane & 3;
         dim = FULL ? DP : head_dim;
-        const int row = 4 * (g >> 1) + (g & 1);
+        const int row = (g >> 1) + 4 * (g & 1);
         kc = row * (dim / 2) + c * (DP / 8);
-        ks = row * (dim / 16) + c * (DP / 64);
-        vc = 4 * c * (dim / 2) + g * (DP / 16);
-        vs = 4 * c * (dim / 16) + g * (DP / 8) / 16;
+        ks = row * (dim / 8) + c * (DP / 32);
+        vc = c * (dim / 2) + g * (DP / 16);
+        vs = c * (dim / 8) + g * (DP / 8) / 16 * 2;
     }
 };
 
 template <int DP, bool FULL>
-__device__ __forceinline__ void load_keys(const uint8_t *codes, const uint16_t *scales,
+__device__ __forceinline__ void load_keys(const uint8_t *codes, const uint8_t *scales,
                                           const LaneOffsets<DP, FULL> &o, int c, KeyRegs<DP> &r) {
     const int dim = FULL ? DP : o.dim;
     codes += o.kc;
     scales += o.ks;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint8_t *cp = codes + i * dim;          // two rows on
-        const uint16_t *sp = scales + i * (dim / 8);
+        const uint8_t *cp = codes + i * 4 * dim;  // eight rows on
+        const uint8_t *sp = scales + i * dim;
         if constexpr (DP == 64) {
             uint2 w = make_uint2(0u, 0u);
             uint32_t d = 0;
             if (FULL || 16 * c < dim) {
                 w = __ldg(reinterpret_cast<const uint2 *>(cp));
-                d = __ldg(sp);
+                d = __ldg(reinterpret_cast<const uint16_t *>(sp));
             }
             r.w[i][0] = w.x;
             r.w[i][1] = w.y;
@@ -193,27 +193,27 @@ __device__ __forceinline__ void load_keys(const uint8_t *codes, const uint16_t *
 }
 
 template <int DP, bool FULL>
-__device__ __forceinline__ void load_values(const uint8_t *codes, const uint16_t *scales,
+__device__ __forceinline__ void load_values(const uint8_t *codes, const uint8_t *scales,
                                             const LaneOffsets<DP, FULL> &o, int g, ValueRegs<DP> &r) {
     const int dim = FULL ? DP : o.dim;
     codes += o.vc;
     scales += o.vs;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        const uint8_t *cp = codes + t * (dim / 2);
-        const uint16_t *sp = scales + t * (dim / 16);
+        const uint8_t *cp = codes + t * 2 * dim;  // four rows on
+        const uint8_t *sp = scales + t * (dim / 2);
         r.d[t] = 0;
 #pragma unroll
         for (int j = 0; j < ValueRegs<DP>::W; ++j) r.w[t][j] = 0;
         if (FULL || g * (DP / 8) < dim) {
             if constexpr (DP == 64) {
                 r.w[t][0] = __ldg(reinterpret_cast<const uint32_t *>(cp));
-                r.d[t] = __ldg(sp);
+                r.d[t] = __ldg(reinterpret_cast<const uint16_t *>(sp));
             } else if constexpr (DP == 128) {
                 const uint2 w = __ldg(reinterpret_cast<const uint2 *>(cp));
                 r.w[t][0] = w.x;
                 r.w[t][1] = w.y;
-                r.d[t] = __ldg(sp);
+                r.d[t] = __ldg(reinterpret_cast<const uint16_t *>(sp));
             } else {
                 const uint4 w = __ldg(reinterpret_cast<const uint4 *>(cp));
                 r.w[t][0] = w.x;
@@ -307,7 +307,7 @@ __device__ __forceinline__ void step_weights(const AttnParams &P, float (&s)[kSt
                                              int token0, int len, const int (&page)[kStepGroups],
                                              const uint64_t (&see)[NT][2]) {
     const int g = lane >> 2;
-    const int tok = 4 * (g >> 1) + (g & 1);  // this lane's score rows: tok, tok + 2
+    const int tok = (g >> 1) + 4 * (g & 1);  // this lane's score rows: tok, tok + 8
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         uint32_t ok = ~0u;
@@ -316,7 +316,7 @@ __device__ __forceinline__ void step_weights(const AttnParams &P, float (&s)[kSt
             for (int q = 0; q < kStepGroups; ++q)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int j = token0 + q * kGroup + tok + 2 * (i >> 1) - len;
+                    const int j = token0 + q * kGroup + tok + 8 * (i >> 1) - len;
                     const bool sees = page[q] >= 0 && (j < 0 || (j < P.tree && ((see[n][i & 1] >> j) & 1ull)));
                     if (!sees) {
                         ok &= ~(1u << (4 * q + i));
@@ -379,11 +379,14 @@ struct AttnShared {
 constexpr int kAttnSmem = (int)(kLutBase + 256 * kLutStep);
 static_assert(sizeof(AttnShared) + 4096 <= kLutBase, "shared memory below the table");
 
+// A value that is the same in every lane, told so.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(kFull, x, 0); }
+
 template <int DP, int NT, int WARPS, bool FULL>
 __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams P) {
     extern __shared__ char smem[];
     AttnShared &sh = *reinterpret_cast<AttnShared *>(smem);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
     const int g = lane >> 2, c = lane & 3;
     fill_lut(tid, WARPS * 32);
     grid_dependency_wait();
@@ -413,37 +416,41 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
             if ((int64_t)sh.prefix[mid] * per_seq <= at) lo = mid;
             else hi = mid - 1;
         }
-        const int b = lo, groups = sh.prefix[b + 1] - sh.prefix[b];
+        const int b = uniform(lo), groups = uniform(sh.prefix[b + 1] - sh.prefix[b]);
         const int64_t in_seq = at - (int64_t)sh.prefix[b] * per_seq;
-        const int hr = (int)quotient(in_seq, groups);
+        const int hr = uniform((int)quotient(in_seq, groups));
         const int head = hr / P.row_tiles, row0 = (hr % P.row_tiles) * NT * 8;
-        const int ga = (int)(in_seq - (int64_t)hr * groups);
-        const int gb = (int)min((int64_t)groups, ga + (end - at));
-        const int len = min(max(P.lens[b], 0), P.c.pages_per_seq << P.c.page_shift);
+        const int ga = uniform((int)(in_seq - (int64_t)hr * groups));
+        const int gb = uniform((int)min((int64_t)groups, ga + (end - at)));
+        const int len = uniform(min(max(P.lens[b], 0), P.c.pages_per_seq << P.c.page_shift));
 
         // first loads before the query is rotated
         const int32_t *table = P.c.page_table + b * P.c.table_ld;
         const int shift = P.c.page_shift - 4;  // groups of a page
         const int in_page = (1 << shift) - 1;
-        const int64_t v_rows = (int64_t)P.c.kv_heads << P.c.page_shift;  // from a key record to its value record
+        // records of a page, and from a key record to its value record
+        const int64_t v_rows = (int64_t)P.c.kv_heads << P.c.page_shift, page_rows = 2 * v_rows;
+        const int64_t head_row = (int64_t)head << P.c.page_shift;
         KeyRegs<DP> kr[kStepGroups];
         ValueRegs<DP> vr[kStepGroups];
+        // pages and groups are the same for the whole warp, and said to be: the
+        // bases below are then computed once per warp
         auto pages_of = [&](int grp, int (&page)[kStepGroups]) {
 #pragma unroll
             for (int q = 0; q < kStepGroups; ++q) {
-                page[q] = grp + q < gb ? table[(grp + q) >> shift] : -1;
-                if (page[q] >= P.c.pages) page[q] = -1;
+                int p = grp + q < gb ? table[(grp + q) >> shift] : -1;
+                if (p >= P.c.pages) p = -1;
+                page[q] = uniform(p);
             }
         };
-        auto record = [&](int page, int grp) {
-            return (((int64_t)page * 2 * P.c.kv_heads + head) << P.c.page_shift) + (grp & in_page) * kGroup;
-        };
+        auto record = [&](int page, int grp) { return page * page_rows + head_row + (grp & in_page) * kGroup; };
         auto fetch_keys = [&](const int (&page)[kStepGroups], int grp) {
 #pragma unroll
             for (int q = 0; q < kStepGroups; ++q) {
                 if (page[q] >= 0) {
                     const int64_t rec = record(page[q], grp + q);
-                    load_keys<DP, FULL>(P.c.codes + rec * (off.dim / 2), P.c.scales + rec * (off.dim / 16), off, c,
+                    load_keys<DP, FULL>(P.c.codes + rec * (off.dim / 2),
+                                        reinterpret_cast<const uint8_t *>(P.c.scales) + rec * (off.dim / 8), off, c,
                                         kr[q]);
                 }
             }
@@ -453,7 +460,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
             for (int q = 0; q < kStepGroups; ++q) {
                 if (page[q] >= 0) {
                     const int64_t rec = record(page[q], grp + q) + v_rows;
-                    load_values<DP, FULL>(P.c.codes + rec * (off.dim / 2), P.c.scales + rec * (off.dim / 16), off, g,
+                    load_values<DP, FULL>(P.c.codes + rec * (off.dim / 2),
+                                          reinterpret_cast<const uint8_t *>(P.c.scales) + rec * (off.dim / 8), off, g,
                                           vr[q]);
                 }
             }
@@ -521,7 +529,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         // a record that no query sees counts as zero whatever the memory holds
-                        const int j = token0 + q * kGroup + 4 * c + t - len;
+                        const int j = token0 + q * kGroup + c + 4 * t - len;
                         if (page[q] < 0 || (j >= 0 && (j >= P.tree || !((present >> j) & 1ull)))) vr[q].d[t] = 0;
                     }
                 step_weights<DP, NT, true>(P, s, st, pb, lane, token0, len, page, see);
@@ -735,7 +743,7 @@ AttnPlan plan_attention(int64_t batch, int tree, int heads, int kv_heads, int he
         // and the accumulators of 16 fit the registers (head dimension up to 128)
         p.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
         p.nt = p.rows > 8 && p.dp <= 128 ? 2 : 1;
-        p.warps = p.nt == 2 || p.dp == 256 ? 8 : 12;
+        p.warps = p.nt == 2 || p.dp == 256 ? 8 : 16;
         p.tile_rows = 8 * p.nt;
         p.parts = 1;
         p.group = kGroup;
@@ -832,9 +840,9 @@ cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t s
 
     cudaError_t e;
     if (plan.tc) e = launch_tc_attention(P, stream);
-    else if (plan.dp == 64) e = plan.nt == 1 ? launch_attend<64, 1, 12>(P, stream) : launch_attend<64, 2, 8>(P, stream);
+    else if (plan.dp == 64) e = plan.nt == 1 ? launch_attend<64, 1, 16>(P, stream) : launch_attend<64, 2, 8>(P, stream);
     else if (plan.dp == 128)
-        e = plan.nt == 1 ? launch_attend<128, 1, 12>(P, stream) : launch_attend<128, 2, 8>(P, stream);
+        e = plan.nt == 1 ? launch_attend<128, 1, 16>(P, stream) : launch_attend<128, 2, 8>(P, stream);
     else e = launch_attend<256, 1, 8>(P, stream);
     return e != cudaSuccess ? e : launch_join(P, j.odtype, stream);
 }
