@@ -9,26 +9,10 @@
 #include <type_traits>
 
 #include "tq_device.cuh"
+#include "tq_signs.cuh"
 #include "tq_internal.h"
 
 namespace tq {
-
-// The codec's signs of the head's columns, a bit per column (1 = negative).
-struct SignWords {
-    uint32_t w[8];
-};
-constexpr SignWords sign_words() {
-    SignWords s = {};
-    for (uint32_t k = 0; k < 256; ++k) {
-        uint32_t h = k * 0x9E3779B9u;
-        h ^= h >> 16;
-        h *= 0x85EBCA6Bu;
-        h ^= h >> 13;
-        s.w[k / 32] |= (h >> 31) << (k % 32);
-    }
-    return s;
-}
-static __constant__ SignWords c_sign_words = sign_words();
 
 constexpr float kWeightExp = 7.0f;  // softmax weights are held times 2^7
 constexpr float kLazy = 8.0f;       // log2 by which a maximum may grow before it is followed

@@ -5,8 +5,10 @@
 // A cache record is one token's head vector in the codec of the weights: per
 // 32-element block the sign flip, the 32-point Walsh-Hadamard transform, two
 // fp16 half-block scales and sixteen nibble codes per half (include/tq.h).
+#include "tq_block.cuh"
 #include "tq_device.cuh"
 #include "tq_internal.h"
+#include "tq_signs.cuh"
 
 namespace tq {
 
@@ -310,7 +312,125 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendParam
 }
 
 // ---------------------------------------------------------------------------
-// Read: the same lane layout in reverse.  x~ = s . (H (c d)) / 32 in fp32
+// Append, many tokens: a lane owns a whole block, the transform and the codes
+// stay in its registers (no shuffles: 12 of them and a quarter of the sums are
+// what the eight-lane form adds per four elements).  A CTA takes `per_cta`
+// tokens; their rotary angles stand in shared memory, one fp64 reduction per
+// token and pair.  Keys and values run one after the other, so that a warp's
+// lanes agree about the rotation.
+// ---------------------------------------------------------------------------
+constexpr int kAngles = 2048;  // cos, sin pairs of a CTA
+
+template <int DT>
+__device__ __forceinline__ void load_block32(const char *p, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        float t[4];
+        load4<DT>(p + i * ElemSize<DT>::value, t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[i + k] = t[k];
+    }
+}
+
+// v rotated in place; block `blk` of the head at `x`, angles of its token at cs.
+template <int DT>
+__device__ __forceinline__ void rotate_block(const AppendParams &P, const char *x, int blk, const float2 *cs,
+                                             float (&v)[32]) {
+    const int e0 = 32 * blk, half = P.rot / 2;
+    if (P.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float2 c = cs[(e0 + i) / 2];
+            const float a = v[i] * c.x - v[i + 1] * c.y, b = v[i + 1] * c.x + v[i] * c.y;
+            v[i] = a;
+            v[i + 1] = b;
+        }
+        return;
+    }
+    const bool lower = e0 < half;
+    const char *p = x + (lower ? e0 + half : e0 - half) * ElemSize<DT>::value;
+    const float4 *c4 = reinterpret_cast<const float4 *>(cs + (lower ? e0 : e0 - half));
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        float o[4];
+        load4<DT>(p + i * ElemSize<DT>::value, o);
+        const float4 c0 = c4[i / 2], c1 = c4[i / 2 + 1];
+        const float c[4] = {c0.x, c0.z, c1.x, c1.z}, sn[4] = {c0.y, c0.w, c1.y, c1.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[i + k] = v[i + k] * c[k] + o[k] * (lower ? -sn[k] : sn[k]);
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kKvThreads, 2) kv_append_block_kernel(const AppendParams P, int per_cta) {
+    constexpr int E = ElemSize<DT>::value;
+    __shared__ __align__(16) float2 angles[kAngles];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int64_t token0 = (int64_t)blockIdx.x * per_cta;
+    const int tokens = (int)min((int64_t)per_cta, P.items - token0);
+    const int pairs = P.rot / 2;
+    if (P.positions) {
+        for (int i = threadIdx.x; i < tokens * pairs; i += kKvThreads)
+            angles[i] = rope_cos_sin(P.positions[token0 + i / pairs], P.inv_freq[i % pairs], P.scale, false);
+        __syncthreads();
+    }
+    float thr[7];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) thr[i] = __uint_as_float(c_kv_thr_bits[i]);
+    const int per_plane = P.c.kv_heads * P.blocks;
+    for (int plane = 0; plane < 2; ++plane) {
+        for (int i = threadIdx.x; i < tokens * per_plane; i += kKvThreads) {
+            const int t = i / per_plane, rest = i - t * per_plane;
+            const int head = rest / P.blocks, blk = rest - head * P.blocks;
+            const int64_t token = token0 + t;
+            const char *x = P.x[plane] + (token * P.token_stride[plane] + head * P.head_stride[plane]) * E;
+            float v[32];
+            load_block32<DT>(x + 32 * blk * E, v);
+            if (plane == 0 && P.positions && 32 * blk < P.rot) rotate_block<DT>(P, x, blk, angles + t * pairs, v);
+            const uint32_t bits = c_sign_words.w[blk];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = flip(v[e], (bits << (31 - e)) & 0x80000000u);
+            fwht32_regs(v);
+            uint32_t dbits[2];
+            float D[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float q[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) q[e] = __fmul_rn(v[16 * h + e], v[16 * h + e]);
+#pragma unroll
+                for (int step = 1; step < 16; step <<= 1)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2 * step) q[e] = __fadd_rn(q[e], q[e + step]);
+                const __half hd = __float2half_rn(fminf(__fsqrt_rn(__fmul_rn(q[0], 0.0625f)), kKvScaleMax));
+                dbits[h] = __half_as_ushort(hd);
+                D[h] = __half2float(hd);
+            }
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float lim[7];
+#pragma unroll
+                for (int k = 0; k < 7; ++k) lim[k] = __fmul_rn(thr[k], D[h]);
+#pragma unroll
+                for (int e = 16 * h; e < 16 * h + 16; ++e) w[e >> 3] = add_code(w[e >> 3], v[e], lim, 4 * (e & 7));
+            }
+            const int place = P.places[token];
+            const int64_t page = record_page(P.c, P.seqs[token], place);
+            if (page >= 0) {
+                const int64_t r = record_index(P.c, page, plane, head, place);
+                *reinterpret_cast<uint4 *>(P.c.codes + r * (P.c.head_dim / 2) + 16 * blk) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint32_t *>(P.c.scales + r * (P.c.head_dim / 16) + 2 * blk) =
+                    dbits[0] | (dbits[1] << 16);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Read: the eight-lane layout in reverse.  x~ = s . (H (c d)) / 32 in fp32
 // (tq_dequantize's order), rounded once to the output type.
 // ---------------------------------------------------------------------------
 struct ReadParams {
@@ -365,6 +485,85 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const ReadParams P)
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = flip(v[i], flips[i]);
         if (item < P.items) store4<DT>(base + ((int64_t)h * P.head_stride[plane] + e0) * E, v);
+    }
+}
+
+// Read, many tokens: a lane owns a block; a warp's 32 blocks leave through a
+// stage in shared memory (16-byte chunks, XOR-placed against bank conflicts), so
+// that stores cover whole head vectors instead of 64-byte pieces.
+template <int DT>
+__global__ void __launch_bounds__(kKvThreads, DT == kF32 ? 2 : 3) kv_read_block_kernel(const ReadParams P) {
+    constexpr int E = ElemSize<DT>::value, C = 2 * E;  // 16-byte chunks of a block
+    __shared__ float table[16];
+    __shared__ __align__(16) uint4 stage[kKvThreads * C];
+    if (threadIdx.x < 16)
+        table[threadIdx.x] = __uint_as_float(c_kv_mag_bits[threadIdx.x & 7] ^ ((threadIdx.x & 8u) << 28));
+    __syncthreads();
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int lane = threadIdx.x & 31;
+    uint4 *st = stage + (threadIdx.x & ~31) * C;
+    auto key = [](int l) { return C == 8 ? (l & 7) : ((l >> 1) & 3); };
+    const int64_t first = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) - lane;  // the warp's first block
+    // block i of all: (token, plane, head, block of the head), in this order
+    auto address = [&](int64_t i, int &plane, int &head, int &blk) {
+        blk = (int)(i % P.blocks);
+        int64_t rest = i / P.blocks;
+        head = (int)(rest % P.c.kv_heads);
+        rest /= P.c.kv_heads;
+        plane = (int)(rest & 1);
+        return rest >> 1;
+    };
+    if (first >= P.items) return;
+    {
+        const int64_t i = min(first + lane, P.items - 1);
+        int plane, head, blk;
+        const int64_t token = address(i, plane, head, blk);
+        const int place = P.places[token];
+        const int64_t page = record_page(P.c, P.seqs[token], place);
+        float v[32];
+        if (page >= 0) {
+            const int64_t r = record_index(P.c, page, plane, head, place);
+            const uint4 w4 = *reinterpret_cast<const uint4 *>(P.c.codes + r * (P.c.head_dim / 2) + 16 * blk);
+            const uint32_t sc = *reinterpret_cast<const uint32_t *>(P.c.scales + r * (P.c.head_dim / 16) + 2 * blk);
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            const float2 D = __half22float2(*reinterpret_cast<const __half2 *>(&sc));
+            const float Ds[2] = {__fmul_rn(D.x, 0.03125f), __fmul_rn(D.y, 0.03125f)};
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __fmul_rn(table[(w[e >> 3] >> (4 * (e & 7))) & 15u], Ds[e >> 4]);
+            fwht32_regs(v);
+            const uint32_t bits = c_sign_words.w[blk];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = flip(v[e], (bits << (31 - e)) & 0x80000000u);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            char *dst = reinterpret_cast<char *>(&st[lane * C + (c ^ key(lane))]);
+            if (DT == kF32) {
+                const float t[4] = {v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]};
+                store4<DT>(dst, t);
+            } else {
+                const float t[4] = {v[8 * c % 32], v[8 * c % 32 + 1], v[8 * c % 32 + 2], v[8 * c % 32 + 3]};
+                const float u[4] = {v[8 * c % 32 + 4], v[8 * c % 32 + 5], v[8 * c % 32 + 6], v[8 * c % 32 + 7]};
+                store4<DT>(dst, t);
+                store4<DT>(dst + 8, u);
+            }
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c0 = 0; c0 < C; ++c0) {
+        const int c = c0 * 32 + lane, l = c / C;
+        if (first + l < P.items) {
+            int plane, head, blk;
+            const int64_t token = address(first + l, plane, head, blk);
+            *reinterpret_cast<uint4 *>(
+                P.out[plane] + (token * P.token_stride[plane] + head * P.head_stride[plane] + 32 * blk) * E +
+                16 * (c % C)) = st[l * C + ((c % C) ^ key(l))];
+        }
     }
 }
 
@@ -449,6 +648,10 @@ int heads_per_item(int64_t threads_per_head, int heads, int64_t enough) {
     return h;
 }
 
+// Blocks from which on a lane takes a whole one (about three warps for each of
+// the GPU's 592 schedulers); below, eight lanes share a block and finish sooner.
+constexpr int64_t kManyBlocks = 1 << 16;
+
 unsigned blocks_of(int64_t threads) { return (unsigned)((threads + kKvThreads - 1) / kKvThreads); }
 
 }  // namespace
@@ -513,6 +716,20 @@ cudaError_t launch_kv_append(const KvAppendJob &j, cudaStream_t stream) {
     P.interleaved = j.interleaved;
     P.scale = j.scale;
     P.blocks = j.c.head_dim / 32;
+    // whole blocks per lane once there are enough of them, and where a block's
+    // rotary partners are a block too
+    const bool whole = !j.positions || (j.rot % 32 == 0 && (j.interleaved || j.rot % 64 == 0));
+    if (j.tokens * 2 * j.c.kv_heads * P.blocks >= kManyBlocks && whole) {
+        const int64_t of_token = j.c.kv_heads * P.blocks;  // blocks of a plane
+        int64_t per = of_token >= kKvThreads ? 1 : kKvThreads / of_token;
+        if (j.positions && per * (j.rot / 2) > kAngles) per = kAngles / (j.rot / 2);
+        P.items = j.tokens;
+        const unsigned grid = (unsigned)((j.tokens + per - 1) / per);
+        if (j.dtype == kF32) return launch_dependent(kv_append_block_kernel<kF32>, grid, kKvThreads, 0, stream, P, (int)per);
+        if (j.dtype == kBF16)
+            return launch_dependent(kv_append_block_kernel<kBF16>, grid, kKvThreads, 0, stream, P, (int)per);
+        return launch_dependent(kv_append_block_kernel<kF16>, grid, kKvThreads, 0, stream, P, (int)per);
+    }
     P.hchunk = heads_per_item(j.tokens * 2 * P.blocks * 8, j.c.kv_heads, (int64_t)1 << 18);
     P.chunks = (j.c.kv_heads + P.hchunk - 1) / P.hchunk;
     P.items = j.tokens * 2 * P.chunks * P.blocks;
@@ -535,6 +752,13 @@ cudaError_t launch_kv_read(const KvReadJob &j, cudaStream_t stream) {
     P.seqs = j.seqs;
     P.places = j.places;
     P.blocks = j.c.head_dim / 32;
+    P.items = j.tokens * 2 * j.c.kv_heads * P.blocks;
+    if (P.items >= kManyBlocks) {
+        const unsigned grid = blocks_of(P.items);
+        if (j.dtype == kF32) return launch_dependent(kv_read_block_kernel<kF32>, grid, kKvThreads, 0, stream, P);
+        if (j.dtype == kBF16) return launch_dependent(kv_read_block_kernel<kBF16>, grid, kKvThreads, 0, stream, P);
+        return launch_dependent(kv_read_block_kernel<kF16>, grid, kKvThreads, 0, stream, P);
+    }
     P.hchunk = heads_per_item(j.tokens * 2 * P.blocks * 8, j.c.kv_heads, (int64_t)1 << 18);
     P.chunks = (j.c.kv_heads + P.hchunk - 1) / P.hchunk;
     P.items = j.tokens * 2 * P.chunks * P.blocks;

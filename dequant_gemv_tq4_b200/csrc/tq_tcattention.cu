@@ -18,6 +18,7 @@
 //                  the score's own columns
 // While one stream's softmax runs, the tensor cores work for the other.
 #include "tq_attention.cuh"
+#include "tq_block.cuh"
 
 namespace tq {
 
@@ -317,26 +318,12 @@ __device__ __forceinline__ void rotate_row(const AttnParams &P, int64_t x, bool 
 }
 
 // ---- softmax of one row's 128 scores ---------------------------------------------
-// Packed fp32 pairs (each half one IEEE operation).
-__device__ __forceinline__ uint64_t a_pack(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void a_unpack(uint64_t r, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
-}
-__device__ __forceinline__ uint64_t a_fma2(uint64_t a, uint64_t b, uint64_t c) {
+// Packed fp32 pairs: each half one IEEE operation.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-__device__ __forceinline__ uint64_t a_add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // Output sums of this thread's row times f.
 template <int D>
 __device__ __forceinline__ void rescale_row(uint32_t t_o, float f) {
@@ -366,10 +353,10 @@ __device__ __forceinline__ void weights128(uint32_t *v, uint64_t scale2, uint64_
 #pragma unroll
     for (int e = 0; e < 128; e += 2) {
         float a, b;
-        a_unpack(a_fma2(a_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), scale2, off2), a, b);
+        unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), scale2, off2), a, b);
         a = ex2(a);
         b = ex2(b);
-        sum[(e >> 1) & 1] = a_add2(sum[(e >> 1) & 1], a_pack(a, b));
+        sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(a, b));
         const __half2 h = __floats2half2_rn(a, b);
         v[e / 2] = *reinterpret_cast<const uint32_t *>(&h);
         if ((e & 31) == 30) a_st16(t_p + (e >> 5) * 16u, v + (e >> 5) * 16);
@@ -391,8 +378,8 @@ __device__ __forceinline__ void follow(uint32_t t_o, float scale, bool have, flo
 
 __device__ __forceinline__ float sum_of(const uint64_t (&sum)[2]) {
     float s0, s1, s2, s3;
-    a_unpack(sum[0], s0, s1);
-    a_unpack(sum[1], s2, s3);
+    unpack2(sum[0], s0, s1);
+    unpack2(sum[1], s2, s3);
     return (s0 + s1) + (s2 + s3);
 }
 
@@ -406,7 +393,7 @@ __device__ __forceinline__ void softmax_row(uint32_t t_s, uint32_t t_o, float sc
     a_wait_ld();
     follow<D>(t_o, scale, have, max128(v, m), m, l);
     const float off = kWeightExp - m * scale;
-    const uint64_t scale2 = a_pack(scale, scale), off2 = a_pack(off, off);
+    const uint64_t scale2 = pack2(scale, scale), off2 = pack2(off, off);
     uint64_t sum[2] = {0, 0};
     weights128(v, scale2, off2, t_s, sum);
     l += sum_of(sum);

@@ -219,12 +219,16 @@ def test_append_is_the_codec_and_read_undoes_it(cuda_lib, dtype, n, seqs, kv, di
         assert torch.all((got - ref).abs() <= tol)
 
 
-@pytest.mark.parametrize("rot,interleaved,dtype,dim", [(128, False, F32, 128), (128, True, BF16, 128),
-                                                       (64, False, F16, 96), (50, False, F32, 64),
-                                                       (6, True, BF16, 32), (256, False, BF16, 256)])
-def test_append_rotates_keys(cuda_lib, rot, interleaved, dtype, dim):
-    n, kv, page = 150, 3, 32
-    codes, scales, table = _pool(cuda_lib, 2, 3, kv, dim, page)
+# (n = 150: eight lanes a block; more: a block per lane, or eight lanes where the halves are no whole blocks)
+@pytest.mark.parametrize("rot,interleaved,dtype,dim,n", [(128, False, F32, 128, 150), (128, True, BF16, 128, 150),
+                                                         (64, False, F16, 96, 150), (50, False, F32, 64, 150),
+                                                         (6, True, BF16, 32, 150), (256, False, BF16, 256, 150),
+                                                         (128, False, BF16, 128, 3001), (96, True, F16, 128, 2999),
+                                                         (64, False, F32, 96, 4001), (96, False, BF16, 128, 3001),
+                                                         (256, False, F32, 256, 1500)])
+def test_append_rotates_keys(cuda_lib, rot, interleaved, dtype, dim, n):
+    kv, page = 3, 32
+    codes, scales, table = _pool(cuda_lib, 2, -(-n // 2 // page) + 1, kv, dim, page)
     s, p = [i % 2 for i in range(n)], [i // 2 for i in range(n)]
     k, v = _rand(1, n, kv, dim, dtype=dtype), _rand(2, n, kv, dim, dtype=dtype)
     pos = torch.randint(0, 2000000, (n,), generator=torch.Generator().manual_seed(3)).to(torch.int32)
