@@ -59,6 +59,11 @@ struct RopeParams {
     int interleaved, inverse, copy_tail;
 };
 
+// Heads whose loads go out together: the output may be the input, so the
+// compiler cannot move a head's loads before another's stores by itself.
+template <int V>
+constexpr int kRopeAtOnce = V == 8 ? 2 : 4;
+
 // V elements at p: one 16-byte access or a scalar one.
 template <int DT, int V>
 __device__ __forceinline__ void load_v(const char *p, float (&v)[V]) {
@@ -108,7 +113,7 @@ __device__ __forceinline__ void store_v(char *p, const float (&v)[V]) {
 
 template <int DT, int V>
 __global__ void __launch_bounds__(kKvThreads) rope_kernel(const RopeParams P) {
-    constexpr int E = ElemSize<DT>::value;
+    constexpr int E = ElemSize<DT>::value, kRopeHeads = kRopeAtOnce<V>;
     grid_dependency_wait();
     grid_dependents_launch();
     const int64_t item = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
@@ -124,10 +129,14 @@ __global__ void __launch_bounds__(kKvThreads) rope_kernel(const RopeParams P) {
     if (slot >= P.rot_slots) {  // past the rotated part: copied
         if (!P.copy_tail) return;
         const int e = P.rot + (slot - P.rot_slots) * V;
-        for (int h = h0; h < h1; ++h) {
-            float v[V];
-            load_v<DT, V>(x + (h * P.x_head + e) * E, v);
-            store_v<DT, V>(o + (h * P.o_head + e) * E, v);
+        for (int h = h0; h < h1; h += kRopeHeads) {
+            float v[kRopeHeads][V];
+#pragma unroll
+            for (int k = 0; k < kRopeHeads; ++k)
+                if (h + k < h1) load_v<DT, V>(x + ((h + k) * P.x_head + e) * E, v[k]);
+#pragma unroll
+            for (int k = 0; k < kRopeHeads; ++k)
+                if (h + k < h1) store_v<DT, V>(o + ((h + k) * P.o_head + e) * E, v[k]);
         }
         return;
     }
@@ -138,29 +147,38 @@ __global__ void __launch_bounds__(kKvThreads) rope_kernel(const RopeParams P) {
     // pair i of the item: (a0 + i, a1 + i), or elements 2i, 2i+1 of 2V neighbours
     const int a0 = P.interleaved ? 2 * slot * V : slot * V;
     const int a1 = P.interleaved ? a0 + V : a0 + P.rot / 2;
-    for (int h = h0; h < h1; ++h) {
-        float u[V], w[V];
-        load_v<DT, V>(x + (h * P.x_head + a0) * E, u);
-        load_v<DT, V>(x + (h * P.x_head + a1) * E, w);
-        float ru[V], rw[V];
-        if (P.interleaved && V > 1) {
+    for (int h = h0; h < h1; h += kRopeHeads) {
+        float u[kRopeHeads][V], w[kRopeHeads][V];
 #pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const float2 c0 = cs[i / 2], c1 = cs[(V + i) / 2];
-                ru[i] = u[i] * c0.x - u[i + 1] * c0.y;
-                ru[i + 1] = u[i] * c0.y + u[i + 1] * c0.x;
-                rw[i] = w[i] * c1.x - w[i + 1] * c1.y;
-                rw[i + 1] = w[i] * c1.y + w[i + 1] * c1.x;
+        for (int k = 0; k < kRopeHeads; ++k)
+            if (h + k < h1) {
+                load_v<DT, V>(x + ((h + k) * P.x_head + a0) * E, u[k]);
+                load_v<DT, V>(x + ((h + k) * P.x_head + a1) * E, w[k]);
             }
-        } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                ru[i] = u[i] * cs[i].x - w[i] * cs[i].y;
-                rw[i] = u[i] * cs[i].y + w[i] * cs[i].x;
+        for (int k = 0; k < kRopeHeads; ++k) {
+            float ru[V], rw[V];
+            if (P.interleaved && V > 1) {
+#pragma unroll
+                for (int i = 0; i < V; i += 2) {
+                    const float2 c0 = cs[i / 2], c1 = cs[(V + i) / 2];
+                    ru[i] = u[k][i] * c0.x - u[k][i + 1] * c0.y;
+                    ru[i + 1] = u[k][i] * c0.y + u[k][i + 1] * c0.x;
+                    rw[i] = w[k][i] * c1.x - w[k][i + 1] * c1.y;
+                    rw[i + 1] = w[k][i] * c1.y + w[k][i + 1] * c1.x;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    ru[i] = u[k][i] * cs[i].x - w[k][i] * cs[i].y;
+                    rw[i] = u[k][i] * cs[i].y + w[k][i] * cs[i].x;
+                }
+            }
+            if (h + k < h1) {
+                store_v<DT, V>(o + ((h + k) * P.o_head + a0) * E, ru);
+                store_v<DT, V>(o + ((h + k) * P.o_head + a1) * E, rw);
             }
         }
-        store_v<DT, V>(o + (h * P.o_head + a0) * E, ru);
-        store_v<DT, V>(o + (h * P.o_head + a1) * E, rw);
     }
 }
 
@@ -321,16 +339,25 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendParam
 // ---------------------------------------------------------------------------
 constexpr int kAngles = 2048;  // cos, sin pairs of a CTA
 
+// 32 elements as they are in memory, and as fp32.
 template <int DT>
-__device__ __forceinline__ void load_block32(const char *p, float (&v)[32]) {
+struct RawBlock {
+    static constexpr int N = 2 * ElemSize<DT>::value;
+    uint4 q[N];
+    __device__ __forceinline__ void load(const char *p) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-        float t[4];
-        load4<DT>(p + i * ElemSize<DT>::value, t);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[i + k] = t[k];
+        for (int i = 0; i < N; ++i) q[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
     }
-}
+    __device__ __forceinline__ float at(int e) const {  // (e is a constant after unrolling)
+        const uint4 &w4 = q[e * ElemSize<DT>::value / 16];
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        if (DT == kF32) return __uint_as_float(w[e & 3]);
+        const uint32_t x = w[(e >> 1) & 3];
+        if (DT == kBF16) return __uint_as_float((e & 1) ? x & 0xffff0000u : x << 16);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+        return (e & 1) ? f.y : f.x;
+    }
+};
 
 // v rotated in place; block `blk` of the head at `x`, angles of its token at cs.
 template <int DT>
@@ -348,12 +375,12 @@ __device__ __forceinline__ void rotate_block(const AppendParams &P, const char *
         return;
     }
     const bool lower = e0 < half;
-    const char *p = x + (lower ? e0 + half : e0 - half) * ElemSize<DT>::value;
+    RawBlock<DT> raw;
+    raw.load(x + (lower ? e0 + half : e0 - half) * ElemSize<DT>::value);
     const float4 *c4 = reinterpret_cast<const float4 *>(cs + (lower ? e0 : e0 - half));
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
-        float o[4];
-        load4<DT>(p + i * ElemSize<DT>::value, o);
+        const float o[4] = {raw.at(i), raw.at(i + 1), raw.at(i + 2), raw.at(i + 3)};
         const float4 c0 = c4[i / 2], c1 = c4[i / 2 + 1];
         const float c[4] = {c0.x, c0.z, c1.x, c1.z}, sn[4] = {c0.y, c0.w, c1.y, c1.w};
 #pragma unroll
@@ -385,8 +412,13 @@ __global__ void __launch_bounds__(kKvThreads, 2) kv_append_block_kernel(const Ap
             const int head = rest / P.blocks, blk = rest - head * P.blocks;
             const int64_t token = token0 + t;
             const char *x = P.x[plane] + (token * P.token_stride[plane] + head * P.head_stride[plane]) * E;
+            RawBlock<DT> raw;
+            raw.load(x + 32 * blk * E);
+            const int place = P.places[token];
+            const int64_t page = record_page(P.c, P.seqs[token], place);
             float v[32];
-            load_block32<DT>(x + 32 * blk * E, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = raw.at(e);
             if (plane == 0 && P.positions && 32 * blk < P.rot) rotate_block<DT>(P, x, blk, angles + t * pairs, v);
             const uint32_t bits = c_sign_words.w[blk];
 #pragma unroll
@@ -416,8 +448,6 @@ __global__ void __launch_bounds__(kKvThreads, 2) kv_append_block_kernel(const Ap
 #pragma unroll
                 for (int e = 16 * h; e < 16 * h + 16; ++e) w[e >> 3] = add_code(w[e >> 3], v[e], lim, 4 * (e & 7));
             }
-            const int place = P.places[token];
-            const int64_t page = record_page(P.c, P.seqs[token], place);
             if (page >= 0) {
                 const int64_t r = record_index(P.c, page, plane, head, place);
                 *reinterpret_cast<uint4 *>(P.c.codes + r * (P.c.head_dim / 2) + 16 * blk) =
@@ -504,21 +534,17 @@ __global__ void __launch_bounds__(kKvThreads, DT == kF32 ? 2 : 3) kv_read_block_
     const int lane = threadIdx.x & 31;
     uint4 *st = stage + (threadIdx.x & ~31) * C;
     auto key = [](int l) { return C == 8 ? (l & 7) : ((l >> 1) & 3); };
-    const int64_t first = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) - lane;  // the warp's first block
-    // block i of all: (token, plane, head, block of the head), in this order
-    auto address = [&](int64_t i, int &plane, int &head, int &blk) {
-        blk = (int)(i % P.blocks);
-        int64_t rest = i / P.blocks;
-        head = (int)(rest % P.c.kv_heads);
-        rest /= P.c.kv_heads;
-        plane = (int)(rest & 1);
-        return rest >> 1;
-    };
+    // blocks in the order token, plane, head, block of the head; this lane's one
+    const int64_t first = ((int64_t)blockIdx.x * kKvThreads + threadIdx.x) - lane;
     if (first >= P.items) return;
+    const int per_token = 2 * P.c.kv_heads * P.blocks;
+    const int64_t i = min(first + lane, P.items - 1);
+    const int64_t token = i / per_token;
+    const int rest = (int)(i - token * per_token);
+    const int plane_head = rest / P.blocks, blk = rest - plane_head * P.blocks;
+    const int plane = plane_head >= P.c.kv_heads, head = plane_head - plane * P.c.kv_heads;
+    char *mine = P.out[plane] + (token * P.token_stride[plane] + head * P.head_stride[plane] + 32 * blk) * E;
     {
-        const int64_t i = min(first + lane, P.items - 1);
-        int plane, head, blk;
-        const int64_t token = address(i, plane, head, blk);
         const int place = P.places[token];
         const int64_t page = record_page(P.c, P.seqs[token], place);
         float v[32];
@@ -557,86 +583,91 @@ __global__ void __launch_bounds__(kKvThreads, DT == kF32 ? 2 : 3) kv_read_block_
 #pragma unroll
     for (int c0 = 0; c0 < C; ++c0) {
         const int c = c0 * 32 + lane, l = c / C;
-        if (first + l < P.items) {
-            int plane, head, blk;
-            const int64_t token = address(first + l, plane, head, blk);
-            *reinterpret_cast<uint4 *>(
-                P.out[plane] + (token * P.token_stride[plane] + head * P.head_stride[plane] + 32 * blk) * E +
-                16 * (c % C)) = st[l * C + ((c % C) ^ key(l))];
-        }
+        char *dst = reinterpret_cast<char *>(__shfl_sync(kFull, reinterpret_cast<unsigned long long>(mine), l));
+        if (first + l < P.items)
+            *reinterpret_cast<uint4 *>(dst + 16 * (c % C)) = st[l * C + ((c % C) ^ key(l))];
     }
 }
 
 // ---------------------------------------------------------------------------
 // Commit: the records of an accepted branch move down to where the sequence
-// continues.  One thread owns one 16-byte piece of the codes (or one 4-byte
-// piece of the scales) of a (layer, sequence, plane, head) and moves it for
-// the whole branch, eight records at a time: all eight loads before the
-// stores.  The branch increases, so a record's target never lies behind a
-// source that is still to be read.
+// continues.  A CTA takes one layer of one sequence: its first warp finds the
+// branch's records, once for all planes, heads and pieces; then a thread owns a
+// 16-byte piece of the codes (or 4 bytes of the scales) of a (plane, head) and
+// moves it for the whole branch, eight records at a time, all eight loads
+// before the stores.  The branch increases, so a record's target never lies
+// behind a source that is still to be read.
 // ---------------------------------------------------------------------------
 struct CommitParams {
     KvCache c;  // of layer 0
     int64_t code_layer, scale_layer;  // strides of a layer, elements
     const int32_t *lens, *path;
     int64_t path_ld;
-    int64_t items;  // layers * batch * 2 * heads * pieces
     int steps, pieces, code_pieces;
 };
+constexpr int kMaxSteps = 64;
 
+// Moves piece (plane_head, offset) of the branch's records; `from` and `to` are
+// the rows of plane 0, head 0 (to < 0: nothing to move).
 template <typename T>
-__device__ __forceinline__ void move_branch(const CommitParams &P, char *plane0, int64_t record_bytes, int seq,
-                                            int plane, int head, int offset) {
-    const int len = max(P.lens[seq], 0);
-    const int32_t *path = P.path + seq * P.path_ld;
-    int last = -1;
-    for (int i0 = 0; i0 < P.steps; i0 += 8) {
+__device__ __forceinline__ void move_branch(char *pool, const int64_t *from, const int64_t *to, int count,
+                                            int64_t row, int64_t record_bytes, int offset) {
+    for (int i0 = 0; i0 < count; i0 += 8) {
         T v[8];
-        int64_t to[8];
-        bool end = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            to[i] = -1;
-            const int src = !end && i0 + i < P.steps ? path[i0 + i] : -1;
-            if (src <= last || src > INT32_MAX - len) {  // the branch ends here
-                end = true;
-                continue;
-            }
-            last = src;
-            if (src == i0 + i) continue;  // in place already
-            const int64_t from_page = record_page(P.c, seq, len + src);
-            const int64_t to_page = record_page(P.c, seq, len + i0 + i);
-            if (from_page < 0 || to_page < 0) continue;
-            v[i] = *reinterpret_cast<const T *>(
-                plane0 + record_index(P.c, from_page, plane, head, len + src) * record_bytes + offset);
-            to[i] = record_index(P.c, to_page, plane, head, len + i0 + i) * record_bytes + offset;
-        }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (to[i] >= 0) *reinterpret_cast<T *>(plane0 + to[i]) = v[i];
-        if (end) return;
+            if (i0 + i < count && to[i0 + i] >= 0)
+                v[i] = *reinterpret_cast<const T *>(pool + (from[i0 + i] + row) * record_bytes + offset);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i0 + i < count && to[i0 + i] >= 0)
+                *reinterpret_cast<T *>(pool + (to[i0 + i] + row) * record_bytes + offset) = v[i];
     }
 }
 
 __global__ void __launch_bounds__(kKvThreads) kv_commit_kernel(const CommitParams P) {
+    __shared__ int64_t from[kMaxSteps], to[kMaxSteps];
+    __shared__ int branch;
     grid_dependency_wait();
     grid_dependents_launch();
-    const int64_t item = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
-    if (item >= P.items) return;
-    const int piece = (int)(item % P.pieces);
-    int64_t rest = item / P.pieces;
-    const int head = (int)(rest % P.c.kv_heads);
-    rest /= P.c.kv_heads;
-    const int plane = (int)(rest & 1);
-    rest >>= 1;
-    const int seq = (int)(rest % P.c.batch);
-    const int64_t layer = rest / P.c.batch;
-    if (piece < P.code_pieces)
-        move_branch<uint4>(P, reinterpret_cast<char *>(P.c.codes + layer * P.code_layer), P.c.head_dim / 2, seq, plane,
-                           head, 16 * piece);
-    else
-        move_branch<uint32_t>(P, reinterpret_cast<char *>(P.c.scales + layer * P.scale_layer), P.c.head_dim / 8, seq,
-                              plane, head, 4 * (piece - P.code_pieces));
+    const int seq = blockIdx.x % P.c.batch, lane = threadIdx.x & 31;
+    const int64_t layer = blockIdx.x / P.c.batch;
+    if (threadIdx.x < 32) {
+        const int len = max(P.lens[seq], 0);
+        const int32_t *path = P.path + seq * P.path_ld;
+        uint32_t ends[2];
+        int src[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = lane + 32 * k;
+            src[k] = i < P.steps ? path[i] : -1;
+            const int before = i > 0 && i < P.steps ? path[i - 1] : -1;
+            ends[k] = __ballot_sync(kFull, i >= P.steps || src[k] <= before || src[k] > INT32_MAX - len);
+        }
+        const int count = ends[0] ? __ffs(ends[0]) - 1 : ends[1] ? 31 + __ffs(ends[1]) : 64;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = lane + 32 * k;
+            if (i >= count) continue;
+            const int64_t a = record_page(P.c, seq, len + src[k]), z = record_page(P.c, seq, len + i);
+            const bool moves = src[k] != i && a >= 0 && z >= 0;
+            from[i] = moves ? record_index(P.c, a, 0, 0, len + src[k]) : -1;
+            to[i] = moves ? record_index(P.c, z, 0, 0, len + i) : -1;
+        }
+        if (lane == 0) branch = count;
+    }
+    __syncthreads();
+    const int count = branch;
+    for (int item = threadIdx.x; item < 2 * P.c.kv_heads * P.pieces; item += blockDim.x) {
+        const int plane_head = item / P.pieces, piece = item - plane_head * P.pieces;
+        const int64_t row = (int64_t)plane_head << P.c.page_shift;
+        if (piece < P.code_pieces)
+            move_branch<uint4>(reinterpret_cast<char *>(P.c.codes + layer * P.code_layer), from, to, count, row,
+                               P.c.head_dim / 2, 16 * piece);
+        else
+            move_branch<uint32_t>(reinterpret_cast<char *>(P.c.scales + layer * P.scale_layer), from, to, count, row,
+                                  P.c.head_dim / 8, 4 * (piece - P.code_pieces));
+    }
 }
 
 // Heads per work item: as many as share work (angles, indices) while the
@@ -781,8 +812,10 @@ cudaError_t launch_kv_commit(const KvCommitJob &j, cudaStream_t stream) {
     P.steps = j.steps;
     P.code_pieces = j.c.head_dim / 32;
     P.pieces = P.code_pieces + j.c.head_dim / 32;
-    P.items = j.layers * j.c.batch * 2 * j.c.kv_heads * P.pieces;
-    return launch_dependent(kv_commit_kernel, blocks_of(P.items), kKvThreads, 0, stream, P);
+    // (a CTA no wider than a layer's pieces need)
+    const int pieces = 2 * j.c.kv_heads * P.pieces;
+    const unsigned threads = pieces >= kKvThreads ? kKvThreads : (unsigned)(pieces + 31) / 32 * 32;
+    return launch_dependent(kv_commit_kernel, (unsigned)(j.layers * j.c.batch), threads, 0, stream, P);
 }
 
 }  // namespace tq
