@@ -57,11 +57,6 @@ __device__ __forceinline__ int worker_count(const AttnParams &P, int64_t W) {
     return (int)(n < P.workers ? n : P.workers);
 }
 
-// a / b of non-negative numbers, in 32 bits where both fit
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

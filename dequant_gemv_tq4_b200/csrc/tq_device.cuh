@@ -209,6 +209,11 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&o)[4]) {
     o[3] = prmt(lo47, hi47, 0x7362u);  // elements 6, 7
 }
 
+// a / b of non-negative numbers, in 32 bits where both fit
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // L2 prefetch hint for the line holding p (no data returned, no fault on a
 // valid address).
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }

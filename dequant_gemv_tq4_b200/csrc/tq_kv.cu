@@ -389,7 +389,7 @@ __device__ __forceinline__ void rotate_block(const AppendParams &P, const char *
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kKvThreads, 2) kv_append_block_kernel(const AppendParams P, int per_cta) {
+__global__ void __launch_bounds__(kKvThreads, DT == kF32 ? 2 : 3) kv_append_block_kernel(const AppendParams P, int per_cta) {
     constexpr int E = ElemSize<DT>::value;
     __shared__ __align__(16) float2 angles[kAngles];
     grid_dependency_wait();
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kKvThreads, DT == kF32 ? 2 : 3) kv_read_block_
     if (first >= P.items) return;
     const int per_token = 2 * P.c.kv_heads * P.blocks;
     const int64_t i = min(first + lane, P.items - 1);
-    const int64_t token = i / per_token;
+    const int64_t token = quotient(i, per_token);
     const int rest = (int)(i - token * per_token);
     const int plane_head = rest / P.blocks, blk = rest - plane_head * P.blocks;
     const int plane = plane_head >= P.c.kv_heads, head = plane_head - plane * P.c.kv_heads;
@@ -558,25 +558,32 @@ __global__ void __launch_bounds__(kKvThreads, DT == kF32 ? 2 : 3) kv_read_block_
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = __fmul_rn(table[(w[e >> 3] >> (4 * (e & 7))) & 15u], Ds[e >> 4]);
             fwht32_regs(v);
-            const uint32_t bits = c_sign_words.w[blk];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = flip(v[e], (bits << (31 - e)) & 0x80000000u);
         } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = 0.f;
         }
+        // rounded, signs put on the rounded values
+        const uint32_t signs = DT == kF32 ? c_sign_words.w[blk] : c_sign_pairs.w[blk];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            char *dst = reinterpret_cast<char *>(&st[lane * C + (c ^ key(lane))]);
-            if (DT == kF32) {
-                const float t[4] = {v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]};
-                store4<DT>(dst, t);
-            } else {
-                const float t[4] = {v[8 * c % 32], v[8 * c % 32 + 1], v[8 * c % 32 + 2], v[8 * c % 32 + 3]};
-                const float u[4] = {v[8 * c % 32 + 4], v[8 * c % 32 + 5], v[8 * c % 32 + 6], v[8 * c % 32 + 7]};
-                store4<DT>(dst, t);
-                store4<DT>(dst + 8, u);
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (DT == kF32) {
+                    o[k] = __float_as_uint(v[4 * c + k]) ^ ((signs << (31 - 4 * c - k)) & 0x80000000u);
+                } else {
+                    const int p = (4 * c + k) % 16;  // pair
+                    if (DT == kBF16) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * p], v[2 * p + 1]);
+                        o[k] = *reinterpret_cast<const uint32_t *>(&h);
+                    } else {
+                        const __half2 h = __floats2half2_rn(v[2 * p], v[2 * p + 1]);
+                        o[k] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                    o[k] ^= (signs << (15 - p)) & 0x80008000u;
+                }
             }
+            st[lane * C + (c ^ key(lane))] = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
     __syncwarp();

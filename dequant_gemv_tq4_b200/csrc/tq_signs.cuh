@@ -23,4 +23,17 @@ constexpr SignWords sign_words() {
 }
 static __constant__ SignWords c_sign_words = sign_words();
 
+// The same for pairs of 16-bit values: word b has the signs of block b's even
+// columns in its low half and of the odd ones in its high half, so that one
+// shift brings column pair i to bits 15 and 31.
+constexpr SignWords sign_pairs() {
+    const SignWords s = sign_words();
+    SignWords p = {};
+    for (int b = 0; b < 8; ++b)
+        for (int i = 0; i < 16; ++i)
+            p.w[b] |= ((s.w[b] >> (2 * i)) & 1u) << i | ((s.w[b] >> (2 * i + 1)) & 1u) << (16 + i);
+    return p;
+}
+static __constant__ SignWords c_sign_pairs = sign_pairs();
+
 }  // namespace tq
