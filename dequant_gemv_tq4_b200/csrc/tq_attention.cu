@@ -91,7 +91,7 @@ __device__ __forceinline__ void rotate_query(const AttnParams &P, const char *x,
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
                 float t[4];
-                load4<DT>(x + (int64_t)(e0 + i) * ElemSize<DT>::value, t);
+                load4_ordinary<DT>(x + (int64_t)(e0 + i) * ElemSize<DT>::value, t);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i + k] = flip(t[k], (bits << (31 - i - k)) & 0x80000000u);
             }
@@ -167,8 +167,8 @@ __device__ __forceinline__ void load_keys(const uint8_t *codes, const uint8_t *s
             uint2 w = make_uint2(0u, 0u);
             uint32_t d = 0;
             if (FULL || 16 * c < dim) {
-                w = __ldg(reinterpret_cast<const uint2 *>(cp));
-                d = __ldg(reinterpret_cast<const uint16_t *>(sp));
+                w = ld(reinterpret_cast<const uint2 *>(cp));
+                d = ld(reinterpret_cast<const uint16_t *>(sp));
             }
             r.w[i][0] = w.x;
             r.w[i][1] = w.y;
@@ -179,8 +179,8 @@ __device__ __forceinline__ void load_keys(const uint8_t *codes, const uint8_t *s
                 uint4 w = make_uint4(0u, 0u, 0u, 0u);
                 uint32_t d = 0;
                 if (FULL || c * (DP / 4) + 32 * j < dim) {
-                    w = __ldg(reinterpret_cast<const uint4 *>(cp) + j);
-                    d = __ldg(reinterpret_cast<const uint32_t *>(sp) + j);
+                    w = ld(reinterpret_cast<const uint4 *>(cp) + j);
+                    d = ld(reinterpret_cast<const uint32_t *>(sp) + j);
                 }
                 r.w[i][4 * j] = w.x;
                 r.w[i][4 * j + 1] = w.y;
@@ -207,20 +207,20 @@ __device__ __forceinline__ void load_values(const uint8_t *codes, const uint8_t 
         for (int j = 0; j < ValueRegs<DP>::W; ++j) r.w[t][j] = 0;
         if (FULL || g * (DP / 8) < dim) {
             if constexpr (DP == 64) {
-                r.w[t][0] = __ldg(reinterpret_cast<const uint32_t *>(cp));
-                r.d[t] = __ldg(reinterpret_cast<const uint16_t *>(sp));
+                r.w[t][0] = ld(reinterpret_cast<const uint32_t *>(cp));
+                r.d[t] = ld(reinterpret_cast<const uint16_t *>(sp));
             } else if constexpr (DP == 128) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(cp));
+                const uint2 w = ld(reinterpret_cast<const uint2 *>(cp));
                 r.w[t][0] = w.x;
                 r.w[t][1] = w.y;
-                r.d[t] = __ldg(reinterpret_cast<const uint16_t *>(sp));
+                r.d[t] = ld(reinterpret_cast<const uint16_t *>(sp));
             } else {
-                const uint4 w = __ldg(reinterpret_cast<const uint4 *>(cp));
+                const uint4 w = ld(reinterpret_cast<const uint4 *>(cp));
                 r.w[t][0] = w.x;
                 r.w[t][1] = w.y;
                 r.w[t][2] = w.z;
                 r.w[t][3] = w.w;
-                r.d[t] = __ldg(reinterpret_cast<const uint32_t *>(sp));
+                r.d[t] = ld(reinterpret_cast<const uint32_t *>(sp));
             }
         }
     }

@@ -280,13 +280,13 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendParam
     for (int h = h0; h < h1; ++h) {
         const char *x = base + (int64_t)h * P.head_stride[plane] * E;
         float v[4];
-        load4<DT>(x + e0 * E, v);
+        load4_ordinary<DT>(x + e0 * E, v);
         if (rotate) {
             float o[4];
             if (P.interleaved) {
                 o[0] = v[1]; o[1] = v[0]; o[2] = v[3]; o[3] = v[2];
             } else if (whole) {
-                load4<DT>(x + first * E, o);
+                load4_ordinary<DT>(x + first * E, o);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -346,7 +346,7 @@ struct RawBlock {
     uint4 q[N];
     __device__ __forceinline__ void load(const char *p) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) q[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        for (int i = 0; i < N; ++i) q[i] = ld(reinterpret_cast<const uint4 *>(p) + i);
     }
     __device__ __forceinline__ float at(int e) const {  // (e is a constant after unrolling)
         const uint4 &w4 = q[e * ElemSize<DT>::value / 16];

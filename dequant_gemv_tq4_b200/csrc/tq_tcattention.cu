@@ -246,10 +246,10 @@ __device__ __forceinline__ void load_token(const AttnParams &P, int64_t rec, boo
         const uint4 *codes = reinterpret_cast<const uint4 *>(P.c.codes + rec * (D / 2));
         const uint2 *scales = reinterpret_cast<const uint2 *>(P.c.scales + rec * (D / 16));
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) r.w[i] = __ldg(codes + i);
+        for (int i = 0; i < D / 32; ++i) r.w[i] = ld(codes + i);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-            const uint2 d = __ldg(scales + i);
+            const uint2 d = ld(scales + i);
             r.d[2 * i] = d.x;
             r.d[2 * i + 1] = d.y;
         }
@@ -290,7 +290,7 @@ __device__ __forceinline__ void rotate_row(const AttnParams &P, int64_t x, bool 
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
             float t[4] = {0.f, 0.f, 0.f, 0.f};
-            if (valid) load4<DT>(at + (int64_t)(32 * blk + i) * E, t);
+            if (valid) load4_ordinary<DT>(at + (int64_t)(32 * blk + i) * E, t);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[i + k] = flip(t[k], (bits << (31 - i - k)) & 0x80000000u);
         }
