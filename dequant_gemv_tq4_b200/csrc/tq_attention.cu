@@ -377,7 +377,8 @@ struct AttnShared {
     int scan[32];
 };
 constexpr int kAttnSmem = (int)(kLutBase + 256 * kLutStep);
-static_assert(sizeof(AttnShared) + 4096 <= kLutBase, "shared memory below the table");
+constexpr int kMaxSmemBase = 4096;
+static_assert(sizeof(AttnShared) + kMaxSmemBase <= kLutBase, "shared memory below the table");
 
 // A value that is the same in every lane, told so.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(kFull, x, 0); }
@@ -757,8 +758,15 @@ AttnPlan plan_attention(int64_t batch, int tree, int heads, int kv_heads, int he
 
 template <int DP, int NT, int WARPS, bool FULL>
 cudaError_t launch_attend_as(const AttnParams &P, cudaStream_t stream) {
-    static SharedMemoryLimit limit;
-    const cudaError_t e = limit.raise(attend_kernel<DP, NT, WARPS, FULL>, kAttnSmem);
+    // the table stands at a fixed address: dynamic shared memory has to begin
+    // low enough for what lies below it
+    int dev = 0, reserved = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
+    if (e == cudaSuccess && reserved > kMaxSmemBase) e = cudaErrorInvalidValue;
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attend_kernel<DP, NT, WARPS, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kAttnSmem);
     if (e != cudaSuccess) return e;
     return launch_dependent(attend_kernel<DP, NT, WARPS, FULL>, P.workers / WARPS, WARPS * 32, kAttnSmem, stream, P);
 }
@@ -831,6 +839,8 @@ cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t s
     P.parts = plan.parts;
     P.tile_rows = plan.tile_rows;
     P.header = reinterpret_cast<unsigned *>(j.workspace);
+    P.inject_skip = (debug_flags() & kDebugSkipCacheKeys) ? 1 : 0;
+    P.timeout_cycles = P.inject_skip ? 10000000ll : 2000000000ll;  // about 5 ms, a second
     char *ws = j.workspace + 256;
     P.prefix = reinterpret_cast<int *>(ws);
     ws += round_up((size_t)(j.c.batch + 1) * 4, 256);

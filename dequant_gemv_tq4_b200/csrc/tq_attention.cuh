@@ -4,8 +4,6 @@
 
 #include <math.h>
 
-#include <atomic>
-
 #include <type_traits>
 
 #include "tq_device.cuh"
@@ -38,6 +36,8 @@ struct AttnParams {
     int parts;       // partial results that a worker leaves of a unit
     int tile_rows;   // rows of a partial result
     unsigned *header;  // status word
+    long long timeout_cycles;  // of a wait in the tcgen05 kernel
+    int inject_skip;           // test hook: its first CTA never hands over its first keys
     int *prefix;     // [batch + 1] groups before each sequence
     float *part_ml;  // [slots][tile_rows][2]: maximum, sum
     float *part_o;   // [slots][tile_rows][head_dim]
@@ -164,25 +164,6 @@ __device__ __forceinline__ void scan_sequences(const AttnParams &P, int *prefix,
     if (tid == threads - 1) prefix[P.c.batch] = base + inc;
     __syncthreads();
 }
-
-// Raises a kernel's dynamic shared memory limit, once on each device.
-class SharedMemoryLimit {
-    std::atomic<uint64_t> done[4] = {};  // a bit per device
-
-public:
-    template <typename K>
-    cudaError_t raise(K kernel, int bytes) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        if (dev < 0 || dev >= 256) return cudaErrorInvalidDevice;
-        const uint64_t bit = 1ull << (dev & 63);
-        if (done[dev >> 6].load(std::memory_order_relaxed) & bit) return cudaSuccess;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e == cudaSuccess) done[dev >> 6].fetch_or(bit, std::memory_order_relaxed);
-        return e;
-    }
-};
 
 // The launch that joins the parts of every row, rotates back, divides and
 // rounds; a programmatic dependent of the attention launch before it.

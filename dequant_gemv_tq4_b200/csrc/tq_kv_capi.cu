@@ -26,7 +26,9 @@ tq_status check_cache(const tq_kv_cache *c, tq::KvCache *out) {
     if (c->pages < 0 || c->batch < 0 || c->pages_per_seq < 0 || c->page_table_ld < c->pages_per_seq)
         return TQ_ERR_INVALID_ARG;
     if (c->batch > TQ_KV_MAX_BATCH || c->pages > INT32_MAX) return TQ_ERR_SHAPE;
+    // places fit 31 bits, and so do the groups of 16 tokens of all sequences
     if (c->pages_per_seq > ((int64_t)1 << 30) / c->page_size) return TQ_ERR_SHAPE;
+    if (c->pages_per_seq * c->page_size > TQ_KV_MAX_CAPACITY / (c->batch > 0 ? c->batch : 1)) return TQ_ERR_SHAPE;
     if (c->pages > 0 && (!c->codes || !c->scales)) return TQ_ERR_INVALID_ARG;
     if (c->batch > 0 && c->pages_per_seq > 0 && !c->page_table) return TQ_ERR_INVALID_ARG;
     if (!aligned(c->codes, 16) || !aligned(c->scales, 16) || !aligned(c->page_table, 4)) return TQ_ERR_ALIGNMENT;

@@ -315,7 +315,9 @@ TQ_API tq_status tq_workspace_status(void *workspace, int clear, void *stream);
  * the same for the tensor-core prefill product (tq_gemm_prefill and m > 32):
  * the first CTA never issues its second activation-tile copy (nor counts its
  * bytes), its waits expire after ~5 ms, every tensor-memory column is still
- * released, and the status word is set.
+ * released, and the status word is set.  Bit 5: the same for the tcgen05
+ * attention kernel (tq_kv_attention): its first CTA never hands over its
+ * first keys.
  */
 TQ_API void tq_debug_set_flags(uint32_t flags);
 
@@ -465,7 +467,8 @@ TQ_API tq_status tq_nvfp4_gemm_batch(const tq_nvfp4_gemm_desc *descs, int count,
  *    attention leaves it out.
  *  - Sizes: head_dim a multiple of 32 up to TQ_KV_MAX_HEAD_DIM; page_size a
  *    power of two from 16 to TQ_KV_MAX_PAGE; a sequence's table spans at most
- *    2^30 tokens.  Offsets into the pool are 64-bit.
+ *    2^30 tokens, the whole table TQ_KV_MAX_CAPACITY.  Offsets into the pool
+ *    are 64-bit.
  *
  * Head operands (x, k, v, q, out) are [tokens][heads][dim] with unit element
  * stride and the strides given, in elements.
@@ -479,6 +482,7 @@ TQ_API tq_status tq_nvfp4_gemm_batch(const tq_nvfp4_gemm_desc *descs, int count,
 #define TQ_KV_MAX_TOKENS ((int64_t)1 << 24)
 #define TQ_ROPE_MAX_DIM 1024
 #define TQ_KV_MAX_SCALE 65536.0f
+#define TQ_KV_MAX_CAPACITY ((int64_t)1 << 34)
 
 typedef struct {
     uint8_t *codes;            /* device, 16-byte aligned */
@@ -575,8 +579,13 @@ TQ_API tq_status tq_kv_read(const tq_kv_cache *cache, const int32_t *seqs, const
  *            `stream`; need not be cleared, keeps nothing between calls
  * The rotated query, centroid times scale and the softmax weights enter the
  * tensor cores as fp16; sums, the running maximum and the softmax's sum are
- * fp32.  A record that no row attends to may hold anything.
- * tree <= TQ_KV_MAX_TREE.
+ * fp32.  A record that no row attends to may hold anything; one that some row
+ * attends to holds finite scales (tq_kv_append writes no others).
+ * tree <= TQ_KV_MAX_TREE.  Up to 16 rows (tree * heads / kv_heads) of a
+ * key/value head, and every head_dim other than 64 and 128, run the mma.sync
+ * kernel; more rows the tcgen05 kernel, whose waits are bounded: one that
+ * expires (after about a second) is recorded in the workspace's status word,
+ * see tq_workspace_status, and the outputs are then incomplete.  Two launches.
  */
 TQ_API size_t tq_kv_attention_workspace_bytes(int64_t batch, int64_t tree, int64_t heads, int64_t kv_heads,
                                               int64_t head_dim);

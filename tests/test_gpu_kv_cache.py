@@ -397,6 +397,12 @@ CASES = [
     (1, 7, 71, 1, 128, 16, [333], F16, "tree"),
     (1, 9, 8, 1, 256, 16, [222], BF16, "absent"),
     (40, 1, 4, 2, 64, 16, [7 * i for i in range(40)], F16, None),
+    (1, 3, 2, 1, 192, 1024, [1500], BF16, "tree"),
+    (2, 1, 16, 2, 224, 256, [0, 700], F16, None),
+    (1, 5, 34, 2, 128, 512, [900], F32, "tree"),  # 85 rows on the tensor cores, some of a warp's missing
+    (3, 50, 3, 1, 64, 16, [0, 128, 700], BF16, "absent"),  # 150 rows: a row tile of its own for the last 22
+    (1, 1, 4, 1, 64, 1024, [45000], F16, None),  # more parts than a warp joins at once
+    (1, 24, 4, 2, 128, 64, [30000], BF16, "tree"),
 ]
 
 
@@ -418,6 +424,7 @@ def test_attention(cuda_lib, case):
     # run again: the same bits, whatever the workspace held
     ws = cuda_lib.kv_attention_workspace(B, T, H, kv, D).fill_(255)
     assert torch.equal(cuda_lib.kv_attention(codes, scales, table, _i32(lens), q.to(DEV), parents=par, ws=ws), got)
+    assert cuda_lib.workspace_status(ws) == 0
 
 
 @pytest.mark.parametrize("out_dtype", [F32, BF16, F16])
@@ -500,6 +507,61 @@ def test_attention_invalid_pages_and_lengths(cuda_lib):
     assert torch.equal(a, b)
     assert cuda_lib.kv_attention(codes, scales, table[:0], _i32([]), q[:0].to(DEV)).shape == (0, T, H, D)
     assert cuda_lib.kv_attention(codes, scales, table, _i32(lens), q[:, :0].to(DEV)).shape == (B, 0, H, D)
+
+
+def test_attention_refuses_a_small_or_crooked_workspace(cuda_lib):
+    codes, scales, table = _pool(cuda_lib, 2, 2, 2, 64, 16)
+    q = torch.zeros(2, 3, 4, 64, device=DEV)
+    need = cuda_lib.tq_kv_attention_workspace_bytes(2, 3, 4, 2, 64)
+    ws = torch.empty(need + 256, dtype=torch.uint8, device=DEV)
+    cuda_lib.kv_attention(codes, scales, table, _i32([1, 2]), q, ws=ws[:need])
+    for bad in (ws[:need - 1], ws[8:]):
+        with pytest.raises(cuda_lib.TQError, match="WORKSPACE"):
+            cuda_lib.kv_attention(codes, scales, table, _i32([1, 2]), q, ws=bad)
+    with pytest.raises(ValueError, match="lens"):
+        cuda_lib.kv_attention(codes, scales, table, _i32([1, 2, 3]), q)
+    with pytest.raises(ValueError, match="parents"):
+        cuda_lib.kv_attention(codes, scales, table, _i32([1, 2]), q, parents=_i32([[0, 0]]))
+    with pytest.raises(ValueError, match="q"):
+        cuda_lib.kv_attention(codes, scales, table, _i32([1, 2]), q[:1])
+    with pytest.raises(cuda_lib.TQError, match="ALIGNMENT"):
+        cuda_lib.kv_attention(codes, scales, table, _i32([1, 2]), torch.zeros(2, 3, 4, 68, device=DEV)[..., 2:66])
+    with pytest.raises(TypeError):
+        cuda_lib.kv_attention(codes, scales, table, _i32([1, 2]), q.double())
+
+
+def test_attention_rows_do_not_touch_one_another(cuda_lib):
+    """NaN and infinity in one query row leave every other row's bits alone, on both kernels."""
+    for T, H, kv in ((3, 4, 2), (16, 8, 2)):
+        B, D, page = 2, 128, 16
+        codes, scales, table = _filled(cuda_lib, B, 8, kv, D, page, seed=61)
+        q, lens = _rand(2, B, T, H, D, dtype=BF16).to(DEV), _i32([70, 100])
+        want = cuda_lib.kv_attention(codes, scales, table, lens, q)
+        bad = q.clone()
+        bad[0, 1, 2], bad[1, 2, 3, 5] = float("nan"), float("inf")
+        got = cuda_lib.kv_attention(codes, scales, table, lens, bad)
+        keep = torch.ones(B, T, H, dtype=torch.bool)
+        keep[0, 1, 2] = keep[1, 2, 3] = False
+        assert torch.equal(got.cpu()[keep], want.cpu()[keep])
+
+
+def test_attention_reports_a_wait_that_runs_out(cuda_lib):
+    """The tcgen05 kernel's bounded waits: keys that are never handed over end in a
+    status, not in a hang, and the next call is right again."""
+    B, T, H, kv, D, page = 2, 16, 8, 2, 128, 16
+    codes, scales, table = _filled(cuda_lib, B, 20, kv, D, page, seed=71)
+    q, lens = _rand(1, B, T, H, D, dtype=BF16).to(DEV), _i32([250, 300])
+    ws = cuda_lib.kv_attention_workspace(B, T, H, kv, D)
+    want = cuda_lib.kv_attention(codes, scales, table, lens, q, ws=ws)
+    assert cuda_lib.workspace_status(ws) == 0
+    cuda_lib.tq_debug_set_flags(32)
+    try:
+        cuda_lib.kv_attention(codes, scales, table, lens, q, ws=ws)
+    finally:
+        cuda_lib.tq_debug_set_flags(0)
+    assert cuda_lib.workspace_status(ws, clear=False) == 8
+    assert torch.equal(cuda_lib.kv_attention(codes, scales, table, lens, q, ws=ws), want)
+    assert cuda_lib.workspace_status(ws) == 0
 
 
 def test_attention_far_pages(cuda_lib):

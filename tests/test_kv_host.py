@@ -37,6 +37,7 @@ CACHE_ERRORS = [
     (dict(page_size=0), INVALID), (dict(page_size=8), SHAPE), (dict(page_size=48), SHAPE),
     (dict(page_size=2048), SHAPE), (dict(batch=4097), SHAPE), (dict(pages=1 << 31), SHAPE),
     (dict(pages_per_seq=(1 << 26) + 1, page_table_ld=1 << 27), SHAPE),
+    (dict(batch=512, pages_per_seq=1 << 22, page_table_ld=1 << 22), SHAPE),
 ]
 
 
