@@ -10,7 +10,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtq.so")
 SOURCES = ["tq_codec.cu", "tq_gemv.cu", "tq_tcgemv.cu", "tq_nvfp4.cu", "tq_prefill.cu", "tq_kv.cu",
            "tq_attention.cu", "tq_tcattention.cu", "tq_capi.cu", "tq_kv_capi.cu"]
-HEADERS = ["tq_device.cuh", "tq_block.cuh", "tq_signs.cuh", "tq_attention.cuh", "tq_internal.h", "tq_codebook.h",
+HEADERS = ["tq_device.cuh", "tq_cache.cuh", "tq_attention.cuh", "tq_internal.h", "tq_codebook.h",
            os.path.join("..", "..", "include", "tq.h")]
 
 NVCC_FLAGS = [

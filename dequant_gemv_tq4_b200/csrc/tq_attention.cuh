@@ -6,8 +6,7 @@
 
 #include <type_traits>
 
-#include "tq_device.cuh"
-#include "tq_signs.cuh"
+#include "tq_cache.cuh"
 #include "tq_internal.h"
 
 namespace tq {

@@ -1,11 +1,76 @@
-// tq_block.cuh -- a 32-element block in one lane's registers: the transform in
-// the codec's stage order and the code of a value, shared by the weight codec and
-// the key/value cache.
+// tq_cache.cuh -- what the key/value cache's kernels and the attention over it
+// share: ordinary loads, the sign pattern of a head's columns, and a 32-element
+// block in one lane's registers, with the arithmetic of the weight codec
+// (tq_codec.cu), operation for operation.
 #pragma once
 
-#include <stdint.h>
+#include "tq_device.cuh"
 
 namespace tq {
+
+// An ordinary load.  A programmatic dependent that reads what the kernel before
+// it writes uses this after its wait: the read-only path (load4, __ldg) asks for
+// data that nobody writes while the kernel is resident.
+template <typename T>
+__device__ __forceinline__ T ld(const T *p) {
+    return *p;
+}
+
+// load4 by ordinary loads.
+template <int DT>
+__device__ __forceinline__ void load4_ordinary(const void *p, float (&v)[4]) {
+    if constexpr (DT == kF32) {
+        const float4 q = ld(reinterpret_cast<const float4 *>(p));
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+        const uint2 q = ld(reinterpret_cast<const uint2 *>(p));
+        if constexpr (DT == kBF16) {
+            v[0] = __uint_as_float(q.x << 16);
+            v[1] = __uint_as_float(q.x & 0xffff0000u);
+            v[2] = __uint_as_float(q.y << 16);
+            v[3] = __uint_as_float(q.y & 0xffff0000u);
+        } else {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&q.x));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&q.y));
+            v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+        }
+    }
+}
+
+// a / b of non-negative numbers, in 32 bits where both fit
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The codec's signs of the head's columns, a bit per column (1 = negative).
+struct SignWords {
+    uint32_t w[8];
+};
+constexpr SignWords sign_words() {
+    SignWords s = {};
+    for (uint32_t k = 0; k < 256; ++k) {
+        uint32_t h = k * 0x9E3779B9u;
+        h ^= h >> 16;
+        h *= 0x85EBCA6Bu;
+        h ^= h >> 13;
+        s.w[k / 32] |= (h >> 31) << (k % 32);
+    }
+    return s;
+}
+static __constant__ SignWords c_sign_words = sign_words();
+
+// The same for pairs of 16-bit values: word b has the signs of block b's even
+// columns in its low half and of the odd ones in its high half, so that one
+// shift brings column pair i to bits 15 and 31.
+constexpr SignWords sign_pairs() {
+    const SignWords s = sign_words();
+    SignWords p = {};
+    for (int b = 0; b < 8; ++b)
+        for (int i = 0; i < 16; ++i)
+            p.w[b] |= ((s.w[b] >> (2 * i)) & 1u) << i | ((s.w[b] >> (2 * i + 1)) & 1u) << (16 + i);
+    return p;
+}
+static __constant__ SignWords c_sign_pairs = sign_pairs();
 
 // Code of one rotated value y against the ascending thresholds t of its half,
 // added into `word` at nibble position `sh`: bit 3 = [y < 0], bits 0..2 =

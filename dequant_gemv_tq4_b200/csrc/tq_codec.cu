@@ -12,7 +12,6 @@
 // Pre-rotation: one warp owns one 128-column superblock of one row per step;
 // lane = 8*j + p holds elements 4p..4p+3 of block j; two butterfly stages in
 // registers (h = 1, 2), three across lanes (h = 4, 8, 16 via shfl_xor).
-#include "tq_block.cuh"
 #include "tq_device.cuh"
 #include "tq_internal.h"
 
@@ -30,6 +29,23 @@ __constant__ uint32_t c_mag_bits[8] = TQ_MAG_F32_INIT;
 // sb in the tile-major layout [tile][sb][16 rows].
 __device__ __forceinline__ size_t unit_row(int row, int sb, int nsb) {
     return ((size_t)(row >> 4) * nsb + sb) * 16 + (row & 15);
+}
+
+// Code of one rotated value y against the ascending thresholds t of its half,
+// added into `word` at nibble position `sh`: bit 3 = [y < 0], bits 0..2 =
+// #{j : |y| > t_j} by a three-compare binary search.  Each bit is a
+// conditional add consumed right after its compare, so the compiler can
+// predicate the adds instead of materialising (or spilling) the predicates.
+__device__ __forceinline__ uint32_t add_code(uint32_t word, float y, const float (&t)[7], int sh) {
+    const float a = fabsf(y);
+    const bool b2 = a > t[3];
+    const bool b1 = a > (b2 ? t[5] : t[1]);
+    const bool b0 = a > (b1 ? (b2 ? t[6] : t[2]) : (b2 ? t[4] : t[0]));
+    if (b2) word += 4u << sh;
+    if (b1) word += 2u << sh;
+    if (b0) word += 1u << sh;
+    if (y < 0.0f) word += 8u << sh;
+    return word;
 }
 
 // -------------------------------------------------------------------------
@@ -50,6 +66,56 @@ __device__ __forceinline__ uint32_t block_sign_bits(uint32_t k0) {
 __device__ __forceinline__ void packed_sign_words(uint32_t bits, uint32_t (&ps)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) ps[i] = (((bits >> (2 * i)) & 1u) << 15) | (((bits >> (2 * i + 1)) & 1u) << 31);
+}
+
+// Packed fp32 pairs (sm_100 add/sub.rn.f32x2): each half is one IEEE fp32
+// operation rounded to nearest even, exactly the scalar __fadd_rn/__fsub_rn.
+// Their operands here are loads or scalar products, never a packed product
+// (a packed multiply feeding a packed add may be contracted into an FMA).
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The 32-point transform in the codec's stage order h = 1, 2, 4, 8, 16.
+// Element t and element t + 16 share one packed register: stages h < 16 pair
+// register t with register t + h (both halves at once), stage 16 combines
+// the two halves of each register in scalar.  Every element sees the same
+// operations on the same operands as the sequential definition.
+__device__ __forceinline__ void fwht32_regs(float (&v)[32]) {
+    uint64_t P[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) P[t] = pack2(v[t], v[t + 16]);
+#pragma unroll
+    for (int h = 1; h < 16; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if ((i & h) == 0) {
+                const uint64_t a = P[i], b = P[i + h];
+                P[i] = add2(a, b);
+                P[i + h] = sub2(a, b);
+            }
+#pragma unroll
+    for (int t = 0; t < 16; ++t) {
+        float lo, hi;
+        unpack2(P[t], lo, hi);
+        v[t] = __fadd_rn(lo, hi);
+        v[t + 16] = __fsub_rn(lo, hi);
+    }
 }
 
 // 32 input elements -> fp32 with the sign flip applied (exact).

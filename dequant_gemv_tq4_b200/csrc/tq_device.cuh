@@ -88,35 +88,6 @@ __device__ __forceinline__ void load4<kF16>(const void *p, float (&v)[4]) {
     v[0] = f0.x; v[1] = f0.y; v[2] = f1.x; v[3] = f1.y;
 }
 
-// An ordinary load.  A programmatic dependent that reads what the kernel before
-// it writes uses this after its wait: the read-only path (load4, __ldg) asks for
-// data that nobody writes while the kernel is resident.
-template <typename T>
-__device__ __forceinline__ T ld(const T *p) {
-    return *p;
-}
-
-// load4 by ordinary loads.
-template <int DT>
-__device__ __forceinline__ void load4_ordinary(const void *p, float (&v)[4]) {
-    if constexpr (DT == kF32) {
-        const float4 q = ld(reinterpret_cast<const float4 *>(p));
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-    } else {
-        const uint2 q = ld(reinterpret_cast<const uint2 *>(p));
-        if constexpr (DT == kBF16) {
-            v[0] = __uint_as_float(q.x << 16);
-            v[1] = __uint_as_float(q.x & 0xffff0000u);
-            v[2] = __uint_as_float(q.y << 16);
-            v[3] = __uint_as_float(q.y & 0xffff0000u);
-        } else {
-            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&q.x));
-            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&q.y));
-            v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-        }
-    }
-}
-
 // Stores of 4 consecutive fp32 values rounded (nearest-even) to the dtype.
 template <int DT>
 __device__ __forceinline__ void store4(void *p, const float (&v)[4]);
@@ -236,11 +207,6 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&o)[4]) {
     o[1] = prmt(lo03, hi03, 0x7362u);  // elements 2, 3
     o[2] = prmt(lo47, hi47, 0x5140u);  // elements 4, 5
     o[3] = prmt(lo47, hi47, 0x7362u);  // elements 6, 7
-}
-
-// a / b of non-negative numbers, in 32 bits where both fit
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // L2 prefetch hint for the line holding p (no data returned, no fault on a

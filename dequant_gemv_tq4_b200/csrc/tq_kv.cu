@@ -5,10 +5,8 @@
 // A cache record is one token's head vector in the codec of the weights: per
 // 32-element block the sign flip, the 32-point Walsh-Hadamard transform, two
 // fp16 half-block scales and sixteen nibble codes per half (include/tq.h).
-#include "tq_block.cuh"
-#include "tq_device.cuh"
+#include "tq_cache.cuh"
 #include "tq_internal.h"
-#include "tq_signs.cuh"
 
 namespace tq {
 

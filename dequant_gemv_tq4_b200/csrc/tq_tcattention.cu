@@ -18,7 +18,6 @@
 //                  the score's own columns
 // While one stream's softmax runs, the tensor cores work for the other.
 #include "tq_attention.cuh"
-#include "tq_block.cuh"
 
 namespace tq {
 
