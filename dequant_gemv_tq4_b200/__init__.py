@@ -643,24 +643,25 @@ def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, laye
 
 def _cache(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, layers: bool = False) -> KvCache:
     """The C description of one layer's cache (of layer 0, with ``layers``)."""
-    shape = codes.shape[1:] if layers else codes.shape
-    if len(shape) != 5 or shape[1] != 2 or codes.dtype is not torch.uint8:
+    shape, device = codes.shape, codes.device
+    if len(shape) != 5 + layers or shape[-4] != 2 or codes.dtype is not torch.uint8:
         _bad("codes", codes, "uint8 [pages, 2, kv_heads, page_size, head_dim / 2]")
-    pages, _, kv_heads, page_size, half = shape
-    device = codes.device
-    if scales.dtype is not torch.int16 or scales.shape != (*codes.shape[:-1], half // 8) or scales.device != device:
+    half = shape[-1]
+    if scales.dtype is not torch.int16 or scales.shape != (*shape[:-1], half // 8) or scales.device != device:
         _bad("scales", scales, f"int16 [pages, 2, kv_heads, page_size, head_dim / 16] on {device}")
-    for name, t in (("codes", codes), ("scales", scales)):
-        if not (t[0] if layers and t.shape[0] else t).is_contiguous():
-            _bad(name, t, "a contiguous tensor")
+    one_layer = layers and shape[0]
+    if not (codes[0] if one_layer else codes).is_contiguous():
+        _bad("codes", codes, "a contiguous tensor")
+    if not (scales[0] if one_layer else scales).is_contiguous():
+        _bad("scales", scales, "a contiguous tensor")
     if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.device != device:
         _bad("page_table", page_table, f"int32 [batch, pages of a sequence] on {device}")
     batch, per_seq = page_table.shape
     ld, one = page_table.stride()
     if one != 1 and per_seq > 1:
         _bad("page_table", page_table, "unit stride in the last dimension")
-    return KvCache(codes.data_ptr(), scales.data_ptr(), pages, page_table.data_ptr(), batch, per_seq,
-                   ld if batch > 1 else per_seq, kv_heads, 2 * half, page_size)
+    return KvCache(codes.data_ptr(), scales.data_ptr(), shape[-5], page_table.data_ptr(), batch, per_seq,
+                   ld if batch > 1 else per_seq, shape[-3], 2 * half, shape[-2])
 
 
 def _rope_desc(inv_freq: torch.Tensor, device, interleaved=False, scale=1.0, inverse=False) -> RopeDesc:
@@ -715,7 +716,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, inter
         with torch.cuda.device(dev):
             return rope(x, positions, inv_freq, interleaved, scale, inverse, out, stream)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.dtype is not x.dtype:
         _bad("out", out, f"{x.dtype}")
     shape = x.shape
@@ -766,7 +767,7 @@ def kv_read(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
     n = seqs.numel()
     shape = (n, cache.kv_heads, cache.head_dim)
     if k is None and v is None:
-        k, v = torch.empty((2, *shape), dtype=dtype, device=dev)
+        k, v = scales.new_empty((2, *shape), dtype=dtype).unbind(0)
     elif k is None:
         k = torch.empty(shape, dtype=v.dtype, device=dev)
     elif v is None:
@@ -807,13 +808,13 @@ def kv_attention(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Te
     batch, tree, heads, dim = q.shape
     shape = (cache.batch, tree, heads, cache.head_dim)
     if out is None:
-        out = torch.empty(q.shape, dtype=dtype or q.dtype, device=dev)
+        out = torch.empty_like(q, dtype=dtype, memory_format=torch.contiguous_format)
     qs, os_ = _heads(q, "q", dev, shape), _heads(out, "out", dev, shape)
     if ws is None:
         nbytes = tq_kv_attention_workspace_bytes(batch, tree, heads, cache.kv_heads, dim)
         if nbytes == 0:
             raise ValueError("kv_attention: invalid sizes (heads is a multiple of kv_heads, up to 64 drafted tokens)")
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = codes.new_empty((nbytes,))
     else:
         if ws.device != dev or not ws.is_contiguous():
             _bad("ws", ws, f"a contiguous tensor on {dev}")
