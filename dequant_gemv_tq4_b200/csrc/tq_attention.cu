@@ -37,6 +37,8 @@ constexpr int kGroup = 16;               // tokens of a group
 constexpr uint32_t kLutBase = 0x10000u;  // shared-memory address of the centroid table
 constexpr uint32_t kLutStep = 256;       // bytes between its rows (128 used)
 constexpr int kLeastGroups = 1;          // groups of a warp's range at least
+constexpr int kExtraGroups = 4;
+constexpr int kTcExtra = 4;
 constexpr int kTcLeastRows = 16;         // above: the tcgen05 kernel
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
@@ -421,8 +423,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
         const int64_t in_seq = at - (int64_t)sh.prefix[b] * per_seq;
         const int hr = uniform((int)quotient(in_seq, groups));
         const int head = hr / P.row_tiles, row0 = (hr % P.row_tiles) * NT * 8;
-        const int ga = uniform((int)(in_seq - (int64_t)hr * groups));
-        const int gb = uniform((int)min((int64_t)groups, ga + (end - at)));
+        const int va = uniform((int)(in_seq - (int64_t)hr * groups));
+        const int vb = uniform((int)min((int64_t)groups, va + (end - at)));
+        at += vb - va;
+        const int ga = max(va - P.extra, 0), gb = max(vb - P.extra, 0);
+        if (ga >= gb) continue;
         const int len = uniform(min(max(P.lens[b], 0), P.c.pages_per_seq << P.c.page_shift));
 
         // first loads before the query is rotated
@@ -575,7 +580,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
                 }
             }
         }
-        at += gb - ga;
     }
 }
 
@@ -608,8 +612,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
     const int workers = worker_count(P, W);
     const int hr = head * P.row_tiles + tile;
     const int64_t first = (int64_t)at * per_seq + (int64_t)hr * groups;
-    // the worker of group x: the largest i with i W / workers <= x
-    const int64_t i0 = quotient((first + 1) * workers - 1, W), i1 = quotient((first + groups) * workers - 1, W);
+    // the worker of group x: the largest i with i W / workers <= x; the unit's
+    // first group with tokens is `extra` on
+    const int64_t i0 = quotient((first + P.extra + 1) * workers - 1, W), i1 = quotient((first + groups) * workers - 1, W);
     const int64_t s0 = ((int64_t)b * per_seq + hr + i0) * P.parts;  // the unit's first slot
     const int n = (int)(i1 - i0 + 1) * P.parts, w = warp % RW;      // and how many
     const int D = P.c.head_dim;
@@ -725,7 +730,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams 
 struct AttnPlan {
     bool tc;  // the tcgen05 kernel
     int dp, nt, warps;
-    int rows, row_tiles, tile_rows, group, workers, least, parts;
+    int rows, row_tiles, tile_rows, group, workers, least, extra, parts;
     int64_t slots;
 };
 
@@ -739,6 +744,7 @@ AttnPlan plan_attention(int64_t batch, int tree, int heads, int kv_heads, int he
         p.group = 128;
         p.workers = sm_count;
         p.least = 1;
+        p.extra = kTcExtra;
     } else {
         // tiles of 8 rows, or 16 where a (sequence, head) has more than 8 rows
         // and the accumulators of 16 fit the registers (head dimension up to 128)
@@ -750,6 +756,7 @@ AttnPlan plan_attention(int64_t batch, int tree, int heads, int kv_heads, int he
         p.group = kGroup;
         p.workers = sm_count * p.warps;
         p.least = kLeastGroups;
+        p.extra = kExtraGroups;
     }
     p.row_tiles = (p.rows + p.tile_rows - 1) / p.tile_rows;
     p.slots = (batch * kv_heads * p.row_tiles + p.workers) * p.parts;
@@ -836,6 +843,7 @@ cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t s
     P.group = plan.group;
     P.workers = plan.workers;
     P.least = plan.least;
+    P.extra = plan.extra;
     P.parts = plan.parts;
     P.tile_rows = plan.tile_rows;
     P.header = reinterpret_cast<unsigned *>(j.workspace);

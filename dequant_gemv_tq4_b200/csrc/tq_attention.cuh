@@ -32,12 +32,13 @@ struct AttnParams {
     int group;       // tokens of a group: what ranges are counted in
     int workers;     // ranges at most
     int least;       // groups of a range at least
+    int extra;       // groups that beginning a unit counts for: its first `extra` hold no tokens
     int parts;       // partial results that a worker leaves of a unit
     int tile_rows;   // rows of a partial result
     unsigned *header;  // status word
     long long timeout_cycles;  // of a wait in the tcgen05 kernel
-    int inject_skip;           // test hook: its first CTA never hands over its first keys
-    int *prefix;     // [batch + 1] groups before each sequence
+    int inject_skip;           // test hook: the first tile's first keys are never handed over
+    int *prefix;     // [batch + 1] groups of a unit of each sequence before this one
     float *part_ml;  // [slots][tile_rows][2]: maximum, sum
     float *part_o;   // [slots][tile_rows][head_dim]
 };
@@ -143,7 +144,7 @@ __device__ __forceinline__ void scan_sequences(const AttnParams &P, int *prefix,
     const int per = (P.c.batch + threads - 1) / threads;
     int sum = 0;
     for (int i = tid * per; i < min(P.c.batch, (tid + 1) * per); ++i)
-        sum += (seq_tokens(P, P.lens[i]) + P.group - 1) / P.group;
+        sum += (seq_tokens(P, P.lens[i]) + P.group - 1) / P.group + P.extra;
     int inc = sum;
     const int lane = tid & 31;
 #pragma unroll
@@ -158,7 +159,7 @@ __device__ __forceinline__ void scan_sequences(const AttnParams &P, int *prefix,
     int at = base + inc - sum;
     for (int i = tid * per; i < min(P.c.batch, (tid + 1) * per); ++i) {
         prefix[i] = at;
-        at += (seq_tokens(P, P.lens[i]) + P.group - 1) / P.group;
+        at += (seq_tokens(P, P.lens[i]) + P.group - 1) / P.group + P.extra;
     }
     if (tid == threads - 1) prefix[P.c.batch] = base + inc;
     __syncthreads();

@@ -127,8 +127,8 @@ constexpr uint32_t kDebugUseMmaSync = 8u;
 // the later contributions itself instead of reading them (the path taken
 // when a contributor cannot run)
 constexpr uint32_t kDebugStealAll = 16u;
-// bit 5: the first CTA of the tcgen05 attention kernel never hands over its
-// first keys, so that its bounded waits expire and report a timeout
+// bit 5: the tcgen05 attention kernel never hands over its first tile's first
+// keys, so that its bounded waits expire and report a timeout
 constexpr uint32_t kDebugSkipCacheKeys = 32u;
 void set_debug_flags(uint32_t flags);
 uint32_t debug_flags();

@@ -201,27 +201,32 @@ struct Walk {  // the parts of a worker's range, the same for every warp
     int per_seq;
     int64_t at, end;
     __device__ __forceinline__ bool next(const AttnParams &P, Part &p) {
-        if (at >= end) return false;
-        int lo = 0, hi = P.c.batch - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if ((int64_t)prefix[mid] * per_seq <= at) lo = mid;
-            else hi = mid - 1;
+        while (at < end) {
+            int lo = 0, hi = P.c.batch - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if ((int64_t)prefix[mid] * per_seq <= at) lo = mid;
+                else hi = mid - 1;
+            }
+            const int groups = prefix[lo + 1] - prefix[lo];
+            const int64_t in_seq = at - (int64_t)prefix[lo] * per_seq;
+            const int hr = (int)quotient(in_seq, groups);
+            const int va = (int)(in_seq - (int64_t)hr * groups);
+            const int vb = (int)min((int64_t)groups, va + (end - at));
+            at += vb - va;
+            p.ta = max(va - P.extra, 0);
+            p.tb = max(vb - P.extra, 0);
+            if (p.ta >= p.tb) continue;
+            p.b = lo;
+            p.head = hr / P.row_tiles;
+            p.row0 = hr % P.row_tiles * P.tile_rows;
+            p.unit = (int64_t)lo * per_seq + hr;
+            const int len = P.lens[lo];
+            p.n = seq_tokens(P, len);
+            p.len = min(max(len, 0), P.c.pages_per_seq << P.c.page_shift);
+            return true;
         }
-        const int tiles = prefix[lo + 1] - prefix[lo];
-        const int64_t in_seq = at - (int64_t)prefix[lo] * per_seq;
-        const int hr = (int)quotient(in_seq, tiles);
-        p.b = lo;
-        p.head = hr / P.row_tiles;
-        p.row0 = hr % P.row_tiles * P.tile_rows;
-        p.ta = (int)(in_seq - (int64_t)hr * tiles);
-        p.tb = (int)min((int64_t)tiles, p.ta + (end - at));
-        p.unit = (int64_t)lo * per_seq + hr;
-        const int len = P.lens[lo];
-        p.n = seq_tokens(P, len);
-        p.len = min(max(len, 0), P.c.pages_per_seq << P.c.page_shift);
-        at += p.tb - p.ta;
-        return true;
+        return false;
     }
 };
 
@@ -653,7 +658,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                     a_proxy_fence();
                     __syncwarp();
                     // (never, where a test wants the waits for it to run out)
-                    if (lane == 0 && !(P.inject_skip && blockIdx.x == 0 && piece == 0))
+                    if (lane == 0 && !(P.inject_skip && p.unit == 0 && p.ta == 0 && piece == tile_no * kPieces))
                         a_arrive(bar((values ? kVFull : kKFull) + (int)st));
                     piece += kDecodeWarps;
                 }

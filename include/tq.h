@@ -316,8 +316,8 @@ TQ_API tq_status tq_workspace_status(void *workspace, int clear, void *stream);
  * the first CTA never issues its second activation-tile copy (nor counts its
  * bytes), its waits expire after ~5 ms, every tensor-memory column is still
  * released, and the status word is set.  Bit 5: the same for the tcgen05
- * attention kernel (tq_kv_attention): its first CTA never hands over its
- * first keys.
+ * attention kernel (tq_kv_attention): the first tile's first keys are never
+ * handed over.
  */
 TQ_API void tq_debug_set_flags(uint32_t flags);
 
