@@ -401,8 +401,6 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
     const int per_seq = P.c.kv_heads * P.row_tiles;
     const int64_t W = (int64_t)sh.prefix[P.c.batch] * per_seq;
     if (blockIdx.x == 0 && tid == 0) P.header[0] = 0u;  // no wait here that could run out
-    if (blockIdx.x == 0)
-        for (int i = tid; i <= P.c.batch; i += WARPS * 32) P.prefix[i] = sh.prefix[i];
     // the first warps of all CTAs come first, so that a few ranges spread over the SMs
     const int workers = worker_count(P, W);
     const int me = warp * gridDim.x + blockIdx.x;
@@ -554,7 +552,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 
         // this part of the unit: maxima and sums, and DP / 8 neighbouring
         // elements of two rows for each lane
-        const int64_t slot = (int64_t)b * per_seq + hr + me;
+        const int64_t unit = (int64_t)b * per_seq + hr, slot = unit + me;
+        if (lane == 0 && ga == 0) P.span[2 * unit] = me;
+        if (lane == 0 && gb == groups - P.extra) P.span[2 * unit + 1] = me;
         uint64_t present = ~0ull;
         if (P.parents) present = TreeWords(P, tree, lane).present();
 #pragma unroll
@@ -585,144 +585,134 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 
 // ---------------------------------------------------------------------------
 // The parts of each row joined, rotated back, divided and rounded.  CTAs of
-// eight warps.  RW = 8: the warps share one row's parts, and the first adds up
-// and finishes.  RW = 1: a warp takes kJoinRows neighbouring rows, which have
-// the same parts, so that finding them and waiting for them is paid once.
+// eight warps; RW = 8: the warps share one row's parts, and the first adds up
+// and finishes.  RW = 1: a warp takes a row.  What bounds this launch is its
+// chain of dependent loads (span, then maxima, sums and the first values), so
+// the attention kernel leaves each unit's span of slots ready to be read.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 4;
 
 template <int OT, int RW>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P) {
-    constexpr int R = RW == 1 ? kJoinRows : 1;
     __shared__ float so[RW == 1 ? 1 : kJoinWarps][256];
     __shared__ float sl[kJoinWarps], sm[kJoinWarps];
-    grid_dependency_wait();
-    grid_dependents_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int quads = (P.rows + R - 1) / R;  // (a tile's rows are a multiple of R)
     const int index = (int)blockIdx.x * (kJoinWarps / RW) + warp / RW;
-    if (index >= P.c.batch * P.c.kv_heads * quads) return;  // (whole CTAs where RW > 1)
-    const int bh = index / quads, row = index % quads * R;
+    const int bh = index / P.rows, row = index % P.rows;
     const int b = bh / P.c.kv_heads, head = bh % P.c.kv_heads;
     const int tile = row / P.tile_rows, r = row % P.tile_rows;
-    const int per_seq = P.c.kv_heads * P.row_tiles;
-    const int at = P.prefix[b], groups = P.prefix[b + 1] - at;
-    const int64_t W = (int64_t)P.prefix[P.c.batch] * per_seq;
-    const int workers = worker_count(P, W);
-    const int hr = head * P.row_tiles + tile;
-    const int64_t first = (int64_t)at * per_seq + (int64_t)hr * groups;
-    // the worker of group x: the largest i with i W / workers <= x; the unit's
-    // first group with tokens is `extra` on
-    const int64_t i0 = quotient((first + P.extra + 1) * workers - 1, W), i1 = quotient((first + groups) * workers - 1, W);
-    const int64_t s0 = ((int64_t)b * per_seq + hr + i0) * P.parts;  // the unit's first slot
-    const int n = (int)(i1 - i0 + 1) * P.parts, w = warp % RW;      // and how many
+    const int t = row / P.group_heads, h = head * P.group_heads + row % P.group_heads;
     const int D = P.c.head_dim;
+    uint32_t flips[2];
+#pragma unroll
+    for (int sb = 0; sb < 2; ++sb) flips[sb] = c_sign_words.w[sb * 4 + lane / 8] >> (4 * (lane & 7));
+    grid_dependency_wait();
+    grid_dependents_launch();
+    if (index >= P.c.batch * P.c.kv_heads * P.rows) return;  // (whole CTAs where RW > 1)
+    const int64_t unit = (int64_t)bh * P.row_tiles + tile;
+    // its workers; a call that gave up left some of these unwritten, so they are bounded
+    const int2 span = *reinterpret_cast<const int2 *>(P.span + 2 * unit);
+    const int first = min(max(span.x, 0), P.workers - 1);
+    const int last = min(max(span.y, first), P.workers - 1);
+    const int64_t s0 = (unit + first) * P.parts;                // the unit's first slot
+    const int n = (last - first + 1) * P.parts, w = warp % RW;  // and how many
 
-    float acc[R][2][4], m[R], l[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-        m[k] = kNoMax;
-        l[k] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[k][0][i] = acc[k][1][i] = 0.f;
-    }
+    float acc[2][4] = {}, m = kNoMax, l = 0.f;
+    // parts whose values are on their way: many in a launch of few rows; of many
+    // rows, as many as leave the registers for other warps (4 instead of 2: 193
+    // against 174 us for 131072 rows; 4 instead of 8: 17.7 against 16.2 us for 32)
+    constexpr int kAhead = RW == 1 ? 2 : 8;
     // this warp's share of the parts, up to 32 at a time: a lane takes one
-    // part's maxima and sums, then all lanes its values
+    // part's maximum and sum, then all lanes its values
     const int share = n * (w + 1) / RW;
     for (int c = n * w / RW; c < share; c += 32) {
-        float f[R];
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            float2 p = make_float2(kNoMax, 0.f);
-            if (c + lane < share && row + k < P.rows)
-                p = reinterpret_cast<const float2 *>(P.part_ml)[(s0 + c + lane) * P.tile_rows + r + k];
-            float mx = fmaxf(m[k], p.y > 0.f ? p.x : kNoMax);
-#pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
-            f[k] = p.y > 0.f ? ex2((p.x - mx) * P.scale_log2) : 0.f;
-            float sum = f[k] * p.y;
-#pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
-            const float old = ex2((m[k] - mx) * P.scale_log2);
-            l[k] = l[k] * old + sum;
-            m[k] = mx;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[k][0][i] *= old;
-                acc[k][1][i] *= old;
-            }
-        }
+        float2 p = make_float2(kNoMax, 0.f);
+        if (c + lane < share) p = reinterpret_cast<const float2 *>(P.part_ml)[(s0 + c + lane) * P.tile_rows + r];
         const int count = min(32, share - c);
         const float *src = P.part_o + ((s0 + c) * P.tile_rows + r) * D + 4 * lane;
-#pragma unroll 4
-        for (int j = 0; j < count; ++j) {
+        float4 v[kAhead][2];
+        auto values = [&](int j, float4 (&o)[2]) {
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
+            for (int sb = 0; sb < 2; ++sb) {
+                o[sb] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j < count && sb * 128 + 4 * lane < D)
+                    o[sb] = *reinterpret_cast<const float4 *>(src + (int64_t)j * P.tile_rows * D + sb * 128);
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) values(j, v[j]);
+        float mx = fmaxf(m, p.y > 0.f ? p.x : kNoMax);
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
+        const float f = p.y > 0.f ? ex2((p.x - mx) * P.scale_log2) : 0.f;
+        float sum = f * p.y;
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
+        const float old = ex2((m - mx) * P.scale_log2);
+        l = l * old + sum;
+        m = mx;
+#pragma unroll
+        for (int sb = 0; sb < 2; ++sb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[sb][i] *= old;
+        for (int j = 0; j < count; j += kAhead) {
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const float fj = j + q < count ? __shfl_sync(kFull, f, j + q) : 0.f;
                 // (a part without a token may never have been written: its values do not count)
-                const float fk = __shfl_sync(kFull, f[k], j);
+                if (fj != 0.f) {
 #pragma unroll
-                for (int sb = 0; sb < 2; ++sb) {
-                    if (sb * 128 + 4 * lane < D && fk != 0.f) {
-                        const float4 o = *reinterpret_cast<const float4 *>(src + (size_t)k * D + sb * 128);
-                        acc[k][sb][0] += fk * o.x;
-                        acc[k][sb][1] += fk * o.y;
-                        acc[k][sb][2] += fk * o.z;
-                        acc[k][sb][3] += fk * o.w;
+                    for (int sb = 0; sb < 2; ++sb) {
+                        acc[sb][0] += fj * v[q][sb].x;
+                        acc[sb][1] += fj * v[q][sb].y;
+                        acc[sb][2] += fj * v[q][sb].z;
+                        acc[sb][3] += fj * v[q][sb].w;
                     }
                 }
+                values(j + kAhead + q, v[q]);
             }
-            src += (size_t)P.tile_rows * D;
         }
     }
     if (RW > 1) {
 #pragma unroll
         for (int sb = 0; sb < 2; ++sb)
             *reinterpret_cast<float4 *>(&so[warp][sb * 128 + 4 * lane]) =
-                make_float4(acc[0][sb][0], acc[0][sb][1], acc[0][sb][2], acc[0][sb][3]);
+                make_float4(acc[sb][0], acc[sb][1], acc[sb][2], acc[sb][3]);
         if (lane == 0) {
-            sl[warp] = l[0];
-            sm[warp] = m[0];
+            sl[warp] = l;
+            sm[warp] = m;
         }
         __syncthreads();
         if (warp != 0) return;
         float mx = kNoMax;
 #pragma unroll
         for (int x = 0; x < RW; ++x) mx = fmaxf(mx, sm[x]);
-        l[0] = 0.f;
+        l = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[0][0][i] = acc[0][1][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.f;
 #pragma unroll
         for (int x = 0; x < RW; ++x) {
             const float f = ex2((sm[x] - mx) * P.scale_log2);
-            l[0] += f * sl[x];
+            l += f * sl[x];
 #pragma unroll
             for (int sb = 0; sb < 2; ++sb)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[0][sb][i] += f * so[x][sb * 128 + 4 * lane + i];
+                for (int i = 0; i < 4; ++i) acc[sb][i] += f * so[x][sb * 128 + 4 * lane + i];
         }
     }
-    uint32_t flips[2];
+    const float inv = l > 0.f ? 0.03125f / l : 0.f;
+    char *out = P.out + (b * P.o_batch + t * P.o_token + h * P.o_head) * ElemSize<OT>::value;
 #pragma unroll
-    for (int sb = 0; sb < 2; ++sb) flips[sb] = c_sign_words.w[sb * 4 + lane / 8] >> (4 * (lane & 7));
+    for (int sb = 0; sb < 2; ++sb) {
+        if (sb * 128 >= D) break;
+        const int e = sb * 128 + 4 * lane;
+        float v[4];
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        if (row + k >= P.rows) break;
-        const int t = (row + k) / P.group_heads, h = head * P.group_heads + (row + k) % P.group_heads;
-        const float inv = l[k] > 0.f ? 0.03125f / l[k] : 0.f;
-        char *out = P.out + (b * P.o_batch + t * P.o_token + h * P.o_head) * ElemSize<OT>::value;
+        for (int i = 0; i < 4; ++i) v[i] = acc[sb][i] * inv;
+        fwht32_warp(v, lane & 7);
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb) {
-            if (sb * 128 >= D) break;
-            const int e = sb * 128 + 4 * lane;
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = acc[k][sb][i] * inv;
-            fwht32_warp(v, lane & 7);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = flip(v[i], (flips[sb] << (31 - i)) & 0x80000000u);
-            if (e < D) store4<OT>(out + (int64_t)e * ElemSize<OT>::value, v);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = flip(v[i], (flips[sb] << (31 - i)) & 0x80000000u);
+        if (e < D) store4<OT>(out + (int64_t)e * ElemSize<OT>::value, v);
     }
 }
 
@@ -786,20 +776,24 @@ cudaError_t launch_attend(const AttnParams &P, cudaStream_t stream) {
 
 template <int OT, int RW>
 cudaError_t launch_join_as(const AttnParams &P, cudaStream_t stream) {
-    constexpr int R = RW == 1 ? kJoinRows : 1;
-    const int64_t items = (int64_t)P.c.batch * P.c.kv_heads * ((P.rows + R - 1) / R);
-    return launch_dependent(join_kernel<OT, RW>, (unsigned)((items * RW + kJoinWarps - 1) / kJoinWarps),
-                            kJoinWarps * 32, 0, stream, P);
+    const int64_t warps = (int64_t)P.c.batch * P.c.kv_heads * P.rows * RW;
+    return launch_dependent(join_kernel<OT, RW>, (unsigned)((warps + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0,
+                            stream, P);
 }
 
-// A warp takes four rows where that gives at least eight warps an SM and the
-// parts are few (about workers / units + 1 of them); else eight warps share a row.
+// Eight warps share a row where rows are few and their parts (about workers /
+// units + 1) many; else a warp takes a row.  Whole call, eight warps against
+// one: 32 rows of up to 297 parts 16 and 82 us; 256 rows of 38 parts 30 and 40;
+// 1024 rows of 10 parts 23 and 19; 2048 rows of 19 parts 33 and 28.
+constexpr int64_t kManyParts = 16;
+constexpr int64_t kFewRows = 148 * 8;
+
 template <int OT>
 cudaError_t launch_join_by(const AttnParams &P, cudaStream_t stream) {
     const int64_t pairs = (int64_t)P.c.batch * P.c.kv_heads;
-    const bool few = (int64_t)P.workers * P.parts <= 6 * pairs * P.row_tiles;
-    return few && pairs * ((P.rows + kJoinRows - 1) / kJoinRows) >= 148 * 8 ? launch_join_as<OT, 1>(P, stream)
-                                                                           : launch_join_as<OT, 8>(P, stream);
+    const int64_t parts = (int64_t)P.workers * P.parts / (pairs * P.row_tiles) + 1;
+    return parts > kManyParts && pairs * P.rows <= kFewRows ? launch_join_as<OT, 8>(P, stream)
+                                                            : launch_join_as<OT, 1>(P, stream);
 }
 
 }  // namespace
@@ -809,11 +803,11 @@ cudaError_t launch_join(const AttnParams &P, int odtype, cudaStream_t stream) {
     return odtype == kBF16 ? launch_join_by<kBF16>(P, stream) : launch_join_by<kF16>(P, stream);
 }
 
-// Workspace: a 256-byte header (status word), the prefix sums, the parts'
+// Workspace: a 256-byte header (status word), the units' spans, the parts'
 // maxima and sums, their values.
 size_t attention_workspace_bytes(int64_t batch, int tree, int heads, int kv_heads, int head_dim, int sm_count) {
     const AttnPlan p = plan_attention(batch, tree, heads, kv_heads, head_dim, sm_count);
-    return 256 + round_up((size_t)(batch + 1) * 4, 256) + round_up((size_t)p.slots * p.tile_rows * 8, 256) +
+    return 256 + round_up((size_t)batch * kv_heads * p.row_tiles * 8, 256) + round_up((size_t)p.slots * p.tile_rows * 8, 256) +
            (size_t)p.slots * p.tile_rows * head_dim * 4;
 }
 
@@ -850,8 +844,8 @@ cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t s
     P.inject_skip = (debug_flags() & kDebugSkipCacheKeys) ? 1 : 0;
     P.timeout_cycles = P.inject_skip ? 10000000ll : 2000000000ll;  // about 5 ms, a second
     char *ws = j.workspace + 256;
-    P.prefix = reinterpret_cast<int *>(ws);
-    ws += round_up((size_t)(j.c.batch + 1) * 4, 256);
+    P.span = reinterpret_cast<int *>(ws);
+    ws += round_up((size_t)j.c.batch * j.c.kv_heads * plan.row_tiles * 8, 256);
     P.part_ml = reinterpret_cast<float *>(ws);
     ws += round_up((size_t)plan.slots * plan.tile_rows * 8, 256);
     P.part_o = reinterpret_cast<float *>(ws);

@@ -38,7 +38,7 @@ struct AttnParams {
     unsigned *header;  // status word
     long long timeout_cycles;  // of a wait in the tcgen05 kernel
     int inject_skip;           // test hook: the first tile's first keys are never handed over
-    int *prefix;     // [batch + 1] groups of a unit of each sequence before this one
+    int *span;       // [units][2] first and last worker that leaves a part of the unit
     float *part_ml;  // [slots][tile_rows][2]: maximum, sum
     float *part_o;   // [slots][tile_rows][head_dim]
 };

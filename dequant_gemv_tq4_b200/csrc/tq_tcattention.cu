@@ -192,6 +192,7 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t half, int r, int chunk) {
 // A worker's part of a unit: tiles [ta, tb) of a (sequence, head, row tile).
 struct Part {
     int b, head, row0, len, n, ta, tb;
+    bool last;  // the unit ends with it
     int64_t unit;
 };
 
@@ -217,6 +218,7 @@ struct Walk {  // the parts of a worker's range, the same for every warp
             p.ta = max(va - P.extra, 0);
             p.tb = max(vb - P.extra, 0);
             if (p.ta >= p.tb) continue;
+            p.last = vb == groups;
             p.b = lo;
             p.head = hr / P.row_tiles;
             p.row0 = hr % P.row_tiles * P.tile_rows;
@@ -498,8 +500,6 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
     walk.prefix = prefix;
     walk.per_seq = P.c.kv_heads * P.row_tiles;
     const int64_t W = (int64_t)prefix[P.c.batch] * walk.per_seq;
-    if (blockIdx.x == 0)
-        for (int i = tid; i <= P.c.batch; i += kTcaThreads) P.prefix[i] = prefix[i];
     const int workers = worker_count(P, W);
     const int me = blockIdx.x;
     walk.at = me < workers ? quotient(W * me, workers) : 0;
@@ -577,6 +577,8 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
             ++parts_done;
             if (ok) {
                 a_fence_after();
+                if (tid == 0 && p.ta == 0) P.span[2 * p.unit] = me;
+                if (tid == 0 && p.last) P.span[2 * p.unit + 1] = me;
                 const int64_t slot = (p.unit + me) * P.parts + (pair ? 0 : s);
                 const int64_t row0 = slot * P.tile_rows + out_row - lane;  // of this warp
                 // a token that is not there answers zero
