@@ -8,6 +8,8 @@
 #include "tq_cache.cuh"
 #include "tq_internal.h"
 
+#include <algorithm>
+
 namespace tq {
 
 namespace {
@@ -58,9 +60,12 @@ struct RopeParams {
 };
 
 // Heads whose loads go out together: the output may be the input, so the
-// compiler cannot move a head's loads before another's stores by itself.
+// compiler cannot move a head's loads before another's stores by itself.  With
+// eight pairs in a lane a second head costs more warps than it hides waits:
+// 32768 tokens x 32 heads x 128 in bf16, one head 90 us and two 111 us; with
+// four pairs (fp32), one head 98 us and four 89 us at 16384 tokens.
 template <int V>
-constexpr int kRopeAtOnce = V == 8 ? 2 : 4;
+constexpr int kRopeAtOnce = V == 8 ? 1 : 4;
 
 // V elements at p: one 16-byte access or a scalar one.
 template <int DT, int V>
@@ -675,18 +680,28 @@ __global__ void __launch_bounds__(kKvThreads) kv_commit_kernel(const CommitParam
     }
 }
 
-// Heads per work item: as many as share work (angles, indices) while the
-// launch still has `enough` threads to fill the GPU's 148 SMs; short inputs
-// take one head per item.
-int heads_per_item(int64_t threads_per_head, int heads, int64_t enough) {
-    int h = heads;
-    while (h > 1 && threads_per_head * ((heads + h - 1) / h) < enough) h = (h + 1) / 2;
+// Heads per work item, which share its angles and indices: up to eight while
+// the launch still has kEnoughThreads (three or four warps for each of the
+// GPU's 592 schedulers); short inputs take one head per item.  Rotary positions
+// of 32 heads x 128 in bf16: 512 tokens 4.1 us, 5.3 us where 2^18 threads are
+// enough; 2048 tokens 7.6 and 8.7; at most 4, 8 and all heads, 8192 tokens
+// 26.9, 28.2 and 36.1 us; 32768 tokens 91.5, 89.7 and 98.7; of 8191 tokens in
+// fp32 with half of the elements rotated 50.4, 46.8 and 47.2.
+constexpr int64_t kEnoughThreads = 1 << 16;
+constexpr int kMostHeads = 8;
+
+int heads_per_item(int64_t threads_per_head, int heads) {
+    int h = std::min(heads, kMostHeads);
+    while (h > 1 && threads_per_head * ((heads + h - 1) / h) < kEnoughThreads) h = (h + 1) / 2;
     return h;
 }
 
-// Blocks from which on a lane takes a whole one (about three warps for each of
-// the GPU's 592 schedulers); below, eight lanes share a block and finish sooner.
-constexpr int64_t kManyBlocks = 1 << 16;
+// Blocks from which on a lane takes a whole one; below, eight lanes share a
+// block and finish sooner.  Append of bf16 with rotary positions, 8 heads x 128,
+// eight lanes against one: 2^14 blocks 4.6 and 6.5 us, 2^15 blocks 6.6 and 6.6,
+// 2^16 blocks 9.7 and 6.7, 2^20 blocks 85 and 50.  Read: 2^14 blocks 3.3 and
+// 3.1, 2^15 blocks 4.5 and 3.1, 2^20 blocks 49 and 27.
+constexpr int64_t kManyBlocks = 1 << 15;
 
 unsigned blocks_of(int64_t threads) { return (unsigned)((threads + kKvThreads - 1) / kKvThreads); }
 
@@ -719,7 +734,7 @@ cudaError_t launch_rope(const RopeJob &j, cudaStream_t stream) {
     P.rot_slots = j.rot / 2 / V;
     P.slots = P.rot_slots + (P.copy_tail ? (j.dim - j.rot) / V : 0);
     if (P.slots == 0) return cudaSuccess;
-    P.hchunk = heads_per_item(j.tokens * P.slots, j.heads, (int64_t)1 << 18);
+    P.hchunk = heads_per_item(j.tokens * P.slots, j.heads);
     P.chunks = (j.heads + P.hchunk - 1) / P.hchunk;
     P.items = j.tokens * P.chunks * P.slots;
     const unsigned grid = blocks_of(P.items);
@@ -766,7 +781,7 @@ cudaError_t launch_kv_append(const KvAppendJob &j, cudaStream_t stream) {
             return launch_dependent(kv_append_block_kernel<kBF16>, grid, kKvThreads, 0, stream, P, (int)per);
         return launch_dependent(kv_append_block_kernel<kF16>, grid, kKvThreads, 0, stream, P, (int)per);
     }
-    P.hchunk = heads_per_item(j.tokens * 2 * P.blocks * 8, j.c.kv_heads, (int64_t)1 << 18);
+    P.hchunk = heads_per_item(j.tokens * 2 * P.blocks * 8, j.c.kv_heads);
     P.chunks = (j.c.kv_heads + P.hchunk - 1) / P.hchunk;
     P.items = j.tokens * 2 * P.chunks * P.blocks;
     const unsigned grid = blocks_of(P.items * 8);
@@ -795,7 +810,7 @@ cudaError_t launch_kv_read(const KvReadJob &j, cudaStream_t stream) {
         if (j.dtype == kBF16) return launch_dependent(kv_read_block_kernel<kBF16>, grid, kKvThreads, 0, stream, P);
         return launch_dependent(kv_read_block_kernel<kF16>, grid, kKvThreads, 0, stream, P);
     }
-    P.hchunk = heads_per_item(j.tokens * 2 * P.blocks * 8, j.c.kv_heads, (int64_t)1 << 18);
+    P.hchunk = heads_per_item(j.tokens * 2 * P.blocks * 8, j.c.kv_heads);
     P.chunks = (j.c.kv_heads + P.hchunk - 1) / P.hchunk;
     P.items = j.tokens * 2 * P.chunks * P.blocks;
     const unsigned grid = blocks_of(P.items * 8);
