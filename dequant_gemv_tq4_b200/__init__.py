@@ -616,15 +616,21 @@ def _heads(t: torch.Tensor, name: str, device, shape):
     return st
 
 
-def _off_device(device) -> bool:
-    """Whether a device is not the current one (the library launches on the current one)."""
+def _elsewhere(device, stream):
+    """The context that a call has to run in, None if that is the current one:
+    the library launches on the current device, and memory that a call allocates
+    belongs to the stream that the call runs on."""
     if device.type != "cuda":
         raise ValueError("expected CUDA tensors")
-    return device.index != torch.cuda.current_device()
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
+        return torch.cuda.stream(stream)
+    return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
-def _raw_stream(stream, device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, layers: int | None = None, device=None):
@@ -712,9 +718,10 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, inter
     if x.dim() != 3:
         _bad("x", x, "[tokens, heads, dim]")
     dev = x.device
-    if _off_device(dev):
-        with torch.cuda.device(dev):
-            return rope(x, positions, inv_freq, interleaved, scale, inverse, out, stream)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return rope(x, positions, inv_freq, interleaved, scale, inverse, out)
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     elif out.dtype is not x.dtype:
@@ -723,7 +730,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, inter
     xs, os_ = _heads(x, "x", dev, shape), _heads(out, "out", dev, shape)
     st = tq_rope(x.data_ptr(), out.data_ptr(), _dt(x.dtype), shape[0], shape[1], shape[2], xs[0], xs[1], os_[0],
                  os_[1], _ints(positions, "positions", dev, shape[:1]),
-                 _rope_desc(inv_freq, dev, interleaved, scale, inverse), _raw_stream(stream, dev))
+                 _rope_desc(inv_freq, dev, interleaved, scale, inverse), _raw_stream(dev))
     if st:
         _check(st, "tq_rope")
     return out
@@ -736,9 +743,10 @@ def kv_append(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tenso
     goes to place places[i] of sequence seqs[i].  ``rope`` = (positions,
     inv_freq) rotates the keys on their way in."""
     dev = codes.device
-    if _off_device(dev):
-        with torch.cuda.device(dev):
-            return kv_append(codes, scales, page_table, seqs, places, k, v, rope, interleaved, rope_scale, stream)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return kv_append(codes, scales, page_table, seqs, places, k, v, rope, interleaved, rope_scale)
     cache = _cache(codes, scales, page_table)
     one = seqs.shape
     n = seqs.numel()
@@ -750,7 +758,7 @@ def kv_append(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tenso
     if rope is not None:
         pos, desc = _ints(rope[0], "positions", dev, (n,)), _rope_desc(rope[1], dev, interleaved, rope_scale)
     st = tq_kv_append(cache, _ints(seqs, "seqs", dev, (n,)), _ints(places, "places", dev, one), n, k.data_ptr(), ks[0],
-                      ks[1], v.data_ptr(), vs[0], vs[1], _dt(k.dtype), pos, desc, _raw_stream(stream, dev))
+                      ks[1], v.data_ptr(), vs[0], vs[1], _dt(k.dtype), pos, desc, _raw_stream(dev))
     if st:
         _check(st, "tq_kv_append")
 
@@ -760,9 +768,10 @@ def kv_read(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
             v: torch.Tensor | None = None, stream=None):
     """(keys, values) [n, kv_heads, head_dim] of the tokens at places[i] of seqs[i]."""
     dev = codes.device
-    if _off_device(dev):
-        with torch.cuda.device(dev):
-            return kv_read(codes, scales, page_table, seqs, places, dtype, k, v, stream)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return kv_read(codes, scales, page_table, seqs, places, dtype, k, v)
     cache = _cache(codes, scales, page_table)
     n = seqs.numel()
     shape = (n, cache.kv_heads, cache.head_dim)
@@ -776,7 +785,7 @@ def kv_read(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
         _bad("v", v, f"{k.dtype}")
     ks, vs = _heads(k, "k", dev, shape), _heads(v, "v", dev, shape)
     st = tq_kv_read(cache, _ints(seqs, "seqs", dev, (n,)), _ints(places, "places", dev, (n,)), n, k.data_ptr(), ks[0],
-                    ks[1], v.data_ptr(), vs[0], vs[1], _dt(k.dtype), _raw_stream(stream, dev))
+                    ks[1], v.data_ptr(), vs[0], vs[1], _dt(k.dtype), _raw_stream(dev))
     if st:
         _check(st, "tq_kv_read")
     return k, v
@@ -799,9 +808,10 @@ def kv_attention(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Te
     place lens[b] + i) and that token's ancestors by ``parents`` [batch, tree]
     (None: a chain).  ``scale`` defaults to head_dim^-0.5, ``dtype`` to q's."""
     dev = codes.device
-    if _off_device(dev):
-        with torch.cuda.device(dev):
-            return kv_attention(codes, scales, page_table, lens, q, parents, scale, dtype, out, ws, stream)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return kv_attention(codes, scales, page_table, lens, q, parents, scale, dtype, out, ws)
     cache = _cache(codes, scales, page_table)
     if q.dim() != 4:
         _bad("q", q, "[batch, tree, heads, head_dim]")
@@ -822,7 +832,7 @@ def kv_attention(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Te
     par = None if parents is None else _ints(parents, "parents", dev, (batch, tree))
     st = tq_kv_attention(cache, _ints(lens, "lens", dev, (batch,)), par, tree, q.data_ptr(), _dt(q.dtype), qs[0],
                          qs[1], qs[2], out.data_ptr(), _dt(out.dtype), os_[0], os_[1], os_[2], tree, heads,
-                         dim ** -0.5 if scale is None else scale, ws.data_ptr(), nbytes, _raw_stream(stream, dev))
+                         dim ** -0.5 if scale is None else scale, ws.data_ptr(), nbytes, _raw_stream(dev))
     if st:
         _check(st, "tq_kv_attention")
     return out
@@ -835,14 +845,15 @@ def kv_commit(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tenso
     first entry that does not increase (-1).  codes and scales of one layer, or
     with a leading dimension of layers that share the page table."""
     dev = codes.device
-    if _off_device(dev):
-        with torch.cuda.device(dev):
-            return kv_commit(codes, scales, page_table, lens, path, stream)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return kv_commit(codes, scales, page_table, lens, path)
     layered = codes.dim() == 6
     cache = _cache(codes, scales, page_table, layered)
     layers, cs, ss = (codes.shape[0], codes.stride(0), scales.stride(0)) if layered else (1, 0, 0)
     batch, steps = cache.batch, path.shape[-1]
     st = tq_kv_commit(cache, layers, cs, ss, _ints(lens, "lens", dev, (batch,)),
-                      _ints(path, "path", dev, (batch, steps)), steps, steps, _raw_stream(stream, dev))
+                      _ints(path, "path", dev, (batch, steps)), steps, steps, _raw_stream(dev))
     if st:
         _check(st, "tq_kv_commit")

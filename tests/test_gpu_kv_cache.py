@@ -615,6 +615,29 @@ def test_attention_on_another_stream_and_in_graphs(cuda_lib):
             assert torch.equal(out, cuda_lib.kv_attention(codes, scales, table, lens, query, parents=par))
 
 
+def test_what_a_call_allocates_belongs_to_its_stream(cuda_lib):
+    # a call given a stream that is busy: memory that it allocated itself must not
+    # be handed to later work of the current stream while the call still waits
+    B, T, H, kv, D, page = 2, 3, 8, 2, 128, 16
+    codes, scales, table = _filled(cuda_lib, B, 20, kv, D, page, seed=52)
+    q, lens = _rand(1, B, T, H, D, dtype=BF16).to(DEV), _i32([300, 17])
+    want = cuda_lib.kv_attention(codes, scales, table, lens, q)
+    seqs, places = _i32([0, 1, 0]), _i32([5, 6, 299])
+    want_k, want_v = cuda_lib.kv_read(codes, scales, table, seqs, places)
+    nbytes = cuda_lib.tq_kv_attention_workspace_bytes(B, T, H, kv, D)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    got = cuda_lib.kv_attention(codes, scales, table, lens, q, stream=side)
+    got_k, got_v = cuda_lib.kv_read(codes, scales, table, seqs, places, stream=side)
+    for _ in range(4):
+        torch.zeros(nbytes, dtype=torch.uint8, device=DEV)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(got_k, want_k) and torch.equal(got_v, want_v)
+
+
 # ---------------------------------------------------------------------------
 # commit, and the whole step
 # ---------------------------------------------------------------------------
