@@ -88,6 +88,10 @@ tq_status tq_rope(const void *x, void *out, tq_dtype t, int64_t tokens, int64_t 
         return TQ_ERR_INVALID_ARG;
     if (!aligned(x, element_size(t)) || !aligned(out, element_size(t)) || !aligned(positions, 4))
         return TQ_ERR_ALIGNMENT;
+    // in place only element for element
+    if (x == out && ((tokens > 1 && x_token_stride != out_token_stride) ||
+                     (heads > 1 && x_head_stride != out_head_stride)))
+        return TQ_ERR_INVALID_ARG;
     tq::RopeJob j;
     j.x = x;
     j.out = out;
@@ -191,6 +195,12 @@ tq_status tq_kv_commit(const tq_kv_cache *cache, int64_t layers, int64_t code_la
     if (layers > TQ_KV_MAX_LAYERS || steps > TQ_KV_MAX_TREE) return TQ_ERR_SHAPE;
     if (layers > 1 && (code_layer_stride < 0 || scale_layer_stride < 0)) return TQ_ERR_INVALID_ARG;
     if (layers > 1 && (code_layer_stride % 16 != 0 || scale_layer_stride % 8 != 0)) return TQ_ERR_ALIGNMENT;
+    // layers that share records would be moved more than once
+    if (layers > 1 &&
+        ((size_t)code_layer_stride < tq_kv_codes_bytes(cache->pages, cache->kv_heads, cache->head_dim, cache->page_size) ||
+         2 * (size_t)scale_layer_stride <
+             tq_kv_scales_bytes(cache->pages, cache->kv_heads, cache->head_dim, cache->page_size)))
+        return TQ_ERR_INVALID_ARG;
     if (layers == 0 || steps == 0 || cache->batch == 0) return TQ_OK;
     if (!lens || !path) return TQ_ERR_INVALID_ARG;
     if (!aligned(lens, 4) || !aligned(path, 4)) return TQ_ERR_ALIGNMENT;

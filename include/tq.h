@@ -465,6 +465,8 @@ TQ_API tq_status tq_nvfp4_gemm_batch(const tq_nvfp4_gemm_desc *descs, int count,
  *    token whose column is past pages_per_seq, or whose page id is outside
  *    [0, pages), has no place: writes of it are dropped, reads give zeros, and
  *    attention leaves it out.
+ *    Sequences may share pages that are only read; a page that tq_kv_append or
+ *    tq_kv_commit writes stands once in the table.
  *  - Sizes: head_dim a multiple of 32 up to TQ_KV_MAX_HEAD_DIM; page_size a
  *    power of two from 16 to TQ_KV_MAX_PAGE; a sequence's table spans at most
  *    2^30 tokens, the whole table TQ_KV_MAX_CAPACITY.  Offsets into the pool
@@ -604,7 +606,7 @@ TQ_API tq_status tq_kv_attention(const tq_kv_cache *cache, const int32_t *lens, 
  * before it (-1 by custom).  Record lens[b] + path[b][i] moves to place
  * lens[b] + i, for keys and values of all heads and of `layers` layers whose
  * pools lie code_layer_stride / scale_layer_stride elements apart (multiples
- * of 16 bytes) and share the page table.  lens itself is the caller's to
+ * of 16 bytes, a pool or more) and share the page table.  lens itself is the caller's to
  * advance.  Records behind the branch keep what they hold.
  */
 TQ_API tq_status tq_kv_commit(const tq_kv_cache *cache, int64_t layers, int64_t code_layer_stride,

@@ -101,6 +101,9 @@ def test_rope_argument_errors(tq):
     assert rope(heads=1025) == SHAPE
     assert rope(x=FAKE + 1) == ALIGN
     assert rope(xt=-1) == INVALID
+    # in place with other strides: one element's result would be another's input
+    assert rope(xt=256) == INVALID
+    assert rope(oh=72) == INVALID
     assert rope(n=0) == OK
     assert rope(heads=0) == OK
 
@@ -145,6 +148,10 @@ def test_commit_argument_errors(tq):
     assert commit(cs=8) == ALIGN
     assert commit(ss=4) == ALIGN
     assert commit(cs=-16) == INVALID
+    # layers that overlap (a pool here is 8192 bytes of codes, 1024 scales)
+    assert commit(cs=0) == INVALID
+    assert commit(cs=8192 - 16) == INVALID
+    assert commit(ss=1024 - 8) == INVALID
     assert commit(lens=None) == INVALID
     assert commit(path=None) == INVALID
     assert commit(path=FAKE + 1) == ALIGN
