@@ -692,7 +692,11 @@ constexpr int kMostHeads = 8;
 
 int heads_per_item(int64_t threads_per_head, int heads) {
     int h = std::min(heads, kMostHeads);
-    while (h > 1 && threads_per_head * ((heads + h - 1) / h) < kEnoughThreads) h = (h + 1) / 2;
+    for (; h > 1; --h) {
+        const int64_t threads = threads_per_head * ((heads + h - 1) / h);
+        // in a launch of one wave the longest item decides: equal shares
+        if (threads >= (heads % h ? 4 * kEnoughThreads : kEnoughThreads)) break;
+    }
     return h;
 }
 
@@ -730,7 +734,7 @@ cudaError_t launch_rope(const RopeJob &j, cudaStream_t stream) {
     P.scale = j.scale;
     P.interleaved = j.interleaved;
     P.inverse = j.inverse;
-    P.copy_tail = j.out != j.x || j.x_token != j.o_token || j.x_head != j.o_head;
+    P.copy_tail = j.out != j.x;
     P.rot_slots = j.rot / 2 / V;
     P.slots = P.rot_slots + (P.copy_tail ? (j.dim - j.rot) / V : 0);
     if (P.slots == 0) return cudaSuccess;
