@@ -27,6 +27,16 @@
 // are scaled by 2^7.  The maximum they refer to is followed only when it grows
 // by more than 2^8 (rescaling the accumulators is the exception), so a weight
 // is at most 2^15, and weights down to 2^-31 of the largest survive.
+//
+// What bounds it: instruction issue and shared-memory lookups, not HBM.  Per
+// pair of elements of a group the lookup, its address and the scale are three
+// instructions whatever the rows, so up to 8 rows cost the same.  64 sequences,
+// 289,000 tokens together, 32 query over 8 key/value heads of 128: 96.5 us with
+// the joining launch, 3.8 TB/s of records (issue slots 62% used, the
+// shared-memory pipe 57%; 113 us before bases were computed once per warp).
+// One sequence of 1000 tokens 11.5 us, of 30000 25 us: two launches and a
+// warp's chain of waits (page id, records, query), hence ranges down to one
+// group, so that many warps share few tokens.
 #include "tq_attention.cuh"
 
 namespace tq {
@@ -36,10 +46,19 @@ namespace {
 constexpr int kGroup = 16;               // tokens of a group
 constexpr uint32_t kLutBase = 0x10000u;  // shared-memory address of the centroid table
 constexpr uint32_t kLutStep = 256;       // bytes between its rows (128 used)
-constexpr int kLeastGroups = 1;          // groups of a warp's range at least
+// Groups of a warp's range at least: a single token over 1000 cached ones takes
+// 13.8 us with 1 and 17 with 4 (before the joining launch was made cheaper).
+constexpr int kLeastGroups = 1;
+// What beginning a unit costs (its query rotated, its part written), in groups:
+// 0, 2 and 4 take 107, 105.6 and 105.3 us for 64 sequences of up to 8000 tokens;
+// in tiles of the tcgen05 kernel, 0, 2, 3, 4 and 5 take 66, 58, 56, 56 and 57 us
+// for 16 trees of 16 tokens and 167, 166, 163, 162 and 161 us for 4 trees of 64.
 constexpr int kExtraGroups = 4;
 constexpr int kTcExtra = 4;
-constexpr int kTcLeastRows = 16;         // above: the tcgen05 kernel
+// Rows of a key/value head above which the tcgen05 kernel runs.  mma.sync
+// against tcgen05, head dimension 128: 16 sequences of 4000 tokens with 16 rows
+// 55 and 70 us, with 24 rows 83 and 76; 4 of 30000 tokens 67 and 104, 120 and 106.
+constexpr int kTcLeastRows = 16;
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
     uint32_t d;
@@ -139,7 +158,8 @@ struct ValueRegs {
     uint32_t d[4];  // one or two half-block scales
 };
 
-// Where this lane's rows begin within a group (added to warp-uniform bases); with FULL the head dimension is DP itself and no piece is missing.
+// Where this lane's rows begin within a group (added to warp-uniform bases);
+// with FULL the head dimension is DP itself and no piece is missing.
 template <int DP, bool FULL>
 struct LaneOffsets {
     int dim;
@@ -237,7 +257,9 @@ struct AttnState {
     float m[NT][2], l[NT][2];
 };
 
-constexpr int kStepGroups = 2;  // groups of a warp's step
+// Groups of a warp's step: 1 and 2 took 112 and 103.5 us for 64 sequences of up
+// to 8000 tokens (12.3 and 13.8 us for one of 1000).
+constexpr int kStepGroups = 2;
 
 // Scores of a group against the rotated queries: s[n] = K q^T.
 template <int DP, int NT>
@@ -588,7 +610,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 // eight warps; RW = 8: the warps share one row's parts, and the first adds up
 // and finishes.  RW = 1: a warp takes a row.  What bounds this launch is its
 // chain of dependent loads (span, then maxima, sums and the first values), so
-// the attention kernel leaves each unit's span of slots ready to be read.
+// the attention kernel leaves each unit's span of slots ready to be read, and
+// values are loaded before their weights are known (figures: launch_join_by).
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 
@@ -737,7 +760,11 @@ AttnPlan plan_attention(int64_t batch, int tree, int heads, int kv_heads, int he
         p.extra = kTcExtra;
     } else {
         // tiles of 8 rows, or 16 where a (sequence, head) has more than 8 rows
-        // and the accumulators of 16 fit the registers (head dimension up to 128)
+        // and the accumulators of 16 fit the registers (head dimension up to
+        // 128): 16 rows over 64 sequences of 4000 tokens as one tile 126 us, as
+        // two 166.  16 warps where 128 registers hold a tile: 8 rows over the
+        // same 89 us, with 8 warps 105 (one sequence of 30000 tokens, whose
+        // parts have to be joined, 25 and 21)
         p.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
         p.nt = p.rows > 8 && p.dp <= 128 ? 2 : 1;
         p.warps = p.nt == 2 || p.dp == 256 ? 8 : 16;
@@ -807,8 +834,8 @@ cudaError_t launch_join(const AttnParams &P, int odtype, cudaStream_t stream) {
 // maxima and sums, their values.
 size_t attention_workspace_bytes(int64_t batch, int tree, int heads, int kv_heads, int head_dim, int sm_count) {
     const AttnPlan p = plan_attention(batch, tree, heads, kv_heads, head_dim, sm_count);
-    return 256 + round_up((size_t)batch * kv_heads * p.row_tiles * 8, 256) + round_up((size_t)p.slots * p.tile_rows * 8, 256) +
-           (size_t)p.slots * p.tile_rows * head_dim * 4;
+    return 256 + round_up((size_t)batch * kv_heads * p.row_tiles * 8, 256) +
+           round_up((size_t)p.slots * p.tile_rows * 8, 256) + (size_t)p.slots * p.tile_rows * head_dim * 4;
 }
 
 cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t stream) {

@@ -278,6 +278,8 @@ cudaError_t launch_kv_commit(const KvCommitJob &job, cudaStream_t stream);
 // 16 tokens, and the groups of all units into equal ranges, one per warp; the
 // part of a unit that one warp takes leaves a partial result in slot
 // (unit + warp) of the workspace, and a second launch joins each unit's parts.
+// (Many rows, tq_tcattention.cu: tiles of 128 or 256 rows, groups of 128
+// tokens, ranges per CTA.)
 struct AttentionJob {
     KvCache c;
     const int32_t *lens, *parents;

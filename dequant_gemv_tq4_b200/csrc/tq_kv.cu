@@ -46,6 +46,9 @@ __device__ __forceinline__ float2 rope_cos_sin(int position, float inv_freq, flo
 // the rotated part) of one token for `hchunk` heads: the angles, which all
 // heads share, are computed once per item.  Bound by HBM for long inputs
 // (each element is read and written once), by the launch for one step.
+// 8191 tokens x 32 heads x 128 in fp32, half of the elements rotated: 46.8 us,
+// 5.7 TB/s; 64 tokens in bf16: 2.8 us.  Angle: 64-bit product and reduction to
+// a turn, then 32-bit functions, so positions in the millions keep 2^-25 turns.
 // ---------------------------------------------------------------------------
 struct RopeParams {
     const char *x;
@@ -208,6 +211,8 @@ __device__ __forceinline__ int64_t record_index(const KvCache &C, int64_t page, 
 // that a token's rotary angles are computed once for all of them.
 // The arithmetic is tq_quantize's, operation for operation (butterfly stages
 // 1, 2 in registers, 4, 8, 16 across lanes; adjacent-pair tree of squares).
+// Bound by the launch and one item's chain: 64 tokens x 8 heads x 128 take
+// 3.6 us with rotary positions, 2.9 without.
 // ---------------------------------------------------------------------------
 struct AppendParams {
     KvCache c;
@@ -339,6 +344,9 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendParam
 // tokens; their rotary angles stand in shared memory, one fp64 reduction per
 // token and pair.  Keys and values run one after the other, so that a warp's
 // lanes agree about the rotation.
+// Bound by the codec's arithmetic: 36 instructions an element, issue slots 67%
+// used, ALU pipe 64%.  16384 tokens x 8 heads x 128 in bf16 with rotary
+// positions 49 us, 1.8 TB/s (without 41; with eight lanes a block 85).
 // ---------------------------------------------------------------------------
 constexpr int kAngles = 2048;  // cos, sin pairs of a CTA
 
@@ -392,7 +400,8 @@ __device__ __forceinline__ void rotate_block(const AppendParams &P, const char *
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kKvThreads, DT == kF32 ? 2 : 3) kv_append_block_kernel(const AppendParams P, int per_cta) {
+__global__ void __launch_bounds__(kKvThreads, DT == kF32 ? 2 : 3)
+    kv_append_block_kernel(const AppendParams P, int per_cta) {
     constexpr int E = ElemSize<DT>::value;
     __shared__ __align__(16) float2 angles[kAngles];
     grid_dependency_wait();
@@ -523,7 +532,9 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const ReadParams P)
 
 // Read, many tokens: a lane owns a block; a warp's 32 blocks leave through a
 // stage in shared memory (16-byte chunks, XOR-placed against bank conflicts), so
-// that stores cover whole head vectors instead of 64-byte pieces.
+// that stores cover whole head vectors instead of 64-byte pieces.  16384 tokens
+// x 8 heads x 128 to bf16: 27 us, 3.2 TB/s, issue slots 68% used (eight lanes a
+// block: 49 us).
 template <int DT>
 __global__ void __launch_bounds__(kKvThreads, DT == kF32 ? 2 : 3) kv_read_block_kernel(const ReadParams P) {
     constexpr int E = ElemSize<DT>::value, C = 2 * E;  // 16-byte chunks of a block
@@ -606,7 +617,9 @@ __global__ void __launch_bounds__(kKvThreads, DT == kF32 ? 2 : 3) kv_read_block_
 // 16-byte piece of the codes (or 4 bytes of the scales) of a (plane, head) and
 // moves it for the whole branch, eight records at a time, all eight loads
 // before the stores.  The branch increases, so a record's target never lies
-// behind a source that is still to be read.
+// behind a source that is still to be read.  Bound by two rounds of dependent
+// loads (path and page ids, then records): 32 layers x one sequence 4.1 us, 32
+// layers x 64 sequences of 8 heads x 128, eight accepted of 64, 12.6 us.
 // ---------------------------------------------------------------------------
 struct CommitParams {
     KvCache c;  // of layer 0
@@ -780,7 +793,8 @@ cudaError_t launch_kv_append(const KvAppendJob &j, cudaStream_t stream) {
         if (j.positions && per * (j.rot / 2) > kAngles) per = kAngles / (j.rot / 2);
         P.items = j.tokens;
         const unsigned grid = (unsigned)((j.tokens + per - 1) / per);
-        if (j.dtype == kF32) return launch_dependent(kv_append_block_kernel<kF32>, grid, kKvThreads, 0, stream, P, (int)per);
+        if (j.dtype == kF32)
+            return launch_dependent(kv_append_block_kernel<kF32>, grid, kKvThreads, 0, stream, P, (int)per);
         if (j.dtype == kBF16)
             return launch_dependent(kv_append_block_kernel<kBF16>, grid, kKvThreads, 0, stream, P, (int)per);
         return launch_dependent(kv_append_block_kernel<kF16>, grid, kKvThreads, 0, stream, P, (int)per);

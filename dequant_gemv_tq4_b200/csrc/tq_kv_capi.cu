@@ -196,10 +196,8 @@ tq_status tq_kv_commit(const tq_kv_cache *cache, int64_t layers, int64_t code_la
     if (layers > 1 && (code_layer_stride < 0 || scale_layer_stride < 0)) return TQ_ERR_INVALID_ARG;
     if (layers > 1 && (code_layer_stride % 16 != 0 || scale_layer_stride % 8 != 0)) return TQ_ERR_ALIGNMENT;
     // layers that share records would be moved more than once
-    if (layers > 1 &&
-        ((size_t)code_layer_stride < tq_kv_codes_bytes(cache->pages, cache->kv_heads, cache->head_dim, cache->page_size) ||
-         2 * (size_t)scale_layer_stride <
-             tq_kv_scales_bytes(cache->pages, cache->kv_heads, cache->head_dim, cache->page_size)))
+    const size_t pool = tq_kv_codes_bytes(cache->pages, cache->kv_heads, cache->head_dim, cache->page_size);
+    if (layers > 1 && ((size_t)code_layer_stride < pool || 2 * (size_t)scale_layer_stride < pool / 4))
         return TQ_ERR_INVALID_ARG;
     if (layers == 0 || steps == 0 || cache->batch == 0) return TQ_OK;
     if (!lens || !path) return TQ_ERR_INVALID_ARG;
