@@ -607,135 +607,176 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 
 // ---------------------------------------------------------------------------
 // The parts of each row joined, rotated back, divided and rounded.  CTAs of
-// eight warps; RW = 8: the warps share one row's parts, and the first adds up
-// and finishes.  RW = 1: a warp takes a row.  What bounds this launch is its
-// chain of dependent loads (span, then maxima, sums and the first values), so
-// the attention kernel leaves each unit's span of slots ready to be read, and
-// values are loaded before their weights are known (figures: launch_join_by).
+// eight warps; a warp takes a row (RW = 1), or all eight share one (RW = 8), as
+// they do in any launch where a row has more than kAlone parts (a long sequence
+// among short ones: 100000 tokens and 64 times 100, 54 us, with a warp for each
+// row 99); a CTA's rows lie far apart, so that such rows seldom meet in one.
+// SB: halves of 128 elements.  What bounds this launch is its chain of dependent loads (span, then
+// maxima, sums and the first values), so the attention kernel leaves each unit's
+// span of slots ready to be read, and values are loaded before their weights are
+// known (figures: launch_join_by).
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
+constexpr int kAlone = 32;
 
-template <int OT, int RW>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttnParams P) {
-    __shared__ float so[RW == 1 ? 1 : kJoinWarps][256];
-    __shared__ float sl[kJoinWarps], sm[kJoinWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int index = (int)blockIdx.x * (kJoinWarps / RW) + warp / RW;
-    const int bh = index / P.rows, row = index % P.rows;
-    const int b = bh / P.c.kv_heads, head = bh % P.c.kv_heads;
-    const int tile = row / P.tile_rows, r = row % P.tile_rows;
-    const int t = row / P.group_heads, h = head * P.group_heads + row % P.group_heads;
+// Maximum, sum and values (4 lane + i of each 128) of parts.
+template <int SB>
+struct JoinState {
+    float acc[SB][4], m, l;
+};
+
+// Parts [c, end) of the slots from s0, row r of each; up to 32 at a time: a lane
+// takes one part's maximum and sum, then all lanes its values.
+template <int AHEAD, int SB>
+__device__ __forceinline__ void join_parts(const AttnParams &P, int64_t s0, int r, int c, int end, int lane,
+                                           JoinState<SB> &st) {
     const int D = P.c.head_dim;
-    uint32_t flips[2];
-#pragma unroll
-    for (int sb = 0; sb < 2; ++sb) flips[sb] = c_sign_words.w[sb * 4 + lane / 8] >> (4 * (lane & 7));
-    grid_dependency_wait();
-    grid_dependents_launch();
-    if (index >= P.c.batch * P.c.kv_heads * P.rows) return;  // (whole CTAs where RW > 1)
-    const int64_t unit = (int64_t)bh * P.row_tiles + tile;
-    // its workers; a call that gave up left some of these unwritten, so they are bounded
-    const int2 span = *reinterpret_cast<const int2 *>(P.span + 2 * unit);
-    const int first = min(max(span.x, 0), P.workers - 1);
-    const int last = min(max(span.y, first), P.workers - 1);
-    const int64_t s0 = (unit + first) * P.parts;                // the unit's first slot
-    const int n = (last - first + 1) * P.parts, w = warp % RW;  // and how many
-
-    float acc[2][4] = {}, m = kNoMax, l = 0.f;
-    // parts whose values are on their way: many in a launch of few rows; of many
-    // rows, as many as leave the registers for other warps (4 instead of 2: 193
-    // against 174 us for 131072 rows; 4 instead of 8: 17.7 against 16.2 us for 32)
-    constexpr int kAhead = RW == 1 ? 2 : 8;
-    // this warp's share of the parts, up to 32 at a time: a lane takes one
-    // part's maximum and sum, then all lanes its values
-    const int share = n * (w + 1) / RW;
-    for (int c = n * w / RW; c < share; c += 32) {
+    st = JoinState<SB>{};
+    st.m = kNoMax;
+    for (; c < end; c += 32) {
         float2 p = make_float2(kNoMax, 0.f);
-        if (c + lane < share) p = reinterpret_cast<const float2 *>(P.part_ml)[(s0 + c + lane) * P.tile_rows + r];
-        const int count = min(32, share - c);
+        if (c + lane < end) p = reinterpret_cast<const float2 *>(P.part_ml)[(s0 + c + lane) * P.tile_rows + r];
+        const int count = min(32, end - c);
         const float *src = P.part_o + ((s0 + c) * P.tile_rows + r) * D + 4 * lane;
-        float4 v[kAhead][2];
-        auto values = [&](int j, float4 (&o)[2]) {
+        float4 v[AHEAD][SB];
+        auto values = [&](int j, float4 (&o)[SB]) {
 #pragma unroll
-            for (int sb = 0; sb < 2; ++sb) {
+            for (int sb = 0; sb < SB; ++sb) {
                 o[sb] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (j < count && sb * 128 + 4 * lane < D)
                     o[sb] = *reinterpret_cast<const float4 *>(src + (int64_t)j * P.tile_rows * D + sb * 128);
             }
         };
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) values(j, v[j]);
-        float mx = fmaxf(m, p.y > 0.f ? p.x : kNoMax);
+        for (int j = 0; j < AHEAD; ++j) values(j, v[j]);
+        float mx = fmaxf(st.m, p.y > 0.f ? p.x : kNoMax);
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
         const float f = p.y > 0.f ? ex2((p.x - mx) * P.scale_log2) : 0.f;
         float sum = f * p.y;
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
-        const float old = ex2((m - mx) * P.scale_log2);
-        l = l * old + sum;
-        m = mx;
+        const float old = ex2((st.m - mx) * P.scale_log2);
+        st.l = st.l * old + sum;
+        st.m = mx;
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb)
+        for (int sb = 0; sb < SB; ++sb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[sb][i] *= old;
-        for (int j = 0; j < count; j += kAhead) {
+            for (int i = 0; i < 4; ++i) st.acc[sb][i] *= old;
+        for (int j = 0; j < count; j += AHEAD) {
 #pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
+            for (int q = 0; q < AHEAD; ++q) {
                 const float fj = j + q < count ? __shfl_sync(kFull, f, j + q) : 0.f;
                 // (a part without a token may never have been written: its values do not count)
                 if (fj != 0.f) {
 #pragma unroll
-                    for (int sb = 0; sb < 2; ++sb) {
-                        acc[sb][0] += fj * v[q][sb].x;
-                        acc[sb][1] += fj * v[q][sb].y;
-                        acc[sb][2] += fj * v[q][sb].z;
-                        acc[sb][3] += fj * v[q][sb].w;
+                    for (int sb = 0; sb < SB; ++sb) {
+                        st.acc[sb][0] += fj * v[q][sb].x;
+                        st.acc[sb][1] += fj * v[q][sb].y;
+                        st.acc[sb][2] += fj * v[q][sb].z;
+                        st.acc[sb][3] += fj * v[q][sb].w;
                     }
                 }
-                values(j + kAhead + q, v[q]);
+                values(j + AHEAD + q, v[q]);
             }
         }
     }
-    if (RW > 1) {
+}
+
+template <int OT, int RW, int SB>
+__global__ void __launch_bounds__(kJoinWarps * 32, RW == 1 ? 4 : 2) join_kernel(const AttnParams P) {
+    constexpr int kRows = kJoinWarps / RW;  // of a CTA
+    // parts whose values are on their way: many in a launch of few rows; of many
+    // rows, as many as leave the registers for other warps (4 instead of 2: 182
+    // against 173 us for 131072 rows; 4 instead of 8: 17.7 against 16.2 us for 32)
+    constexpr int kAhead = RW == 1 ? 2 : 8;
+    __shared__ float so[kJoinWarps][128 * SB];
+    __shared__ float sl[kJoinWarps], sm[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rows = P.c.batch * P.c.kv_heads * P.rows, grid = (int)gridDim.x;
+    const int index = warp / RW * grid + (int)blockIdx.x;
+    const int bh = index / P.rows, row = index % P.rows;
+    const int b = bh / P.c.kv_heads, head = bh % P.c.kv_heads;
+    const int t = row / P.group_heads, h = head * P.group_heads + row % P.group_heads;
+    const int D = P.c.head_dim;
+    uint32_t flips[SB];
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb)
-            *reinterpret_cast<float4 *>(&so[warp][sb * 128 + 4 * lane]) =
-                make_float4(acc[sb][0], acc[sb][1], acc[sb][2], acc[sb][3]);
-        if (lane == 0) {
-            sl[warp] = l;
-            sm[warp] = m;
+    for (int sb = 0; sb < SB; ++sb) flips[sb] = c_sign_words.w[sb * 4 + lane / 8] >> (4 * (lane & 7));
+    // lane k: row k of the CTA, its place in its tile, its unit
+    const int of_lane = min(lane, kRows - 1) * grid + (int)blockIdx.x;
+    const int lane_row = of_lane % P.rows;
+    const int lane_r = lane_row % P.tile_rows;
+    const int64_t unit = (int64_t)(of_lane / P.rows) * P.row_tiles + lane_row / P.tile_rows;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    int64_t slot = 0;
+    int parts = 0;
+    if (of_lane < rows) {
+        // its workers; a call that gave up left some of these unwritten, so they are bounded
+        const int2 span = *reinterpret_cast<const int2 *>(P.span + 2 * unit);
+        const int first = min(max(span.x, 0), P.workers - 1);
+        const int last = min(max(span.y, first), P.workers - 1);
+        slot = (unit + first) * P.parts;       // the unit's first slot
+        parts = (last - first + 1) * P.parts;  // and how many
+    }
+    auto finish = [&](JoinState<SB> &st) {
+        const float inv = st.l > 0.f ? 0.03125f / st.l : 0.f;
+        char *out = P.out + (b * P.o_batch + t * P.o_token + h * P.o_head) * ElemSize<OT>::value;
+#pragma unroll
+        for (int sb = 0; sb < SB; ++sb) {
+            if (sb * 128 >= D) break;
+            const int e = sb * 128 + 4 * lane;
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = st.acc[sb][i] * inv;
+            fwht32_warp(v, lane & 7);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = flip(v[i], (flips[sb] << (31 - i)) & 0x80000000u);
+            if (e < D) store4<OT>(out + (int64_t)e * ElemSize<OT>::value, v);
         }
-        __syncthreads();
-        if (warp != 0) return;
-        float mx = kNoMax;
-#pragma unroll
-        for (int x = 0; x < RW; ++x) mx = fmaxf(mx, sm[x]);
-        l = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.f;
-#pragma unroll
-        for (int x = 0; x < RW; ++x) {
-            const float f = ex2((sm[x] - mx) * P.scale_log2);
-            l += f * sl[x];
-#pragma unroll
-            for (int sb = 0; sb < 2; ++sb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[sb][i] += f * so[x][sb * 128 + 4 * lane + i];
+    };
+    if (RW == 1) {
+        const int n = __shfl_sync(kFull, parts, warp);
+        if (n > 0 && n <= kAlone) {
+            JoinState<SB> st;
+            join_parts<kAhead, SB>(P, __shfl_sync(kFull, slot, warp), __shfl_sync(kFull, lane_r, warp), 0, n, lane, st);
+            finish(st);
         }
     }
-    const float inv = l > 0.f ? 0.03125f / l : 0.f;
-    char *out = P.out + (b * P.o_batch + t * P.o_token + h * P.o_head) * ElemSize<OT>::value;
+    // rows that all warps share (every warp knows them)
+    uint32_t shared = __ballot_sync(kFull, lane < kRows && parts > (RW == 1 ? kAlone : 0));
+#pragma unroll 1
+    for (; shared; shared &= shared - 1) {
+        const int k = __ffs(shared) - 1, n = __shfl_sync(kFull, parts, k);
+        JoinState<SB> st;
+        join_parts<kAhead, SB>(P, __shfl_sync(kFull, slot, k), __shfl_sync(kFull, lane_r, k), n * warp / kJoinWarps,
+                               n * (warp + 1) / kJoinWarps, lane, st);
 #pragma unroll
-    for (int sb = 0; sb < 2; ++sb) {
-        if (sb * 128 >= D) break;
-        const int e = sb * 128 + 4 * lane;
-        float v[4];
+        for (int sb = 0; sb < SB; ++sb)
+            *reinterpret_cast<float4 *>(&so[warp][sb * 128 + 4 * lane]) =
+                make_float4(st.acc[sb][0], st.acc[sb][1], st.acc[sb][2], st.acc[sb][3]);
+        if (lane == 0) {
+            sl[warp] = st.l;
+            sm[warp] = st.m;
+        }
+        __syncthreads();
+        if (warp == k * RW) {
+            float mx = kNoMax;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = acc[sb][i] * inv;
-        fwht32_warp(v, lane & 7);
+            for (int x = 0; x < kJoinWarps; ++x) mx = fmaxf(mx, sm[x]);
+            st = JoinState<SB>{};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = flip(v[i], (flips[sb] << (31 - i)) & 0x80000000u);
-        if (e < D) store4<OT>(out + (int64_t)e * ElemSize<OT>::value, v);
+            for (int x = 0; x < kJoinWarps; ++x) {
+                const float f = ex2((sm[x] - mx) * P.scale_log2);
+                st.l += f * sl[x];
+#pragma unroll
+                for (int sb = 0; sb < SB; ++sb)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) st.acc[sb][i] += f * so[x][sb * 128 + 4 * lane + i];
+            }
+            finish(st);
+        }
+        if (RW == 1) __syncthreads();
     }
 }
 
@@ -804,8 +845,9 @@ cudaError_t launch_attend(const AttnParams &P, cudaStream_t stream) {
 template <int OT, int RW>
 cudaError_t launch_join_as(const AttnParams &P, cudaStream_t stream) {
     const int64_t warps = (int64_t)P.c.batch * P.c.kv_heads * P.rows * RW;
-    return launch_dependent(join_kernel<OT, RW>, (unsigned)((warps + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0,
-                            stream, P);
+    const unsigned grid = (unsigned)((warps + kJoinWarps - 1) / kJoinWarps);
+    return P.c.head_dim <= 128 ? launch_dependent(join_kernel<OT, RW, 1>, grid, kJoinWarps * 32, 0, stream, P)
+                               : launch_dependent(join_kernel<OT, RW, 2>, grid, kJoinWarps * 32, 0, stream, P);
 }
 
 // Eight warps share a row where rows are few and their parts (about workers /

@@ -403,6 +403,9 @@ CASES = [
     (3, 50, 3, 1, 64, 16, [0, 128, 700], BF16, "absent"),  # 150 rows: a row tile of its own for the last 22
     (1, 1, 4, 1, 64, 1024, [45000], F16, None),  # more parts than a warp joins at once
     (1, 24, 4, 2, 128, 64, [30000], BF16, "tree"),
+    # many rows, one long sequence among short ones: its rows are joined by more than a warp
+    (40, 2, 16, 1, 32, 16, [3 * (i % 5) for i in range(39)] + [3000], BF16, "tree"),
+    (20, 8, 16, 2, 64, 16, [10000] + [i % 7 for i in range(19)], F16, "absent"),
 ]
 
 
