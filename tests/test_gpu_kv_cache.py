@@ -403,6 +403,9 @@ CASES = [
     (3, 50, 3, 1, 64, 16, [0, 128, 700], BF16, "absent"),  # 150 rows: a row tile of its own for the last 22
     (1, 1, 4, 1, 64, 1024, [45000], F16, None),  # more parts than a warp joins at once
     (1, 24, 4, 2, 128, 64, [30000], BF16, "tree"),
+    # more sequences than a CTA has threads, for both kernels
+    (1200, 1, 2, 1, 32, 16, [i % 15 for i in range(1200)], F16, None),
+    (520, 17, 1, 1, 64, 16, [i % 31 for i in range(520)], BF16, None),
     # many rows, one long sequence among short ones: its rows are joined by more than a warp
     (40, 2, 16, 1, 32, 16, [3 * (i % 5) for i in range(39)] + [3000], BF16, "tree"),
     (20, 8, 16, 2, 64, 16, [10000] + [i % 7 for i in range(19)], F16, "absent"),
@@ -616,6 +619,24 @@ def test_attention_on_another_stream_and_in_graphs(cuda_lib):
         torch.cuda.synchronize()
         for out, query in zip(outs, (q, q2)):
             assert torch.equal(out, cuda_lib.kv_attention(codes, scales, table, lens, query, parents=par))
+
+
+def test_attention_calls_at_once(cuda_lib):
+    """Calls of both kernels on four streams that overlap, with workspaces of their own."""
+    B, H, kv, D, page = 3, 8, 2, 128, 16
+    codes, scales, table = _filled(cuda_lib, B, 60, kv, D, page, seed=53)
+    lens = _i32([900, 5, 333])
+    qs = [_rand(i, B, T, H, D, dtype=BF16).to(DEV) for i, T in enumerate((1, 30, 4, 20))]
+    want = [cuda_lib.kv_attention(codes, scales, table, lens, q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[] for _ in qs]
+    for _ in range(20):
+        for q, stream, outs in zip(qs, streams, got):
+            outs.append(cuda_lib.kv_attention(codes, scales, table, lens, q, stream=stream))
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        assert all(torch.equal(o, w) for o in outs)
 
 
 def test_what_a_call_allocates_belongs_to_its_stream(cuda_lib):
