@@ -46,6 +46,9 @@ constexpr int kPieces = 8;      // of a tile: 32 tokens' keys or values
 // Shares of the launch's 65536: 256 * 184 + 256 * 72 = 65536.
 constexpr int kSoftRegs = 184, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 256 * kOtherRegs <= kTcaThreads * 128, "register shares");
+// setmaxnreg has to be the same instruction for all four warps of a warpgroup:
+// the shares change hands where whole warpgroups part, above the roles.
+static_assert(kSoftWarps % 4 == 0 && kTcaThreads / 32 % 4 == 0, "shares go by warpgroups");
 constexpr int kTmemCols = 512;
 constexpr uint32_t kOCol = 256;  // output accumulators; scores at 0 and 128
 constexpr unsigned kStatusTimeout = 1u;
@@ -527,9 +530,11 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
     };
     Part p;
 
+    if (warp < kSoftWarps) a_regs_more<kSoftRegs>();
+    else a_regs_fewer<kOtherRegs>();
+
     if (warp < kSoftWarps) {
         // ---- softmax: thread = row of a stream ----------------------------------
-        a_regs_more<kSoftRegs>();
         const int s = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + 128u * s, t_o = tmem + lanes + kOCol + 128u * s;
@@ -630,7 +635,6 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
         }
     } else if (warp != kMmaWarp) {
         // ---- decode ------------------------------------------------------------------
-        a_regs_fewer<kOtherRegs>();
         const int first = warp < kMmaWarp ? warp - kSoftWarps : warp - kSoftWarps - 1;  // of this warp's pieces
         const int shift = P.c.page_shift, in_page = (1 << shift) - 1;
         const int v_rows = P.c.kv_heads << shift;
@@ -690,7 +694,6 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
         }
     } else {
         // ---- tensor-core issue -----------------------------------------------------
-        a_regs_fewer<kOtherRegs>();
         // The whole warp walks and waits, one elected lane issues: descriptors
         // stay warp-uniform that way (uniform registers are what the
         // instruction reads).  Broadcasts say so where values come from memory.
