@@ -1,41 +1,12 @@
 // tq_cache.cuh -- what the key/value cache's kernels and the attention over it
-// share: ordinary loads, the sign pattern of a head's columns, and a 32-element
-// block in one lane's registers, with the arithmetic of the weight codec
-// (tq_codec.cu), operation for operation.
+// share: the sign pattern of a head's columns, and a 32-element block in one
+// lane's registers, with the arithmetic of the weight codec (tq_codec.cu),
+// operation for operation.
 #pragma once
 
 #include "tq_device.cuh"
 
 namespace tq {
-
-// An ordinary load.  A programmatic dependent that reads what the kernel before
-// it writes uses this after its wait: the read-only path (load4, __ldg) asks for
-// data that nobody writes while the kernel is resident.
-template <typename T>
-__device__ __forceinline__ T ld(const T *p) {
-    return *p;
-}
-
-// load4 by ordinary loads.
-template <int DT>
-__device__ __forceinline__ void load4_ordinary(const void *p, float (&v)[4]) {
-    if constexpr (DT == kF32) {
-        const float4 q = ld(reinterpret_cast<const float4 *>(p));
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-    } else {
-        const uint2 q = ld(reinterpret_cast<const uint2 *>(p));
-        if constexpr (DT == kBF16) {
-            v[0] = __uint_as_float(q.x << 16);
-            v[1] = __uint_as_float(q.x & 0xffff0000u);
-            v[2] = __uint_as_float(q.y << 16);
-            v[3] = __uint_as_float(q.y & 0xffff0000u);
-        } else {
-            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&q.x));
-            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&q.y));
-            v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-        }
-    }
-}
 
 // a / b of non-negative numbers, in 32 bits where both fit
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {

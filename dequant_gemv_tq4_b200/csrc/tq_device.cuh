@@ -88,6 +88,35 @@ __device__ __forceinline__ void load4<kF16>(const void *p, float (&v)[4]) {
     v[0] = f0.x; v[1] = f0.y; v[2] = f1.x; v[3] = f1.y;
 }
 
+// An ordinary load.  A programmatic dependent that reads what the kernel before
+// it writes uses this after its wait: the read-only path (load4, __ldg) asks for
+// data that nobody writes while the kernel is resident.
+template <typename T>
+__device__ __forceinline__ T ld(const T *p) {
+    return *p;
+}
+
+// load4 by ordinary loads.
+template <int DT>
+__device__ __forceinline__ void load4_ordinary(const void *p, float (&v)[4]) {
+    if constexpr (DT == kF32) {
+        const float4 q = ld(reinterpret_cast<const float4 *>(p));
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+        const uint2 q = ld(reinterpret_cast<const uint2 *>(p));
+        if constexpr (DT == kBF16) {
+            v[0] = __uint_as_float(q.x << 16);
+            v[1] = __uint_as_float(q.x & 0xffff0000u);
+            v[2] = __uint_as_float(q.y << 16);
+            v[3] = __uint_as_float(q.y & 0xffff0000u);
+        } else {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&q.x));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&q.y));
+            v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+        }
+    }
+}
+
 // Stores of 4 consecutive fp32 values rounded (nearest-even) to the dtype.
 template <int DT>
 __device__ __forceinline__ void store4(void *p, const float (&v)[4]);
@@ -138,7 +167,8 @@ struct ElemSize {
 // PTX wrappers
 // ---------------------------------------------------------------------------
 
-// 128-bit global load that may stay in L1 (small, reused operands).
+// 128-bit global load that may stay in L1 (small, reused operands that no
+// kernel still running writes: packed weights).
 __device__ __forceinline__ uint4 ldg_keep(const void *p) {
     uint4 r;
     asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
@@ -246,7 +276,8 @@ __device__ __forceinline__ void rotate_unit_lane(const char *x, int64_t ldx, int
     const bool valid = sb * kSbBlocks + j < nb && row < m;
     const uint32_t col0 = (uint32_t)sb * kSbElems + 32u * j + 4u * p;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
-    if (valid) load4<DT>(x + ((int64_t)row * ldx + col0) * ElemSize<DT>::value, v);
+    // the activation may be the output of a kernel that let this one start early
+    if (valid) load4_ordinary<DT>(x + ((int64_t)row * ldx + col0) * ElemSize<DT>::value, v);
     if (ROTATE) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = flip(v[i], sign_mask(col0 + i));

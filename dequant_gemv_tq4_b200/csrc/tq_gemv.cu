@@ -194,9 +194,16 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
-__device__ __forceinline__ uint2 ldg64(const void *p) {
+// Loads of pre-rotated activations: ordinary ones, because this kernel is
+// resident while the pre-rotation writes them.
+__device__ __forceinline__ uint2 ld_act64(const void *p) {
     uint2 r;
-    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint4 ld_act128(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
     return r;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -452,7 +459,7 @@ __device__ __forceinline__ void unit_product(uint32_t sc, uint32_t ss, const uin
     for (int j = 0; j < kSbBlocks; ++j) {
         uint4 xb[NT];
 #pragma unroll
-        for (int a = 0; a < NT; ++a) xb[a] = ldg_keep(xcur[a] + xoff + j * 32);
+        for (int a = 0; a < NT; ++a) xb[a] = ld_act128(xcur[a] + xoff + j * 32);
         // code byte b of word cw: logical byte t + 4b of the block
         const uint32_t a00 = lds_lut(prmt(cw0[j], lut_lane, 0x7604u));
         const uint32_t a01 = lds_lut(prmt(cw1[j], lut_lane, 0x7604u));
@@ -618,7 +625,7 @@ template <int CM>
 __device__ __forceinline__ XWords<CM> load_xwords(const char *xb) {
     XWords<CM> xv;
 #pragma unroll
-    for (int k = 0; k < (CM == 0 ? 1 : CM); ++k) xv.w[k] = ldg64(xb + 64 * k);
+    for (int k = 0; k < (CM == 0 ? 1 : CM); ++k) xv.w[k] = ld_act64(xb + 64 * k);
     return xv;
 }
 

@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(256) prerotate_plain_kernel(const __grid_const
             const int64_t r = row + u * groups;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[u][i] = 0.f;
-            if (valid && r < R.m) load4<DT>(R.x + (r * R.ldx + col0) * ElemSize<DT>::value, v[u]);
+            if (valid && r < R.m) load4_ordinary<DT>(R.x + (r * R.ldx + col0) * ElemSize<DT>::value, v[u]);
         }
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {

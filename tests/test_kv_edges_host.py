@@ -22,3 +22,15 @@ def test_registers_change_hands_by_whole_warpgroups():
     assert len(shares) == 2
     within = kernel.index("warp != kMmaWarp")  # warps 12 and 13..15 go separate ways
     assert max(shares) < within
+
+
+@pytest.mark.parametrize("name,begin", [
+    ("tq_device.cuh", "rotate_unit_lane("), ("tq_prefill.cu", "prerotate_plain_kernel("),
+    ("tq_gemv.cu", "unit_product("), ("tq_gemv.cu", "load_xwords(")])
+def test_activations_are_read_by_ordinary_loads(name, begin):
+    """What the kernel before may still be writing (a rotary or attention output, a
+    pre-rotated activation) is not asked for by the read-only path."""
+    body = _code(name).split(begin, 1)[1].split("\n}\n", 1)[0]
+    assert not re.search(r"\b(load4<|__ldg\(|ldg_keep\(|ldg64\(|p_ldg128\()", body)
+    read_only = set(re.findall(r"(\w+)\([^)]*\)\s*\{[^{}]*\basm volatile\(\"ld\.global\.nc", _code(name)))
+    assert not any(re.search(r"\b%s\(" % f, body) for f in read_only)
