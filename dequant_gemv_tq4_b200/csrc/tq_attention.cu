@@ -23,10 +23,11 @@
 // pairs have to hold two tokens of one element; nibbles of two tokens' code
 // words are merged before the lookup (two operations per 8 codes).
 // Roundings to fp16: centroid (2^-12 relative), centroid x scale, rotated
-// query (as in the products of this library), and the softmax weights, which
-// are scaled by 2^7.  The maximum they refer to is followed only when it grows
-// by more than 2^8 (rescaling the accumulators is the exception), so a weight
-// is at most 2^15, and weights down to 2^-31 of the largest survive.
+// query (as in the products of this library; times the softmax's scale and a
+// power of two, RowScale), and the softmax weights, which are scaled by 2^7.
+// The maximum they refer to is followed only when it grows by more than 2^8
+// (rescaling the accumulators is the exception), so a weight is at most 2^15,
+// and weights down to 2^-31 of the largest survive.
 //
 // What bounds it: instruction issue and shared-memory lookups, not HBM.  Per
 // pair of elements of a group the lookup, its address and the scale are three
@@ -95,47 +96,54 @@ __device__ __forceinline__ void fill_lut(int tid, int threads) {
 // The rotated query as operand fragments, straight from memory: lane
 // l = 4 g + c owns row g, elements DP/4 c .. of it, which for a head dimension
 // of 128 is one whole block (of 64: half of one, the other half at lane ^ 1),
-// so that the transform runs in registers.  `x` is the lane's row.
+// so that the transform runs in registers.  `x` is the lane's row.  Returns the
+// unit of row g's scores.
 template <int DT, int DP>
-__device__ __forceinline__ void rotate_query(const AttnParams &P, const char *x, bool valid, int c,
-                                             uint32_t (&qf)[DP / 16][2]) {
+__device__ __forceinline__ float rotate_query(const AttnParams &P, const char *x, bool valid, int c,
+                                              uint32_t (&qf)[DP / 16][2]) {
     constexpr int N = DP / 4 < 32 ? 16 : 32;  // elements of a block that the lane holds
-    const float f = P.negative ? -0.03125f : 0.03125f;
+    constexpr int B = DP / 4 / N;             // such pieces
+    float v[B][N], most[2] = {0.f, 0.f};
 #pragma unroll
-    for (int blk = 0; blk < DP / 4 / N; ++blk) {
+    for (int blk = 0; blk < B; ++blk) {
         const int e0 = c * (DP / 4) + blk * N;
         const uint32_t bits = c_sign_words.w[e0 / 32] >> (e0 % 32);
-        float v[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = 0.f;
-        if (valid && e0 < P.c.head_dim) {
+        for (int i = 0; i < N; i += 4) {
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            if (valid && e0 < P.c.head_dim) load4_ordinary<DT>(x + (int64_t)(e0 + i) * ElemSize<DT>::value, t);
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                float t[4];
-                load4_ordinary<DT>(x + (int64_t)(e0 + i) * ElemSize<DT>::value, t);
+            for (int k = 0; k < 4; ++k) most[k & 1] = fmaxf(most[k & 1], fabsf(t[k]));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[i + k] = flip(t[k], (bits << (31 - i - k)) & 0x80000000u);
-            }
+            for (int k = 0; k < 4; ++k) v[blk][i + k] = flip(t[k], (bits << (31 - i - k)) & 0x80000000u);
         }
+    }
+    float all = fmaxf(most[0], most[1]);
+    all = fmaxf(all, __shfl_xor_sync(kFull, all, 1));
+    all = fmaxf(all, __shfl_xor_sync(kFull, all, 2));
+    const RowScale scale(P.q_factor, all);
+#pragma unroll
+    for (int blk = 0; blk < B; ++blk) {
 #pragma unroll
         for (int h = 1; h < N; h <<= 1)
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 if ((i & h) == 0) {
-                    const float a = v[i], b = v[i + h];
-                    v[i] = a + b;
-                    v[i + h] = a - b;
+                    const float a = v[blk][i], b = v[blk][i + h];
+                    v[blk][i] = a + b;
+                    v[blk][i + h] = a - b;
                 }
         if (N == 16) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = butterfly_xlane(v[i], 1, c & 1);
+            for (int i = 0; i < N; ++i) v[blk][i] = butterfly_xlane(v[blk][i], 1, c & 1);
         }
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            const __half2 h = __floats2half2_rn(v[i] * f, v[i + 1] * f);
+            const __half2 h = __floats2half2_rn(v[blk][i] * scale.factor, v[blk][i + 1] * scale.factor);
             qf[(blk * N + i) / 4][(i / 2) & 1] = *reinterpret_cast<const uint32_t *>(&h);
         }
     }
+    return scale.unit;
 }
 
 // What a lane (l = 4 g + c) holds of a group of 16 tokens.  Key rows: tokens
@@ -254,7 +262,7 @@ __device__ __forceinline__ uint32_t dup_half(uint32_t d, bool high) { return prm
 template <int DP, int NT>
 struct AttnState {
     float o[NT][DP / 16][4];
-    float m[NT][2], l[NT][2];
+    float off[NT][2], unit[NT][2], l[NT][2];  // RowScale
 };
 
 // Groups of a warp's step: 1 and 2 took 112 and 103.5 us for 64 sequences of up
@@ -351,7 +359,7 @@ __device__ __forceinline__ void step_weights(const AttnParams &P, float (&s)[kSt
         float mx[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            mx[k] = st.m[n][k];
+            mx[k] = kNoMax;
 #pragma unroll
             for (int q = 0; q < kStepGroups; ++q) mx[k] = fmaxf(mx[k], fmaxf(s[q][n][k], s[q][n][k + 2]));
         }
@@ -360,12 +368,13 @@ __device__ __forceinline__ void step_weights(const AttnParams &P, float (&s)[kSt
             mx[0] = fmaxf(mx[0], __shfl_xor_sync(kFull, mx[0], x));
             mx[1] = fmaxf(mx[1], __shfl_xor_sync(kFull, mx[1], x));
         }
-        if (__any_sync(kFull, (mx[0] - st.m[n][0]) * P.scale_log2 > kLazy ||
-                                  (mx[1] - st.m[n][1]) * P.scale_log2 > kLazy)) {
+        if (__any_sync(kFull, outgrown(mx[0], st.unit[n][0], st.off[n][0]) ||
+                                  outgrown(mx[1], st.unit[n][1], st.off[n][1]))) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float f = ex2((st.m[n][k] - mx[k]) * P.scale_log2);
-                st.m[n][k] = mx[k];
+                const float off = fminf(st.off[n][k], weight_offset(mx[k], st.unit[n][k]));
+                const float f = ex2(off - st.off[n][k]);
+                st.off[n][k] = off;
                 st.l[n][k] *= f;
 #pragma unroll
                 for (int i = 0; i < DP / 16; ++i) {
@@ -374,13 +383,12 @@ __device__ __forceinline__ void step_weights(const AttnParams &P, float (&s)[kSt
                 }
             }
         }
-        const float base[2] = {kWeightExp - st.m[n][0] * P.scale_log2, kWeightExp - st.m[n][1] * P.scale_log2};
 #pragma unroll
         for (int q = 0; q < kStepGroups; ++q) {
             float p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                p[i] = ex2(fmaf(s[q][n][i], P.scale_log2, base[i & 1]));
+                p[i] = ex2(fmaf(s[q][n][i], st.unit[n][i & 1], st.off[n][i & 1]));
                 if (TAIL && !((ok >> (4 * q + i)) & 1u)) p[i] = 0.f;
             }
             st.l[n][0] += p[0] + p[2];
@@ -513,12 +521,14 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
             const bool valid = row < P.rows;
             const int t = valid ? row / P.group_heads : 0, h = head * P.group_heads + (valid ? row % P.group_heads : 0);
             const int64_t x = b * P.q_batch + t * P.q_token + h * P.q_head;
-            if (P.qdtype == kF32) rotate_query<kF32, DP>(P, P.q + x * 4, valid, c, qf[n]);
-            else if (P.qdtype == kBF16) rotate_query<kBF16, DP>(P, P.q + x * 2, valid, c, qf[n]);
-            else rotate_query<kF16, DP>(P, P.q + x * 2, valid, c, qf[n]);
+            float unit;  // of row g's scores
+            if (P.qdtype == kF32) unit = rotate_query<kF32, DP>(P, P.q + x * 4, valid, c, qf[n]);
+            else if (P.qdtype == kBF16) unit = rotate_query<kBF16, DP>(P, P.q + x * 2, valid, c, qf[n]);
+            else unit = rotate_query<kF16, DP>(P, P.q + x * 2, valid, c, qf[n]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                st.m[n][k] = kNoMax;
+                st.unit[n][k] = __shfl_sync(kFull, unit, 4 * (2 * c + k));  // of row 2c + k
+                st.off[n][k] = weight_offset(kNoMax, st.unit[n][k]);
                 st.l[n][k] = 0.f;
             }
 #pragma unroll
@@ -591,7 +601,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
                 if (row0 + r < P.rows && !((present >> ((row0 + r) / P.group_heads)) & 1ull)) l = 0.f;
                 if (row0 + r < P.rows) {
                     const int64_t at_row = slot * (NT * 8) + r;
-                    if (g == 0) reinterpret_cast<float2 *>(P.part_ml)[at_row] = make_float2(st.m[n][k], l);
+                    if (g == 0) reinterpret_cast<float2 *>(P.part_ml)[at_row] = make_float2(-st.off[n][k], l);
                     if (FULL || g * (DP / 8) < P.c.head_dim) {
                         float4 *dst = reinterpret_cast<float4 *>(P.part_o + at_row * off.dim + g * (DP / 8));
 #pragma unroll
@@ -619,7 +629,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 constexpr int kJoinWarps = 8;
 constexpr int kAlone = 32;
 
-// Maximum, sum and values (4 lane + i of each 128) of parts.
+// Reference (log2), sum and values (4 lane + i of each 128) of parts.
 template <int SB>
 struct JoinState {
     float acc[SB][4], m, l;
@@ -652,11 +662,11 @@ __device__ __forceinline__ void join_parts(const AttnParams &P, int64_t s0, int 
         float mx = fmaxf(st.m, p.y > 0.f ? p.x : kNoMax);
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
-        const float f = p.y > 0.f ? ex2((p.x - mx) * P.scale_log2) : 0.f;
+        const float f = p.y > 0.f ? ex2(p.x - mx) : 0.f;
         float sum = f * p.y;
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
-        const float old = ex2((st.m - mx) * P.scale_log2);
+        const float old = ex2(st.m - mx);
         st.l = st.l * old + sum;
         st.m = mx;
 #pragma unroll
@@ -767,7 +777,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, RW == 1 ? 4 : 2) join_kernel(
             st = JoinState<SB>{};
 #pragma unroll
             for (int x = 0; x < kJoinWarps; ++x) {
-                const float f = ex2((sm[x] - mx) * P.scale_log2);
+                const float f = ex2(sm[x] - mx);
                 st.l += f * sl[x];
 #pragma unroll
                 for (int sb = 0; sb < SB; ++sb)
@@ -901,8 +911,7 @@ cudaError_t launch_attention(const AttentionJob &j, int sm_count, cudaStream_t s
     P.rows = plan.rows;
     P.row_tiles = plan.row_tiles;
     P.qdtype = j.qdtype;
-    P.scale_log2 = fabsf(j.scale) * 1.44269504088896340736f;
-    P.negative = j.scale < 0.f;
+    P.q_factor = j.scale * (1.44269504088896340736f * 0.03125f);
     P.group = plan.group;
     P.workers = plan.workers;
     P.least = plan.least;

@@ -26,8 +26,7 @@ struct AttnParams {
     int tree, heads, group_heads;  // query heads per key/value head
     int rows, row_tiles;           // rows of a (sequence, head), tiles of them
     int qdtype;
-    float scale_log2;  // |scale| log2(e): maxima are taken of the scores before it
-    int negative;      // the scale is negative: the queries' sign is turned
+    float q_factor;    // scale log2(e) / 32: what a rotated query is multiplied with
     // the split and its results (workspace)
     int group;       // tokens of a group: what ranges are counted in
     int workers;     // ranges at most
@@ -39,7 +38,7 @@ struct AttnParams {
     long long timeout_cycles;  // of a wait in the tcgen05 kernel
     int inject_skip;           // test hook: the first tile's first keys are never handed over
     int *span;       // [units][2] first and last worker that leaves a part of the unit
-    float *part_ml;  // [slots][tile_rows][2]: maximum, sum
+    float *part_ml;  // [slots][tile_rows][2]: reference (log2), sum
     float *part_o;   // [slots][tile_rows][head_dim]
 };
 
@@ -61,6 +60,38 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// The scale of a query row.  A row is multiplied with q_factor and a power of
+// two that brings its largest element to [2^14, 2^15), whatever its size and the
+// softmax's scale are: a rotated element is a mean of 32 and no larger, so it
+// stays finite in fp16, and small rows keep their bits.  Scores s are then in
+// units of a power of two, and under the running maximum m
+//   weight = 2^(s unit + off),  off = fl(7 - m unit)
+// is one fused operation at any size of the scores: m unit is exact, and where 7
+// falls between the numbers that fp32 has there, it becomes one of 0 .. 8.  (With
+// a factor that is no power of two the rounding of m times it alone would be many
+// powers of two from 2^28 on.)  `off` stands for the maximum: sums and parts are
+// referred to 2^-off, exactly.  `most`: the row's largest |element|; scores stay
+// finite up to |q scale| = 2^40.
+struct RowScale {
+    float factor;  // of the rotated query
+    float unit;    // of the scores, in log2
+    __device__ __forceinline__ RowScale(float q_factor, float most) {
+        const float m = most * fabsf(q_factor) * 32.0f;
+        const int e = min(max(14 + 127 - (int)(__float_as_uint(m) >> 23), -27), 90);
+        factor = q_factor * __int_as_float((127 + e) << 23);
+        unit = __int_as_float((127 - e) << 23);
+    }
+};
+
+// (finite for a row without a token so far, too: kNoMax times a unit of 2^27)
+__device__ __forceinline__ float weight_offset(float m, float unit) { return fmaf(-m, unit, kWeightExp); }
+
+// Whether a maximum mx is so far above the one that off stands for that it has
+// to be followed: where its own weight would be above 2^15.
+__device__ __forceinline__ bool outgrown(float mx, float unit, float off) {
+    return fmaf(mx, unit, off) > kWeightExp + kLazy;
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {

@@ -298,25 +298,77 @@ __device__ __forceinline__ void decode_token(const TokenRegs<D> &r, uint32_t ope
 }
 
 // ---- query rows: rotated, fp16, swizzled ---------------------------------------
-// Blocks [b0, b1) of a row, one at a time: what runs once per part costs the
-// fetch of its code more than its arithmetic.
+// Blocks [b0, b1) of a row; returns the unit of its scores.  All of the row is
+// asked for at once, because its largest element has to be known first; a row of
+// 16-bit elements waits in its place in the operand (as long as what replaces
+// it), one of fp32 is read again.  The blocks come one at a time: what runs once
+// per part costs the fetch of its code more than its arithmetic.
 template <int DT, int D>
-__device__ __forceinline__ void rotate_row(const AttnParams &P, int64_t x, bool valid, uint32_t operand, int row,
-                                           int b0, int b1) {
-    constexpr int E = ElemSize<DT>::value;
-    const char *at = P.q + x * E;
-    const float f = P.negative ? -0.03125f : 0.03125f;
+__device__ __forceinline__ float rotate_row(const AttnParams &P, int64_t x, bool valid, uint32_t operand, int row,
+                                            int b0, int b1) {
+    constexpr int E = ElemSize<DT>::value, C = D * E / 16;  // 16-byte chunks of the row
+    const uint4 *at = reinterpret_cast<const uint4 *>(P.q + x * E);
+    auto place = [&](int blk, int j) {  // of chunk j of a block
+        return swizzled(operand + (uint32_t)(blk >> 1) * TcaShape<D>::kHalf, row, (blk & 1) * 4 + j);
+    };
+    float most = 0.f;
+    {
+        uint4 raw[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (valid) raw[i] = ld(at + i);
+        }
+        uint32_t most2 = 0;  // of 16-bit elements: magnitudes are ordered as whole numbers
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (DT == kF32) most = fmaxf(most, fabsf(__uint_as_float(w[k])));
+                else most2 = __vmaxu2(most2, w[k] & 0x7FFF7FFFu);
+            }
+            if (DT != kF32 && i / 4 >= b0 && i / 4 < b1) a_sts128(place(i / 4, i % 4), w);
+        }
+        if (DT != kF32) {
+            most2 = max(most2 >> 16, most2 & 0xFFFFu);
+            most = DT == kBF16 ? __uint_as_float(most2 << 16) : __half2float(__ushort_as_half((unsigned short)most2));
+        }
+    }
+    const RowScale scale(P.q_factor, most);
 #pragma unroll 1
     for (int blk = b0; blk < b1; ++blk) {
         const uint32_t bits = c_sign_words.w[blk];
         float v[32];
+        if (DT == kF32) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            float t[4] = {0.f, 0.f, 0.f, 0.f};
-            if (valid) load4_ordinary<DT>(at + (int64_t)(32 * blk + i) * E, t);
+            for (int i = 0; i < 8; ++i) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (valid) q = ld(at + 8 * blk + i);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[i + k] = flip(t[k], (bits << (31 - i - k)) & 0x80000000u);
+                for (int k = 0; k < 4; ++k) v[4 * i + k] = __uint_as_float(w[k]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 q = a_lds128(place(blk, j));
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (DT == kBF16) {
+                        v[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
+                        v[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+                    } else {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                        v[8 * j + 2 * k] = f.x;
+                        v[8 * j + 2 * k + 1] = f.y;
+                    }
+                }
+            }
         }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = flip(v[e], (bits << (31 - e)) & 0x80000000u);
 #pragma unroll
         for (int h = 1; h < 32; h <<= 1)
 #pragma unroll
@@ -326,18 +378,19 @@ __device__ __forceinline__ void rotate_row(const AttnParams &P, int64_t x, bool 
                     v[e] = a + b;
                     v[e + h] = a - b;
                 }
-        const uint32_t half = operand + (uint32_t)(blk >> 1) * TcaShape<D>::kHalf;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const __half2 h = __floats2half2_rn(v[8 * j + 2 * k] * f, v[8 * j + 2 * k + 1] * f);
+                const __half2 h =
+                    __floats2half2_rn(v[8 * j + 2 * k] * scale.factor, v[8 * j + 2 * k + 1] * scale.factor);
                 o[k] = *reinterpret_cast<const uint32_t *>(&h);
             }
-            a_sts128(swizzled(half, row, (blk & 1) * 4 + j), o);
+            a_sts128(place(blk, j), o);
         }
     }
+    return scale.unit;
 }
 
 // ---- softmax of one row's 128 scores ---------------------------------------------
@@ -361,9 +414,9 @@ __device__ __forceinline__ void rescale_row(uint32_t t_o, float f) {
     }
 }
 
-// The maximum of 128 scores v and mx.
-__device__ __forceinline__ float max128(const uint32_t *v, float mx) {
-    float x[4] = {mx, kNoMax, kNoMax, kNoMax};
+// The maximum of 128 scores.
+__device__ __forceinline__ float max128(const uint32_t *v) {
+    float x[4] = {kNoMax, kNoMax, kNoMax, kNoMax};
 #pragma unroll
     for (int e = 0; e < 128; e += 2)
         x[(e >> 1) & 3] = fmaxf(x[(e >> 1) & 3], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
@@ -371,12 +424,12 @@ __device__ __forceinline__ float max128(const uint32_t *v, float mx) {
 }
 
 // Weights of 128 scores into 64 columns at t_p, their sum onto `sum`.
-__device__ __forceinline__ void weights128(uint32_t *v, uint64_t scale2, uint64_t off2, uint32_t t_p,
+__device__ __forceinline__ void weights128(uint32_t *v, uint64_t unit2, uint64_t off2, uint32_t t_p,
                                            uint64_t (&sum)[2]) {
 #pragma unroll
     for (int e = 0; e < 128; e += 2) {
         float a, b;
-        unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), scale2, off2), a, b);
+        unpack2(fma2(pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), unit2, off2), a, b);
         a = ex2(a);
         b = ex2(b);
         sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pack2(a, b));
@@ -386,13 +439,14 @@ __device__ __forceinline__ void weights128(uint32_t *v, uint64_t scale2, uint64_
     }
 }
 
-// The maximum follows to mx where it grew by more than kLazy for a row of the
-// warp.  `have`: the output sums hold earlier products.
+// `off` follows to a maximum mx of the scores where one of the warp's rows has
+// outgrown it.  `have`: the output sums hold earlier products.
 template <int D>
-__device__ __forceinline__ void follow(uint32_t t_o, float scale, bool have, float mx, float &m, float &l) {
-    if (__any_sync(kFull, (mx - m) * scale > kLazy)) {
-        const float f = ex2((m - mx) * scale);
-        m = mx;
+__device__ __forceinline__ void follow(uint32_t t_o, float unit, bool have, float mx, float &off, float &l) {
+    if (__any_sync(kFull, outgrown(mx, unit, off))) {
+        const float lower = fminf(off, weight_offset(mx, unit));
+        const float f = ex2(lower - off);
+        off = lower;
         l *= f;
         // the scores' commit followed this stream's last product: its sums are complete
         if (have) rescale_row<D>(t_o, f);
@@ -409,16 +463,15 @@ __device__ __forceinline__ float sum_of(const uint64_t (&sum)[2]) {
 // Scores at t_s to weights in the first half of their columns; the whole row is
 // in registers between.
 template <int D>
-__device__ __forceinline__ void softmax_row(uint32_t t_s, uint32_t t_o, float scale, bool have, float &m, float &l) {
+__device__ __forceinline__ void softmax_row(uint32_t t_s, uint32_t t_o, float unit, bool have, float &off, float &l) {
     uint32_t v[128];
 #pragma unroll
     for (int k = 0; k < 4; ++k) a_ld32(t_s + 32u * k, v + 32 * k);
     a_wait_ld();
-    follow<D>(t_o, scale, have, max128(v, m), m, l);
-    const float off = kWeightExp - m * scale;
-    const uint64_t scale2 = pack2(scale, scale), off2 = pack2(off, off);
+    follow<D>(t_o, unit, have, max128(v), off, l);
+    const uint64_t unit2 = pack2(unit, unit), off2 = pack2(off, off);
     uint64_t sum[2] = {0, 0};
-    weights128(v, scale2, off2, t_s, sum);
+    weights128(v, unit2, off2, t_s, sum);
     l += sum_of(sum);
     a_wait_st();
 }
@@ -439,9 +492,9 @@ __device__ __forceinline__ uint32_t column_word(int k, int full, uint64_t see, u
 // The same for a tile with columns that do not count (a sequence's last one or
 // two tiles), 32 columns at a time.
 template <int D>
-__device__ __forceinline__ void softmax_row_masked(uint32_t t_s, uint32_t t_o, float scale, bool have, int full,
-                                                   uint64_t see, uint32_t groups, float &m, float &l) {
-    float mx = m;
+__device__ __forceinline__ void softmax_row_masked(uint32_t t_s, uint32_t t_o, float unit, bool have, int full,
+                                                   uint64_t see, uint32_t groups, float &off, float &l) {
+    float mx = kNoMax;
 #pragma unroll 1
     for (int k = 0; k < 4; ++k) {
         uint32_t v[32];
@@ -451,8 +504,7 @@ __device__ __forceinline__ void softmax_row_masked(uint32_t t_s, uint32_t t_o, f
 #pragma unroll
         for (int e = 0; e < 32; ++e) mx = (w >> e) & 1u ? fmaxf(mx, __uint_as_float(v[e])) : mx;
     }
-    follow<D>(t_o, scale, have, mx, m, l);
-    const float off = kWeightExp - m * scale;
+    follow<D>(t_o, unit, have, mx, off, l);
 #pragma unroll 1
     for (int k = 0; k < 4; ++k) {
         uint32_t v[32];
@@ -461,8 +513,8 @@ __device__ __forceinline__ void softmax_row_masked(uint32_t t_s, uint32_t t_o, f
         a_wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-            float a = ex2(fmaf(__uint_as_float(v[e]), scale, off));
-            float b = ex2(fmaf(__uint_as_float(v[e + 1]), scale, off));
+            float a = ex2(fmaf(__uint_as_float(v[e]), unit, off));
+            float b = ex2(fmaf(__uint_as_float(v[e + 1]), unit, off));
             if (!((w >> e) & 1u)) a = 0.f;
             if (!((w >> (e + 1)) & 1u)) b = 0.f;
             l += a + b;
@@ -541,6 +593,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
         uint32_t jobs_done = 0, parts_done = 0;
         const int shift = P.c.page_shift;
         while (walk.next(P, p)) {
+            float unit;  // of this row's scores
             // the query rows: this stream's tile, or half of the common one's blocks
             {
                 const int q_row = p.row0 + (pair ? s * kRowTile : 0) + row;
@@ -551,9 +604,9 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                 const uint32_t operand = base + S::kQ + (pair ? s : 0) * S::kOperand;
                 constexpr int kBlocks = D / 32;
                 const int b0 = pair ? 0 : s * (kBlocks / 2), b1 = pair ? kBlocks : b0 + kBlocks / 2;
-                if (P.qdtype == kF32) rotate_row<kF32, D>(P, x, valid, operand, row, b0, b1);
-                else if (P.qdtype == kBF16) rotate_row<kBF16, D>(P, x, valid, operand, row, b0, b1);
-                else rotate_row<kF16, D>(P, x, valid, operand, row, b0, b1);
+                if (P.qdtype == kF32) unit = rotate_row<kF32, D>(P, x, valid, operand, row, b0, b1);
+                else if (P.qdtype == kBF16) unit = rotate_row<kBF16, D>(P, x, valid, operand, row, b0, b1);
+                else unit = rotate_row<kF16, D>(P, x, valid, operand, row, b0, b1);
                 a_proxy_fence();
             }
             a_named_sync(1, (kSoftWarps + 1) * 32);
@@ -565,7 +618,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
             const uint64_t see = words.of(min(unit_row / P.group_heads, P.tree - 1));
             const int32_t *table = P.c.page_table + p.b * P.c.table_ld;
             const int tiles = p.tb - p.ta, jobs = pair ? 2 * tiles : tiles;
-            float m = kNoMax, l = 0.f;
+            float off = weight_offset(kNoMax, unit), l = 0.f;
             int seen_jobs = 0;
             for (int i = s; i < jobs && ok; i += 2, ++seen_jobs) {
                 const int tile = p.ta + (pair ? i >> 1 : i);
@@ -583,10 +636,9 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                 if (!any_rows) {
                     // no row of this warp is asked for: whatever stands in its lanes stays there
                 } else if (tail)
-                    softmax_row_masked<D>(t_s, t_o, P.scale_log2, seen_jobs > 0, p.len - tile * kTile, see, groups, m,
-                                          l);
+                    softmax_row_masked<D>(t_s, t_o, unit, seen_jobs > 0, p.len - tile * kTile, see, groups, off, l);
                 else
-                    softmax_row<D>(t_s, t_o, P.scale_log2, seen_jobs > 0, m, l);
+                    softmax_row<D>(t_s, t_o, unit, seen_jobs > 0, off, l);
                 a_fence_before();
                 __syncwarp();
                 if (lane == 0) a_arrive(bar(kPReady + s));
@@ -603,7 +655,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                 const int64_t row0 = slot * P.tile_rows + out_row - lane;  // of this warp
                 // a token that is not there answers zero
                 if (unit_row < P.rows)
-                    reinterpret_cast<float2 *>(P.part_ml)[row0 + lane] = make_float2(m, see == 0 ? 0.f : l);
+                    reinterpret_cast<float2 *>(P.part_ml)[row0 + lane] = make_float2(-off, see == 0 ? 0.f : l);
                 // rows leave through this warp's quarter of its stream's query
                 // tile (every product has read it), 32 elements of 32 rows at a
                 // time, so that a store covers whole 128-byte lines of four rows

@@ -571,7 +571,7 @@ TQ_API tq_status tq_kv_read(const tq_kv_cache *cache, const int32_t *seqs, const
  *            its descendants are not attended to and their output is zero.
  *            NULL: a chain, token i continues i - 1
  *   q        device, batch x tree x heads x head_dim of dtype qt, 16-byte
- *            aligned, strides multiples of 8 elements; |q| below 65504
+ *            aligned, strides multiples of 8 elements; |q * scale| below 2^40
  *   out      device, same shape, dtype ot, the same rules (written; must not
  *            overlap q or the cache)
  *   heads    query heads, a multiple of kv_heads
@@ -580,8 +580,9 @@ TQ_API tq_status tq_kv_read(const tq_kv_cache *cache, const int32_t *seqs, const
  *            aligned, exclusively owned by this call until it completes on
  *            `stream`; need not be cleared, keeps nothing between calls
  * The rotated query, centroid times scale and the softmax weights enter the
- * tensor cores as fp16; sums, the running maximum and the softmax's sum are
- * fp32.  A record that no row attends to may hold anything; one that some row
+ * tensor cores as fp16, a query row times the softmax's scale and a power of two
+ * that brings it into fp16's range; sums, the running maximum and the softmax's
+ * sum are fp32.  A record that no row attends to may hold anything; one that some row
  * attends to holds finite scales (tq_kv_append writes no others).
  * tree <= TQ_KV_MAX_TREE.  Up to 16 rows (tree * heads / kv_heads) of a
  * key/value head, and every head_dim other than 64 and 128, run the mma.sync

@@ -52,3 +52,51 @@ def test_products_of_what_the_kernel_before_writes(cuda_lib, rows):
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+# ---------------------------------------------------------------------------
+# scores, values and queries of extreme size
+# ---------------------------------------------------------------------------
+def _rows(codes, scales, table, lens, q):
+    """Per row of a chain: rotated query, the records that it sees (keys, values),
+    all in the rotated domain and fp64."""
+    B, T, H, D = q.shape
+    kv, page = codes.shape[2], codes.shape[3]
+    table, codes, scales = table.cpu().long(), codes.cpu(), scales.cpu()
+    qr = _forward(q) / 32
+    for b in range(B):
+        place = torch.arange(int(lens[b]) + T)
+        at = table[b, place // page]
+        for h in range(kv):
+            k, v = (_rotated_domain(codes[at, w, h, place % page], scales[at, w, h, place % page]) for w in (0, 1))
+            for t in range(T):
+                n = int(lens[b]) + t + 1
+                for g in range(H // kv):
+                    yield (b, t, h * (H // kv) + g), qr[b, t, h * (H // kv) + g], k[:n], v[:n]
+
+
+# (rows of a key/value head: 4 and 12 on mma.sync, 64 and 160 on tcgen05)
+@pytest.mark.parametrize("T,H,kv,D", [(1, 4, 1, 128), (3, 8, 2, 64), (2, 4, 2, 256), (16, 8, 2, 128), (40, 8, 2, 64)])
+@pytest.mark.parametrize("size", [100.0, 1000.0, 60000.0 / 4])
+def test_attention_with_the_largest_scale(cuda_lib, T, H, kv, D, size):
+    """|scale| = 65536, the documented limit: scores up to 2^40 times log2(e).  The weights
+    stay finite, one token has all of the weight, and its value comes out."""
+    lens = [300, 77]
+    codes, scales, table = _filled(cuda_lib, 2, 22, kv, D, 16, seed=81)
+    q = _rand(7, 2, T, H, D, dtype=BF16, scale=size).clamp(-60000, 60000)
+    for scale in (65536.0, -65536.0):
+        got = cuda_lib.kv_attention(codes, scales, table, _i32(lens), q.to(DEV), scale=scale, dtype=F32).cpu().double()
+        assert torch.all(torch.isfinite(got))
+        clear = 0
+        for row, x, k, v in _rows(codes, scales, table, lens, q):
+            z = k @ x * scale
+            top = z.topk(2).values
+            # scores are off by 2^-11 of the products' 2-norm rms; eight times that on each side, and weights
+            # of the others below e^-60
+            if top[0] - top[1] < 16 * 2.0 ** -11 * (k * x).norm(dim=1).amax() * abs(scale) + 60:
+                continue
+            clear += 1
+            best = v[z.argmax()]
+            out = _forward(got[row][None])[0]  # H (s . out) = the rotated value
+            assert (out - best).norm() <= 3 * 2.0 ** -11 * best.norm(), row
+        assert clear > T * H  # of 2 T H rows
