@@ -582,7 +582,9 @@ TQ_API tq_status tq_kv_read(const tq_kv_cache *cache, const int32_t *seqs, const
  * The rotated query, centroid times scale and the softmax weights enter the
  * tensor cores as fp16, a query row times the softmax's scale and a power of two
  * that brings it into fp16's range; sums, the running maximum and the softmax's
- * sum are fp32.  A record that no row attends to may hold anything; one that some row
+ * sum are fp32.  Products of a centroid and a scale below 2^-14 (records of
+ * values below about 1e-5) are multiples of 2^-24, where tq_kv_read gives them
+ * exactly.  A record that no row attends to may hold anything; one that some row
  * attends to holds finite scales (tq_kv_append writes no others).
  * tree <= TQ_KV_MAX_TREE.  Up to 16 rows (tree * heads / kv_heads) of a
  * key/value head, and every head_dim other than 64 and 128, run the mma.sync

@@ -100,3 +100,41 @@ def test_attention_with_the_largest_scale(cuda_lib, T, H, kv, D, size):
             out = _forward(got[row][None])[0]  # H (s . out) = the rotated value
             assert (out - best).norm() <= 3 * 2.0 ** -11 * best.norm(), row
         assert clear > T * H  # of 2 T H rows
+
+
+@pytest.mark.parametrize("T,H,kv,D", [(1, 4, 1, 128), (3, 8, 2, 96), (2, 4, 2, 256), (16, 8, 2, 128), (40, 8, 2, 64)])
+@pytest.mark.parametrize("size,scale", [(1e-5, 65536.0), (1e-6, 65536.0), (1e-6, -3e4), (1e-9, 65536.0),
+                                        (3e4, 1e-4), (1e-7, 0.0)])
+def test_attention_with_queries_of_any_size(cuda_lib, T, H, kv, D, size, scale):
+    """Small queries keep their bits (fp16 alone has steps of 2^-24 there), large ones stay finite."""
+    lens = [200, 31]
+    codes, scales, table = _filled(cuda_lib, 2, 16, kv, D, 16, seed=83)
+    q = _rand(8, 2, T, H, D, scale=size)
+    q[:, :, 0] *= 2.0 ** -7  # rows of one tile that are far apart
+    got = cuda_lib.kv_attention(codes, scales, table, _i32(lens), q.to(DEV), scale=scale, dtype=F32)
+    ref, bar = _attention_ref(codes, scales, table, lens, q, None, scale, F32)
+    assert torch.all((got.cpu().double() - ref).norm(dim=-1) <= bar)
+
+
+@pytest.mark.parametrize("T,H,kv,D", [(1, 4, 1, 128), (2, 4, 2, 256), (16, 8, 2, 128), (40, 8, 2, 64)])
+@pytest.mark.parametrize("size,scale", [(1e-4, 1e3), (1e-5, 1e4), (1e-6, 65536.0)])
+def test_attention_over_small_records(cuda_lib, T, H, kv, D, size, scale):
+    """Keys and values so small that centroid times scale is subnormal in fp16: each
+    product is rounded to a multiple of 2^-24, off by 2^-24 / sqrt(12) rms.  Beside
+    the usual bar that is a score off by |q'| scale times it, and a row off by
+    sqrt(sum p_j^2) sqrt(D / 32) times it; again four times the rms."""
+    lens, page, per = [200, 31], 16, 16
+    codes, scales, table = cuda_lib.kv_cache(2 * per, kv, D, page) + (_i32(range(2 * per)).view(2, per),)
+    n = per * page
+    seqs, places = _i32(torch.arange(2).repeat_interleave(n)), _i32(torch.arange(n).repeat(2))
+    k, v = _rand(91, 2 * n, kv, D, scale=size), _rand(92, 2 * n, kv, D, scale=size)
+    cuda_lib.kv_append(codes, scales, table, seqs, places, k.to(DEV), v.to(DEV))
+    q = _rand(9, 2, T, H, D)
+    got = cuda_lib.kv_attention(codes, scales, table, _i32(lens), q.to(DEV), scale=scale, dtype=F32).cpu().double()
+    ref, bar = _attention_ref(codes, scales, table, lens, q, None, scale, F32)
+    step = 2.0 ** -24 / 12 ** 0.5
+    for row, x, kk, vv in _rows(codes, scales, table, lens, q):
+        p = torch.softmax(kk @ x * scale, 0)
+        spread = (p.square() * vv.square().sum(1) / 32).sum().sqrt()
+        floor = step * (x.norm() * scale * spread + p.norm() * (D / 32) ** 0.5)
+        assert (got[row] - ref[row]).norm() <= bar[row] + 4 * floor, row
