@@ -659,10 +659,10 @@ __device__ __forceinline__ void join_parts(const AttnParams &P, int64_t s0, int 
         };
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) values(j, v[j]);
-        float mx = fmaxf(st.m, p.y > 0.f ? p.x : kNoMax);
+        float mx = fmaxf(st.m, p.y != 0.f ? p.x : kNoMax);  // (a NaN sum counts: it has to reach the output)
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, x));
-        const float f = p.y > 0.f ? ex2(p.x - mx) : 0.f;
+        const float f = p.y != 0.f ? ex2(p.x - mx) : 0.f;
         float sum = f * p.y;
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(kFull, sum, x);
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, RW == 1 ? 4 : 2) join_kernel(
         parts = (last - first + 1) * P.parts;  // and how many
     }
     auto finish = [&](JoinState<SB> &st) {
-        const float inv = st.l > 0.f ? 0.03125f / st.l : 0.f;
+        const float inv = st.l != 0.f ? 0.03125f / st.l : 0.f;  // no token: zeros
         char *out = P.out + (b * P.o_batch + t * P.o_token + h * P.o_head) * ElemSize<OT>::value;
 #pragma unroll
         for (int sb = 0; sb < SB; ++sb) {

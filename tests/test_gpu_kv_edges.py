@@ -138,3 +138,36 @@ def test_attention_over_small_records(cuda_lib, T, H, kv, D, size, scale):
         spread = (p.square() * vv.square().sum(1) / 32).sum().sqrt()
         floor = step * (x.norm() * scale * spread + p.norm() * (D / 32) ** 0.5)
         assert (got[row] - ref[row]).norm() <= bar[row] + 4 * floor, row
+
+
+@pytest.mark.parametrize("T,H,kv,D", [(1, 4, 1, 128), (3, 8, 2, 96), (4, 2, 1, 256), (16, 8, 2, 128), (40, 8, 2, 64)])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_queries_that_are_not_finite_answer_nan(cuda_lib, T, H, kv, D, dtype):
+    """A NaN, an infinity or an overflow upstream does not turn into a plausible row;
+    other rows keep their bits, and a row without a token still answers zeros."""
+    B = 3
+    codes, scales, table = _filled(cuda_lib, B, 22, kv, D, 16, seed=85)
+    table[2] = -1  # nothing to attend to
+    lens = _i32([300, 1, 100])
+    q = _rand(7, B, T, H, D, dtype=dtype).to(DEV)
+    want = cuda_lib.kv_attention(codes, scales, table, lens, q)
+    assert torch.all(torch.isfinite(want)) and not want[2].any()
+    bad, hit = q.clone(), torch.zeros(B, T, H, dtype=torch.bool, device=DEV)
+    values = [float("nan"), float("inf"), -float("inf")] + ([3e38, -1e38] if dtype != F16 else [])
+    at = [(b, t, h, e) for b in range(B) for t, h, e in ((0, 1, 5), (T - 1, H - 1, D - 1), (T // 2, 0, 0))]
+    for i, (b, t, h, e) in enumerate(at):
+        bad[b, t, h, e] = values[i % len(values)]
+        hit[b, t, h] = True
+    bad[0, 0, 1] = float("inf")  # a whole row
+    for scale in (None, -1.0):
+        want = cuda_lib.kv_attention(codes, scales, table, lens, q, scale=scale)
+        got = cuda_lib.kv_attention(codes, scales, table, lens, bad, scale=scale)
+        assert torch.all(torch.isnan(got[:2][hit[:2]]))
+        assert torch.equal(got[~hit], want[~hit])
+        assert not got[2].any()
+    # a drafted token that is not there answers zeros, whatever its query holds
+    if T > 1:
+        parents = torch.arange(-1, T - 1, dtype=torch.int32).repeat(B, 1)
+        parents[:, T - 1] = -2
+        got = cuda_lib.kv_attention(codes, scales, table, lens, bad, parents=parents.to(DEV))
+        assert not got[:, T - 1].any()
