@@ -806,7 +806,9 @@ def kv_attention(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Te
     """Attention of q [batch, tree, heads, head_dim] over the cache: every row
     sees the lens[b] tokens of its sequence, its own drafted token (record at
     place lens[b] + i) and that token's ancestors by ``parents`` [batch, tree]
-    (None: a chain).  ``scale`` defaults to head_dim^-0.5, ``dtype`` to q's."""
+    (None: a chain).  ``scale`` defaults to head_dim^-0.5, ``dtype`` to q's.
+    Whether a wait expired can be asked of a workspace that was passed
+    (``workspace_status(ws)``); one that the call allocates is gone with it."""
     dev = codes.device
     where = _elsewhere(dev, stream)
     if where is not None:

@@ -35,8 +35,10 @@ struct AttnParams {
     int parts;       // partial results that a worker leaves of a unit
     int tile_rows;   // rows of a partial result
     unsigned *header;  // status word
+    unsigned *status;  // [workers] each CTA's, of which the joining launch makes the header's; null: none reports
     long long timeout_cycles;  // of a wait in the tcgen05 kernel
     int inject_skip;           // test hook: the first tile's first keys are never handed over
+    int inject_tmem;           // test hook: the last CTA takes its tensor memory for incomplete
     int *span;       // [units][2] first and last worker that leaves a part of the unit
     float *part_ml;  // [slots][tile_rows][2]: reference (log2), sum
     float *part_o;   // [slots][tile_rows][head_dim]

@@ -130,6 +130,9 @@ constexpr uint32_t kDebugStealAll = 16u;
 // bit 5: the tcgen05 attention kernel never hands over its first tile's first
 // keys, so that its bounded waits expire and report a timeout
 constexpr uint32_t kDebugSkipCacheKeys = 32u;
+// bit 6: the last CTA of that kernel takes its tensor memory for incomplete,
+// does no work and reports it
+constexpr uint32_t kDebugNoTensorMemory = 64u;
 void set_debug_flags(uint32_t flags);
 uint32_t debug_flags();
 

@@ -64,6 +64,7 @@ struct TcaShape {
     static constexpr uint32_t kV = kK + 2 * kOperand;   // two stages
     static constexpr uint32_t kBars = kV + 2 * kOperand;
     static constexpr uint32_t kTmemSlot = kBars + 8 * 16;
+    static constexpr uint32_t kStatus = kTmemSlot + 8;
     static constexpr uint32_t kScan = kTmemSlot + 16;
     static constexpr uint32_t kPrefix = kScan + 32 * 4;
     static constexpr uint32_t kEnd = kPrefix + (kAttnMaxBatch + 1) * 4;
@@ -537,7 +538,11 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
     const int warp = __shfl_sync(kFull, tid >> 5, 0);
     int *prefix = reinterpret_cast<int *>(smem + S::kPrefix);
     auto bar = [&](int i) { return base + S::kBars + 8u * (uint32_t)i; };
+    // this CTA's status, for the joining launch: a word in the header would have
+    // to be cleared before any CTA reports, and nothing orders the CTAs
+    unsigned *status = reinterpret_cast<unsigned *>(smem + S::kStatus);
     if (tid == 0) {
+        *status = 0u;
         for (int i = 0; i < 2; ++i) {
             a_mbar_init(bar(kKFull + i), kPieces / 2);
             a_mbar_init(bar(kKEmpty + i), 1);
@@ -558,13 +563,13 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
     }
     grid_dependency_wait();
     grid_dependents_launch();  // the joining launch; it waits for this one's end
-    if (blockIdx.x == 0 && tid == 0) P.header[0] = 0u;  // status of this call: set, if at all, a second from now
     a_fence_before();
     scan_sequences(P, prefix, reinterpret_cast<int *>(smem + S::kScan), tid, kTcaThreads);
     a_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + S::kTmemSlot);
-    const bool tmem_ok = tmem == 0u;  // all 512 columns: the base is lane 0, column 0 (checked, never expected)
-    if (!tmem_ok && tid == 0) atomicOr(P.header, kStatusTmem);
+    // all 512 columns: the base is lane 0, column 0 (checked, never expected)
+    const bool tmem_ok = tmem == 0u && !(P.inject_tmem && blockIdx.x == gridDim.x - 1);
+    if (!tmem_ok && tid == 0) atomicOr(status, kStatusTmem);
 
     Walk<D> walk;
     walk.prefix = prefix;
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
     bool ok = tmem_ok;
     auto give_up = [&]() {
         ok = false;
-        atomicOr(P.header, kStatusTimeout);
+        atomicOr(status, kStatusTimeout);
     };
     Part p;
 
@@ -814,6 +819,7 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
     // ---- teardown ---------------------------------------------------------------
     a_fence_before();
     __syncthreads();
+    if (tid == 0) P.status[blockIdx.x] = *status;
     if (warp == kMmaWarp) {
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");

@@ -317,7 +317,8 @@ TQ_API tq_status tq_workspace_status(void *workspace, int clear, void *stream);
  * bytes), its waits expire after ~5 ms, every tensor-memory column is still
  * released, and the status word is set.  Bit 5: the same for the tcgen05
  * attention kernel (tq_kv_attention): the first tile's first keys are never
- * handed over.
+ * handed over.  Bit 6: that kernel's last CTA takes its tensor memory for
+ * incomplete and reports it.
  */
 TQ_API void tq_debug_set_flags(uint32_t flags);
 

@@ -171,3 +171,27 @@ def test_queries_that_are_not_finite_answer_nan(cuda_lib, T, H, kv, D, dtype):
         parents[:, T - 1] = -2
         got = cuda_lib.kv_attention(codes, scales, table, lens, bad, parents=parents.to(DEV))
         assert not got[:, T - 1].any()
+
+
+# ---------------------------------------------------------------------------
+# status
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T,H,kv,D", [(16, 8, 2, 128), (40, 8, 2, 64)])
+def test_attention_reports_of_every_cta_count(cuda_lib, T, H, kv, D):
+    """What a CTA of the tcgen05 kernel reports at its start is not lost to the word being
+    cleared by another one, whichever of them comes first."""
+    B, page = 40, 16
+    codes, scales, table = _filled(cuda_lib, B, 20, kv, D, page, seed=73)
+    q, lens = _rand(1, B, T, H, D, dtype=BF16).to(DEV), _i32([(37 * b) % 250 for b in range(B)])
+    ws = cuda_lib.kv_attention_workspace(B, T, H, kv, D).fill_(255)
+    want = cuda_lib.kv_attention(codes, scales, table, lens, q, ws=ws)
+    assert cuda_lib.workspace_status(ws) == 0
+    for _ in range(20):
+        cuda_lib.tq_debug_set_flags(64)
+        try:
+            cuda_lib.kv_attention(codes, scales, table, lens, q, ws=ws)
+        finally:
+            cuda_lib.tq_debug_set_flags(0)
+        assert cuda_lib.workspace_status(ws, clear=False) == 8
+        assert torch.equal(cuda_lib.kv_attention(codes, scales, table, lens, q, ws=ws), want)
+        assert cuda_lib.workspace_status(ws, clear=False) == 0
