@@ -320,6 +320,11 @@ def _stream(stream=None) -> int:
     return int(s.cuda_stream)
 
 
+def _device(device):
+    """The device that was asked for (0 is one), else the current one."""
+    return torch.cuda.current_device() if device is None else device
+
+
 def _dt(t: torch.dtype) -> int:
     if t not in _DTYPE_CODE:
         raise TypeError(f"unsupported dtype {t}")
@@ -341,7 +346,7 @@ def workspace(m: int, n: int, k: int, device=None) -> torch.Tensor:
     nbytes = tq_gemm_workspace_bytes(m, n, k)
     if nbytes == 0:
         raise ValueError("invalid sizes for workspace query")
-    return torch.zeros(nbytes, dtype=torch.uint8, device=device or torch.cuda.current_device())
+    return torch.zeros(nbytes, dtype=torch.uint8, device=_device(device))
 
 
 def tiles(n: int) -> int:
@@ -419,7 +424,7 @@ def prefill_workspace(m: int, k: int, device=None) -> torch.Tensor:
     nbytes = tq_gemm_prefill_workspace_bytes(m, k)
     if nbytes == 0:
         raise ValueError("invalid sizes for workspace query")
-    return torch.zeros(nbytes, dtype=torch.uint8, device=device or torch.cuda.current_device())
+    return torch.zeros(nbytes, dtype=torch.uint8, device=_device(device))
 
 
 def gemm_prefill(codes, scales, n: int, k: int, X: torch.Tensor, dtype=torch.float32, out=None, ws=None,
@@ -501,7 +506,7 @@ def batch_workspace(items, m: int, device=None) -> torch.Tensor:
     nbytes = tq_gemm_batch_workspace_bytes(descs, len(items), m)
     if nbytes == 0:
         raise ValueError("invalid batch for workspace query")
-    return torch.zeros(nbytes, dtype=torch.uint8, device=device or torch.cuda.current_device())
+    return torch.zeros(nbytes, dtype=torch.uint8, device=_device(device))
 
 
 def gemm_batch(items, m: int = 1, ws=None, stream=None, descs=None):
@@ -579,7 +584,7 @@ def nvfp4_batch_workspace(items, m: int, device=None) -> torch.Tensor:
     nbytes = tq_nvfp4_gemm_batch_workspace_bytes(descs, len(items), m)
     if nbytes == 0:
         raise ValueError("invalid batch for workspace query")
-    return torch.zeros(nbytes, dtype=torch.uint8, device=device or torch.cuda.current_device())
+    return torch.zeros(nbytes, dtype=torch.uint8, device=_device(device))
 
 
 def nvfp4_gemm_batch(items, m: int = 1, ws=None, stream=None, descs=None):
@@ -641,7 +646,7 @@ def kv_cache(pages: int, kv_heads: int, head_dim: int, page_size: int = 64, laye
     if nbytes == 0 and pages != 0:
         raise ValueError("kv_cache: head_dim is a multiple of 32 up to 256, page_size a power of two from 16 to 1024")
     lead = () if layers is None else (layers,)
-    device = device or torch.cuda.current_device()
+    device = _device(device)
     codes = torch.zeros((*lead, pages, 2, kv_heads, page_size, head_dim // 2), dtype=torch.uint8, device=device)
     scales = torch.zeros((*lead, pages, 2, kv_heads, page_size, head_dim // 16), dtype=torch.int16, device=device)
     return codes, scales
@@ -707,7 +712,7 @@ def rope_frequencies(rot_dim: int, theta: float = 10000.0, factor: float = 1.0, 
         freq = freq * (keep + (1.0 - keep) / factor)
     elif scaling not in ("none", "ntk"):
         raise ValueError(f"unknown scaling {scaling!r}")
-    return freq.to(torch.float32).to(device or torch.cuda.current_device())
+    return freq.to(torch.float32).to(_device(device))
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = False,
@@ -794,10 +799,12 @@ def kv_read(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
 def kv_attention_workspace(batch: int, tree: int, heads: int, kv_heads: int, head_dim: int,
                            device=None) -> torch.Tensor:
     """A workspace tensor for ``kv_attention`` of these sizes."""
-    nbytes = tq_kv_attention_workspace_bytes(batch, tree, heads, kv_heads, head_dim)
+    device = _device(device)
+    with torch.cuda.device(device):  # the size goes by the device's number of SMs
+        nbytes = tq_kv_attention_workspace_bytes(batch, tree, heads, kv_heads, head_dim)
     if nbytes == 0:
         raise ValueError("invalid sizes for workspace query")
-    return torch.empty(nbytes, dtype=torch.uint8, device=device or torch.cuda.current_device())
+    return torch.empty(nbytes, dtype=torch.uint8, device=_device(device))
 
 
 def kv_attention(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,

@@ -5,6 +5,8 @@ import re
 import pytest
 import torch
 
+OK, INVALID, SHAPE, ALIGN, DTYPE, WORKSPACE, CUDA, UNSUP, TIMEOUT = range(9)
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "dequant_gemv_tq4_b200", "csrc")
 
 
@@ -34,3 +36,57 @@ def test_activations_are_read_by_ordinary_loads(name, begin):
     assert not re.search(r"\b(load4<|__ldg\(|ldg_keep\(|ldg64\(|p_ldg128\()", body)
     read_only = set(re.findall(r"(\w+)\([^)]*\)\s*\{[^{}]*\basm volatile\(\"ld\.global\.nc", _code(name)))
     assert not any(re.search(r"\b%s\(" % f, body) for f in read_only)
+
+
+@pytest.fixture(scope="module")
+def tq():
+    from dequant_gemv_tq4_b200 import build as b
+
+    b.build()
+    import dequant_gemv_tq4_b200 as tq
+
+    tq.load_library()
+    return tq
+
+
+class _TwoDevices:
+    """Device 1 current, a workspace that is larger on device 0: stands for
+    torch.cuda and the size queries where there is no GPU."""
+
+    def __init__(self, monkeypatch, tq):
+        self.current, self.asked = 1, []
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: self.current)
+        monkeypatch.setattr(torch.cuda, "device", self.device)
+        for name in ("zeros", "empty"):
+            monkeypatch.setattr(torch, name, self.allocate)
+        monkeypatch.setattr(torch.Tensor, "to", lambda t, to, *a: t if isinstance(to, torch.dtype) else self.allocate(t.shape, device=to))
+        for name in ("tq_kv_attention_workspace_bytes", "tq_gemm_workspace_bytes", "tq_gemm_prefill_workspace_bytes"):
+            monkeypatch.setattr(tq, name, lambda *a: 256 if self.current else 512)
+
+    def device(self, index):
+        state = self
+
+        class Guard:
+            def __enter__(self):
+                self.before, state.current = state.current, index
+
+            def __exit__(self, *a):
+                state.current = self.before
+        return Guard()
+
+    def allocate(self, shape, dtype=None, device=None):
+        self.asked.append((shape, device))
+        return self
+
+
+@pytest.mark.parametrize("device,want", [(0, 0), (None, 1), (1, 1)])
+def test_device_zero_is_a_device(monkeypatch, tq, device, want):
+    """With device 1 current, device=0 is device 0, and a workspace's size is that device's."""
+    two = _TwoDevices(monkeypatch, tq)
+    tq.kv_cache(2, 1, 64, device=device)
+    tq.rope_frequencies(64, device=device)
+    tq.workspace(4, 64, 64, device=device)
+    tq.prefill_workspace(64, 64, device=device)
+    assert [d for _, d in two.asked] == [want] * 5
+    tq.kv_attention_workspace(2, 1, 4, 2, 64, device=device)
+    assert two.asked[-1] == (256 if want else 512, want)
