@@ -769,9 +769,13 @@ def kv_append(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tenso
 
 
 def kv_read(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor, seqs: torch.Tensor,
-            places: torch.Tensor, dtype=torch.bfloat16, k: torch.Tensor | None = None,
+            places: torch.Tensor, dtype=None, k: torch.Tensor | None = None,
             v: torch.Tensor | None = None, stream=None):
-    """(keys, values) [n, kv_heads, head_dim] of the tokens at places[i] of seqs[i]."""
+    """(keys, values) [n, kv_heads, head_dim] of the tokens at places[i] of seqs[i],
+    of ``dtype`` (that of k or v if one is given, else bfloat16)."""
+    for name, t in (("k", k), ("v", v)):
+        if t is not None and dtype is not None and t.dtype is not dtype:
+            _bad(name, t, f"{dtype}")
     dev = codes.device
     where = _elsewhere(dev, stream)
     if where is not None:
@@ -781,7 +785,7 @@ def kv_read(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tensor,
     n = seqs.numel()
     shape = (n, cache.kv_heads, cache.head_dim)
     if k is None and v is None:
-        k, v = scales.new_empty((2, *shape), dtype=dtype).unbind(0)
+        k, v = scales.new_empty((2, *shape), dtype=dtype or torch.bfloat16).unbind(0)
     elif k is None:
         k = torch.empty(shape, dtype=v.dtype, device=dev)
     elif v is None:
@@ -813,9 +817,12 @@ def kv_attention(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Te
     """Attention of q [batch, tree, heads, head_dim] over the cache: every row
     sees the lens[b] tokens of its sequence, its own drafted token (record at
     place lens[b] + i) and that token's ancestors by ``parents`` [batch, tree]
-    (None: a chain).  ``scale`` defaults to head_dim^-0.5, ``dtype`` to q's.
+    (None: a chain).  ``scale`` defaults to head_dim^-0.5, ``dtype`` to out's if
+    that is given, else to q's.
     Whether a wait expired can be asked of a workspace that was passed
     (``workspace_status(ws)``); one that the call allocates is gone with it."""
+    if out is not None and dtype is not None and out.dtype is not dtype:
+        _bad("out", out, f"{dtype}")
     dev = codes.device
     where = _elsewhere(dev, stream)
     if where is not None:

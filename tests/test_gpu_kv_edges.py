@@ -195,3 +195,20 @@ def test_attention_reports_of_every_cta_count(cuda_lib, T, H, kv, D):
         assert cuda_lib.workspace_status(ws, clear=False) == 8
         assert torch.equal(cuda_lib.kv_attention(codes, scales, table, lens, q, ws=ws), want)
         assert cuda_lib.workspace_status(ws, clear=False) == 0
+
+
+# ---------------------------------------------------------------------------
+# types
+# ---------------------------------------------------------------------------
+def test_read_and_attention_take_the_outputs_type(cuda_lib):
+    codes, scales, table = _filled(cuda_lib, 1, 2, 2, 64, 16, seed=3)
+    zero, at = _i32([0, 0]), _i32([3, 17])
+    want, _ = cuda_lib.kv_read(codes, scales, table, zero, at, dtype=F32)
+    k, v = cuda_lib.kv_read(codes, scales, table, zero, at)
+    assert k.dtype == v.dtype == BF16 and torch.equal(k, want.to(BF16))
+    given = torch.empty(2, 2, 64, dtype=F16, device=DEV)
+    k, v = cuda_lib.kv_read(codes, scales, table, zero, at, k=given)
+    assert k is given and v.dtype == F16 and torch.equal(k, want.half())
+    q, out = _rand(1, 1, 1, 4, 64, dtype=BF16).to(DEV), torch.empty(1, 1, 4, 64, device=DEV)
+    assert cuda_lib.kv_attention(codes, scales, table, _i32([20]), q, out=out) is out
+    assert torch.equal(out, cuda_lib.kv_attention(codes, scales, table, _i32([20]), q, dtype=F32))

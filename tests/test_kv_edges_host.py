@@ -90,3 +90,24 @@ def test_device_zero_is_a_device(monkeypatch, tq, device, want):
     assert [d for _, d in two.asked] == [want] * 5
     tq.kv_attention_workspace(2, 1, 4, 2, 64, device=device)
     assert two.asked[-1] == (256 if want else 512, want)
+
+
+def test_a_type_asked_for_is_not_dropped(tq):
+    """dtype beside an output of another type is refused (before a device is looked at)."""
+    codes = torch.zeros(4, 2, 2, 16, 32, dtype=torch.uint8)
+    scales = torch.zeros(4, 2, 2, 16, 4, dtype=torch.int16)
+    table, one = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    q, out = torch.zeros(1, 1, 2, 64), torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16)
+    kv = torch.zeros(1, 2, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="^out: expected torch.float32"):
+        tq.kv_attention(codes, scales, table, one, q, dtype=torch.float32, out=out)
+    for name in "kv":
+        with pytest.raises(ValueError, match="^%s: expected torch.bfloat16" % name):
+            tq.kv_read(codes, scales, table, one, one, dtype=torch.bfloat16, **{name: kv})
+    # the output's own type, or none: as far as a call without a GPU goes
+    for dtype in (None, torch.bfloat16):
+        with pytest.raises(ValueError, match="CUDA"):
+            tq.kv_attention(codes, scales, table, one, q, dtype=dtype, out=out)
+    for dtype in (None, torch.float16):
+        with pytest.raises(ValueError, match="CUDA"):
+            tq.kv_read(codes, scales, table, one, one, dtype=dtype, k=kv)
