@@ -212,3 +212,86 @@ def test_read_and_attention_take_the_outputs_type(cuda_lib):
     q, out = _rand(1, 1, 1, 4, 64, dtype=BF16).to(DEV), torch.empty(1, 1, 4, 64, device=DEV)
     assert cuda_lib.kv_attention(codes, scales, table, _i32([20]), q, out=out) is out
     assert torch.equal(out, cuda_lib.kv_attention(codes, scales, table, _i32([20]), q, dtype=F32))
+
+
+# ---------------------------------------------------------------------------
+# the largest sizes, and calls captured together
+# ---------------------------------------------------------------------------
+def _chain_ref(codes, scales, table, lens, q, scale, out_dtype):
+    """_attention_ref of a chain, all rows of a (sequence, head) at once, on the GPU."""
+    B, T, H, D = q.shape
+    kv, page = codes.shape[2], codes.shape[3]
+    G = H // kv
+    q = q.cpu()
+    qr = (_forward(q) / 32).to(DEV)
+    ref, bar = torch.zeros(B, T, H, D, device=DEV, dtype=torch.float64), torch.zeros(B, T, H, device=DEV, dtype=torch.float64)
+    table_h, codes_h, scales_h = table.cpu().long(), codes.cpu(), scales.cpu()
+    for b in range(B):
+        n = int(lens[b]) + T
+        place = torch.arange(n)
+        at = table_h[b, place // page]
+        hidden = torch.arange(n)[None] > int(lens[b]) + torch.arange(T)[:, None]
+        hidden = hidden.repeat_interleave(G, 0).to(DEV)
+        for h in range(kv):
+            k, v = (_rotated_domain(codes_h[at, w, h, place % page], scales_h[at, w, h, place % page]).to(DEV)
+                    for w in (0, 1))
+            x = qr[b, :, h * G:(h + 1) * G].reshape(T * G, D)
+            p = torch.softmax((x @ k.T * scale).masked_fill(hidden, -torch.inf), 1)
+            s = (x.square() @ k.square().T).masked_fill(hidden, 0).amax(1).sqrt() * abs(scale)
+            o = _forward((p @ v).cpu()).to(DEV) / 32  # H (s . y); H y with the signs behind has the same norm
+            spread = (p.square() @ (v.square().sum(1) / 32)).sqrt()
+            ref[b, :, h * G:(h + 1) * G] = (p @ v).view(T, G, D)
+            bar[b, :, h * G:(h + 1) * G] = (4 * 2.0 ** -11 * (1 + s) * spread
+                                            + torch.finfo(out_dtype).eps / 2 * o.norm(dim=1)).view(T, G)
+    return ref, bar
+
+
+@pytest.mark.parametrize("B,T,H,kv,D,lens", [
+    (1, 2, 1024, 1, 64, [70]),      # 2048 rows of one head, tcgen05
+    (1, 2, 1024, 1, 32, [70]),      # the same on mma.sync
+    (1, 64, 1024, 1, 64, [40]),     # 65536 rows
+    (1, 1, 1024, 1024, 32, [33]),   # as many key/value heads
+    (4096, 1, 1, 1, 32, None),      # as many sequences, mma.sync
+    (4096, 17, 1, 1, 64, None),     # and tcgen05
+])
+def test_attention_at_the_largest_sizes(cuda_lib, B, T, H, kv, D, lens):
+    lens = [(7 * b) % 30 for b in range(B)] if lens is None else lens
+    codes, scales, table = _filled(cuda_lib, B, -(-(max(lens) + T) // 16), kv, D, 16, seed=D)
+    q = _rand(H, B, T, H, D, dtype=F16)
+    got = cuda_lib.kv_attention(codes, scales, table, _i32(lens), q.to(DEV), scale=0.25, dtype=F32)
+    some = list(range(B)) if B < 100 else [0, 1, 2, 29, 500, 1023, 1024, 2047, 4094, 4095]
+    ref, bar = _chain_ref(codes, scales, table[some], [lens[b] for b in some], q[some], 0.25, F32)
+    turned = _forward(got[some].cpu()).to(DEV)  # H (s . out): the rotated domain, whose norm is sqrt(32) times larger
+    assert torch.all((turned - ref).norm(dim=-1) / 32 ** 0.5 <= bar)
+
+
+def test_graphs_of_both_kernels_share_a_workspace(cuda_lib):
+    """Captured calls of one token and of a tree, one workspace, replayed in turn, over lengths
+    and pages that change between replays."""
+    tq = cuda_lib
+    B, H, kv, D, page = 3, 8, 2, 128, 16
+    codes, scales, table = _filled(tq, B, 40, kv, D, page, seed=57)
+    lens = _i32([100, 5, 600])
+    qs = [_rand(i, B, T, H, D, dtype=BF16).to(DEV) for i, T in enumerate((1, 30, 5, 64))]
+    nbytes = max(tq.kv_attention_workspace(B, q.shape[1], H, kv, D).numel() for q in qs)
+    ws = torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV)
+    outs, graphs, side = [torch.empty_like(q) for q in qs], [], torch.cuda.Stream()
+    for q, out in zip(qs, outs):  # (kernels are loaded before the capture)
+        tq.kv_attention(codes, scales, table, lens, q, out=out, ws=ws)
+    torch.cuda.synchronize()
+    for q, out in zip(qs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            tq.kv_attention(codes, scales, table, lens, q, out=out, ws=ws)
+        graphs.append(g)
+    order = torch.arange(B * 40, dtype=torch.int32).view(B, 40)
+    for step, new in enumerate(([100, 5, 570], [0, 576, 17], [576, 1, 300])):
+        lens.copy_(_i32(new))
+        table.copy_(order.roll(step, 0))
+        for _ in range(3):
+            for g in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        assert tq.workspace_status(ws) == 0
+        for q, out in zip(qs, outs):
+            assert torch.equal(out, tq.kv_attention(codes, scales, table, lens, q))
