@@ -896,6 +896,7 @@ __global__ void __launch_bounds__(warps_for(CM > 0, NT) * 32, 1) gemv_group_kern
     const int gw = blockIdx.x * G::kWarps + warp;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     if (base > G::kMaxSmemBase) {  // layout precondition (checked, never expected)
+        grid_dependency_wait();  // the launch before clears the status
         if (threadIdx.x == 0) atomicOr(P.header + kHeaderStatus, kStatusLayout);
         return;
     }

@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     if (base > kPMaxBase) {  // layout precondition (checked, never expected)
+        grid_dependency_wait();  // the launch before clears the status
         if (threadIdx.x == 0) atomicOr(P.header, kPStatusLayout);
         return;
     }
@@ -331,10 +332,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const uint32_t tmem = p_lds_u32(tmem_slot);
     // both accumulators need the whole of tensor memory: checked, never expected
     const bool tmem_ok = tmem == 0u;
-    if (!tmem_ok && threadIdx.x == 0) atomicOr(P.header, kPStatusTmem);
-    // the activation tiles are the pre-rotation's output
+    // the activation tiles are the pre-rotation's output, and it clears the status
     grid_dependency_wait();
     grid_dependents_launch();
+    if (!tmem_ok && threadIdx.x == 0) atomicOr(P.header, kPStatusTmem);
 
     if (warp == 0) {
         // ---- activation tiles by TMA ----------------------------------------

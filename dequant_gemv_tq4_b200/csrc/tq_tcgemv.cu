@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_gemv_kernel(const __grid_con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     if (base > kTcMaxBase) {  // layout precondition (checked, never expected)
+        grid_dependency_wait();  // the launch before clears the status
         if (threadIdx.x == 0) atomicOr(P.header + kHeaderStatus, kTcStatusLayout);
         return;
     }
@@ -418,7 +419,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_gemv_kernel(const __grid_con
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + (tmem_slot - base));
     const bool tmem_ok = tmem == 0u;  // all 512 columns: base at lane 0, column 0 (checked, never expected)
-    if (!tmem_ok && threadIdx.x == 0) atomicOr(P.header + kHeaderStatus, kTcStatusTmem);
     grid_dependents_launch();
 
     if (warp == 0) {
@@ -627,7 +627,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_gemv_kernel(const __grid_con
         __syncwarp();
     } else {
         // ---- epilogue: thread = weight row; the groups' accumulators -> Y -----------
-        grid_dependency_wait();  // the header (call tag) is prepared by the preceding launch
+        grid_dependency_wait();  // the header (status, call tag) is prepared by the preceding launch
+        if (!tmem_ok && threadIdx.x == kTcEpiWarp0 * 32) atomicOr(P.header + kHeaderStatus, kTcStatusTmem);
         const uint32_t tag = *reinterpret_cast<volatile const unsigned *>(P.header + kHeaderTag);
         const int row = 32 * (warp & 3) + lane;
         const int et = threadIdx.x - kTcEpiWarp0 * 32;  // 0..127

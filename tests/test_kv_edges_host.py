@@ -111,3 +111,13 @@ def test_a_type_asked_for_is_not_dropped(tq):
     for dtype in (None, torch.float16):
         with pytest.raises(ValueError, match="CUDA"):
             tq.kv_read(codes, scales, table, one, one, dtype=dtype, k=kv)
+
+
+@pytest.mark.parametrize("name,kernel", [("tq_gemv.cu", "gemv_group_kernel("), ("tq_tcgemv.cu", "tc_gemv_kernel("),
+                                         ("tq_prefill.cu", "prefill_kernel(")])
+def test_a_product_reports_behind_the_launch_that_clears_its_status(name, kernel):
+    """A product starts while the launch before it, which clears the status word, still runs:
+    nothing is reported ahead of the wait for it."""
+    body = _code(name).split(kernel, 1)[1]
+    assert "atomicOr(P.header" in body
+    assert body.index("grid_dependency_wait()") < body.index("atomicOr(P.header")
