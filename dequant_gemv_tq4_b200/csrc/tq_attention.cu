@@ -32,12 +32,13 @@
 // What bounds it: instruction issue and shared-memory lookups, not HBM.  Per
 // pair of elements of a group the lookup, its address and the scale are three
 // instructions whatever the rows, so up to 8 rows cost the same.  64 sequences,
-// 289,000 tokens together, 32 query over 8 key/value heads of 128: 96.5 us with
-// the joining launch, 3.8 TB/s of records (issue slots 62% used, the
-// shared-memory pipe 57%; 113 us before bases were computed once per warp).
-// One sequence of 1000 tokens 11.5 us, of 30000 25 us: two launches and a
-// warp's chain of waits (page id, records, query), hence ranges down to one
-// group, so that many warps share few tokens.
+// 289,000 tokens together, 32 query over 8 key/value heads of 128: 97.5 us with
+// the joining launch, 3.8 TB/s of records (issue slots 60% used, the
+// shared-memory pipe 56%); 96.2 before rows had a power of two of their own,
+// which takes two registers.  One sequence of 1000 tokens 11.6 us, of 4000 16.5,
+// of 30000 28: two launches, a warp's chain of waits (page id, records, query),
+// hence ranges down to one group, so that many warps share few tokens; and a
+// part of every warp (up to 297 a row) that the joining launch has to read.
 #include "tq_attention.cuh"
 
 namespace tq {
@@ -48,17 +49,19 @@ constexpr int kGroup = 16;               // tokens of a group
 constexpr uint32_t kLutBase = 0x10000u;  // shared-memory address of the centroid table
 constexpr uint32_t kLutStep = 256;       // bytes between its rows (128 used)
 // Groups of a warp's range at least: a single token over 1000 cached ones takes
-// 13.8 us with 1 and 17 with 4 (before the joining launch was made cheaper).
+// 11.6 us with 1 and 12.1 with 4.  (Over 4000 16.5 and 12.5: there fewer parts
+// weigh more.)
 constexpr int kLeastGroups = 1;
 // What beginning a unit costs (its query rotated, its part written), in groups:
-// 0, 2 and 4 take 107, 105.6 and 105.3 us for 64 sequences of up to 8000 tokens;
-// in tiles of the tcgen05 kernel, 0, 2, 3, 4 and 5 take 66, 58, 56, 56 and 57 us
-// for 16 trees of 16 tokens and 167, 166, 163, 162 and 161 us for 4 trees of 64.
+// 0, 2, 4 and 8 take 98.8, 97.3, 96.9 and 97.6 us for 64 sequences of up to 8000
+// tokens; in tiles of the tcgen05 kernel, 0, 2, 3, 4 and 5 take 63.8, 55.2, 52.8,
+// 51.5 and 51.4 us for 16 trees of 16 tokens and 162.7, 160.6, 158.6, 158.1 and
+// 156.2 us for 4 trees of 64.
 constexpr int kExtraGroups = 4;
 constexpr int kTcExtra = 4;
 // Rows of a key/value head above which the tcgen05 kernel runs.  mma.sync
 // against tcgen05, head dimension 128: 16 sequences of 4000 tokens with 16 rows
-// 55 and 70 us, with 24 rows 83 and 76; 4 of 30000 tokens 67 and 104, 120 and 106.
+// 46 and 64 us, with 24 rows 69 and 65; 4 of 30000 tokens 68 and 98, 115 and 99.
 constexpr int kTcLeastRows = 16;
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
@@ -265,8 +268,8 @@ struct AttnState {
     float off[NT][2], unit[NT][2], l[NT][2];  // RowScale
 };
 
-// Groups of a warp's step: 1 and 2 took 112 and 103.5 us for 64 sequences of up
-// to 8000 tokens (12.3 and 13.8 us for one of 1000).
+// Groups of a warp's step: 1 and 2 take 102.8 and 96.9 us for 64 sequences of up
+// to 8000 tokens (10.0 and 11.6 us for one of 1000).
 constexpr int kStepGroups = 2;
 
 // Scores of a group against the rotated queries: s[n] = K q^T.
@@ -619,8 +622,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attend_kernel(const AttnParams 
 // The parts of each row joined, rotated back, divided and rounded.  CTAs of
 // eight warps; a warp takes a row (RW = 1), or all eight share one (RW = 8), as
 // they do in any launch where a row has more than kAlone parts (a long sequence
-// among short ones: 100000 tokens and 64 times 100, 54 us, with a warp for each
-// row 99); a CTA's rows lie far apart, so that such rows seldom meet in one.
+// among short ones: 100000 tokens and 64 times 100, 55 us, with a warp for each
+// row 100); a CTA's rows lie far apart, so that such rows seldom meet in one.
 // SB: halves of 128 elements.  What bounds this launch is its chain of dependent loads (span, then
 // maxima, sums and the first values), so the attention kernel leaves each unit's
 // span of slots ready to be read, and values are loaded before their weights are
@@ -698,7 +701,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, RW == 1 ? 4 : 2) join_kernel(
     constexpr int kRows = kJoinWarps / RW;  // of a CTA
     // parts whose values are on their way: many in a launch of few rows; of many
     // rows, as many as leave the registers for other warps (4 instead of 2: 182
-    // against 173 us for 131072 rows; 4 instead of 8: 17.7 against 16.2 us for 32)
+    // against 173 us for 131072 rows; 4 instead of 8: 17.6 against 16.5 us for 32)
     constexpr int kAhead = RW == 1 ? 2 : 8;
     __shared__ float so[kJoinWarps][128 * SB];
     __shared__ float sl[kJoinWarps], sm[kJoinWarps];
@@ -820,10 +823,10 @@ AttnPlan plan_attention(int64_t batch, int tree, int heads, int kv_heads, int he
     } else {
         // tiles of 8 rows, or 16 where a (sequence, head) has more than 8 rows
         // and the accumulators of 16 fit the registers (head dimension up to
-        // 128): 16 rows over 64 sequences of 4000 tokens as one tile 126 us, as
-        // two 166.  16 warps where 128 registers hold a tile: 8 rows over the
-        // same 89 us, with 8 warps 105 (one sequence of 30000 tokens, whose
-        // parts have to be joined, 25 and 21)
+        // 128): 16 rows over 64 sequences of 4000 tokens as one tile 127 us, as
+        // two 169.  16 warps where 128 registers hold a tile: 8 rows over the
+        // same 92 us, with 8 warps 106 (one sequence of 30000 tokens, whose
+        // parts have to be joined, 28 and 24)
         p.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
         p.nt = p.rows > 8 && p.dp <= 128 ? 2 : 1;
         p.warps = p.nt == 2 || p.dp == 256 ? 8 : 16;
@@ -870,8 +873,8 @@ cudaError_t launch_join_as(const AttnParams &P, cudaStream_t stream) {
 
 // Eight warps share a row where rows are few and their parts (about workers /
 // units + 1) many; else a warp takes a row.  Whole call, eight warps against
-// one: 32 rows of up to 297 parts 16 and 82 us; 256 rows of 38 parts 30 and 40;
-// 1024 rows of 10 parts 23 and 19; 2048 rows of 19 parts 33 and 28.
+// one: 32 rows of up to 297 parts 16.5 and 75 us; 256 rows of 38 parts 33 and 48;
+// 1024 rows of 10 parts 23.5 and 18.5; 2048 rows of 10 parts 46.5 and 35.
 constexpr int64_t kManyParts = 16;
 constexpr int64_t kFewRows = 148 * 8;
 

@@ -19,16 +19,20 @@
 // While one stream's softmax runs, the tensor cores work for the other.
 //
 // What bounds it: the chain scores - softmax - weights - product of the two
-// streams, with the exponentials (one per row and token, 42% of their unit's
-// peak), the decoding (ALU pipe 41%) and the tensor pipe (42%) all less than
+// streams, with the exponentials (one per row and token, 40% of their unit's
+// peak), the decoding (ALU pipe 38%) and the tensor pipe (40%) all less than
 // half used.  4 sequences of 16384 tokens, 64 drafted tokens, 64 query over 8
-// key/value heads of 128: 156 us with the joining launch, 880 TFLOP/s (the
-// mma.sync kernel 917 us).  16 sequences of up to 4000 tokens with 64 rows a
-// head 50 us: half of each 128-row product is padding there.
-// Tiles of 128 tokens: 64-token tiles with two score buffers a stream took 201
-// us against 171; weights handed over in halves 188; a second issuing warp 207.
-// Seven decode warps, the eighth warp of their register share issues; eight in
-// a CTA of 20 warps took 178 us, where seven took 171.
+// key/value heads of 128: 157.5 us with the joining launch, 875 TFLOP/s, at the
+// full clock of a burst (1965 MHz); 174 us once a second of such calls has brought
+// the GPU to its power limit (992 W, 1770 MHz).  16 sequences of up to 4000 tokens
+// with 64 rows a head 51.5 us: a CTA's share is about sixteen tiles in one or two
+// parts, and a part's beginning and end (last product, results out, next query
+// rotated, first score), which nothing overlaps, counts as four tiles; half of
+// each 128-row product is padding there.
+// Forms measured when this one took 171 us for the large case: 64-token tiles
+// with two score buffers a stream 201; weights handed over in halves 188; a
+// second issuing warp 207.  Seven decode warps, the eighth warp of their register
+// share issues; eight in a CTA of 20 warps took 178.
 #include "tq_attention.cuh"
 
 namespace tq {
@@ -727,7 +731,8 @@ __global__ void __launch_bounds__(kTcaThreads, 1) tc_attend_kernel(const AttnPar
                 if (begun) {
                     const uint32_t t = piece / kPieces, st = t & 1u;
                     const bool values = piece & 4u;
-                    if (!a_mbar_wait_warp(bar((values ? kVEmpty : kKEmpty) + (int)st), ((t >> 1) & 1u) ^ 1u, P.timeout_cycles)) {
+                    if (!a_mbar_wait_warp(bar((values ? kVEmpty : kKEmpty) + (int)st), ((t >> 1) & 1u) ^ 1u,
+                                          P.timeout_cycles)) {
                         give_up();
                         break;
                     }
