@@ -75,15 +75,17 @@ __device__ __forceinline__ float ex2(float x) {
 // a factor that is no power of two the rounding of m times it alone would be many
 // powers of two from 2^28 on.)  `off` stands for the maximum: sums and parts are
 // referred to 2^-off, exactly.  `most`: the row's largest |element|; scores stay
-// finite up to |q scale| = 2^40, and a row beyond that, or with an infinity or a
-// NaN, is all NaN, and so are its scores, sum and output.
+// finite up to |q scale| = 2^40 and |q| = 2^122 (sums of 32), and a row beyond
+// that, or with an infinity or a NaN, is all NaN, and so are its scores, sum and
+// output.
 struct RowScale {
     float factor;  // of the rotated query
     float unit;    // of the scores, in log2
     __device__ __forceinline__ RowScale(float q_factor, float most) {
         const float m = most * fabsf(q_factor) * 32.0f;
         const int e = min(max(14 + 127 - (int)(__float_as_uint(m) >> 23), -27), 90);
-        factor = m < 0x1p42f ? q_factor * __int_as_float((127 + e) << 23) : __int_as_float(0x7FFFFFFF);
+        const bool fits = m < 0x1p42f && most < 0x1p122f;
+        factor = fits ? q_factor * __int_as_float((127 + e) << 23) : __int_as_float(0x7FFFFFFF);
         unit = __int_as_float((127 - e) << 23);
     }
 };

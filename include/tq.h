@@ -573,8 +573,9 @@ TQ_API tq_status tq_kv_read(const tq_kv_cache *cache, const int32_t *seqs, const
  *            NULL: a chain, token i continues i - 1
  *   q        device, batch x tree x heads x head_dim of dtype qt, 16-byte
  *            aligned, strides multiples of 8 elements; a row with an
- *            infinity, a NaN or |q * scale| of 2^40 and more answers NaN
- *            (zeros, like any other, where it has no token to attend to)
+ *            infinity, a NaN, or |q * scale| of 2^40 or |q| of 2^122 and more
+ *            answers NaN (zeros, like any other, where it has no token to
+ *            attend to)
  *   out      device, same shape, dtype ot, the same rules (written; must not
  *            overlap q or the cache)
  *   heads    query heads, a multiple of kv_heads

@@ -173,6 +173,25 @@ def test_queries_that_are_not_finite_answer_nan(cuda_lib, T, H, kv, D, dtype):
         assert not got[:, T - 1].any()
 
 
+@pytest.mark.parametrize("T,H,kv,D", [(1, 4, 1, 128), (16, 8, 2, 128), (40, 8, 2, 64)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_queries_near_the_types_limit(cuda_lib, T, H, kv, D, dtype):
+    """With a scale as small as the queries are large: right up to 2^121, NaN where the sum
+    of a block's 32 elements may overflow (all scores minus infinity are no empty row)."""
+    codes, scales, table = _filled(cuda_lib, 1, 22, kv, D, 16, seed=87)
+    lens = [0]
+    q = _rand(7, 1, T, H, D, dtype=F32).clamp(-2, 2).to(dtype)
+    ref, bar = _attention_ref(codes, scales, table, lens, q, None, 0.5, F32)
+    got = cuda_lib.kv_attention(codes, scales, table, _i32(lens), (q.float() * 2.0 ** 120).to(dtype).to(DEV),
+                                scale=2.0 ** -121, dtype=F32)
+    assert torch.all((got.cpu().double() - ref).norm(dim=-1) <= bar)
+    signs = torch.where(_rand(8, 1, T, H, D) < 0, -1.0, 1.0)
+    for value in (2.0 ** 122, 3e38):
+        for sign in (1.0, -1.0, signs):
+            far = (torch.full((1, T, H, D), value) * sign).to(dtype).to(DEV)
+            assert torch.all(torch.isnan(cuda_lib.kv_attention(codes, scales, table, _i32(lens), far, scale=2.0 ** -121)))
+
+
 # ---------------------------------------------------------------------------
 # status
 # ---------------------------------------------------------------------------
